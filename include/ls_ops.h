@@ -74,7 +74,9 @@ typedef enum {
     LS_ERR_CUDA = 5                /* a CUDA call or kernel launch failed; see ls_last_error() */
 } ls_status;
 
-typedef enum { LS_F32 = 0, LS_F16 = 1 } ls_dtype;
+/* LS_BF16 is a storage type of the vocabulary operators (ls_vocab.h) only; every entry point of this
+ * header rejects it. */
+typedef enum { LS_F32 = 0, LS_F16 = 1, LS_BF16 = 2 } ls_dtype;
 
 /* Static description of a status code. */
 const char* ls_status_string(ls_status status);

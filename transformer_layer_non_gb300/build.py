@@ -1,8 +1,10 @@
-"""Build ``libls_ops.so`` (the C-ABI operator library) for sm_103a with nvcc.
+"""Build the C-ABI operator libraries for sm_103a with nvcc: ``libls_ops.so``
+(the layer operators, ``csrc/``) and ``libls_vocab.so`` (the vocabulary
+operators, ``csrc_vocab/``).
 
-The translation units compile in parallel and link into
-``transformer_layer_non_gb300/_build/libls_ops.so``.  A rebuild happens only
-when a source or header is newer than the library.  Usage::
+A library's translation units compile in parallel and link into
+``transformer_layer_non_gb300/_build/``.  A rebuild happens only when a source
+or header is newer than the library.  Usage::
 
     python -m transformer_layer_non_gb300.build [--force] [--verbose]
 """
@@ -22,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libls_ops.so")
+VOCAB_CSRC = os.path.join(PKG, "csrc_vocab")
+VOCAB_LIB = os.path.join(BUILD, "libls_vocab.so")
 # The benchmark's reference streaming kernel (not part of the operator library).
 FLOOR_SRC = os.path.join(PKG, "floor", "stream_floor.cu")
 FLOOR_LIB = os.path.join(BUILD, "libls_floor.so")
@@ -42,28 +46,42 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+def vocab_sources():
+    return sorted(glob.glob(os.path.join(VOCAB_CSRC, "*.cu")))
+
+
+def _headers():
+    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
         os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _vocab_headers():
+    return _headers() + glob.glob(os.path.join(VOCAB_CSRC, "*.cuh")) + glob.glob(
+        os.path.join(VOCAB_CSRC, "*.h"))
+
+
+def _newer_than(lib: str, inputs) -> bool:
+    if not os.path.exists(lib):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(p) <= t for p in inputs)
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link the library; returns its path."""
-    if not force and up_to_date():
-        return LIB
+def up_to_date() -> bool:
+    return _newer_than(LIB, sources() + _headers())
+
+
+def vocab_up_to_date() -> bool:
+    return _newer_than(VOCAB_LIB, vocab_sources() + _vocab_headers())
+
+
+def _compile_and_link(lib: str, srcs, obj_dir: str, verbose: bool, ptxas_verbose: bool) -> str:
     nvcc = _nvcc()
-    os.makedirs(BUILD, exist_ok=True)
+    os.makedirs(obj_dir, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
     def compile_one(src):
-        obj = os.path.join(BUILD, os.path.basename(src).replace(".cu", ".o"))
+        obj = os.path.join(obj_dir, os.path.basename(src).replace(".cu", ".o"))
         cmd = [nvcc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -71,18 +89,33 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        results = list(ex.map(compile_one, sources()))
+        results = list(ex.map(compile_one, srcs))
     if verbose or ptxas_verbose:
         for obj, log in results:
             if log.strip():
                 print(f"== {os.path.basename(obj)}\n{log}", file=sys.stderr)
-    tmp = LIB + f".tmp{os.getpid()}"
+    tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp] + [o for o, _ in results]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, lib)
+    return lib
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """Compile and link the layer operators' library; returns its path."""
+    if not force and up_to_date():
+        return LIB
+    return _compile_and_link(LIB, sources(), BUILD, verbose, ptxas_verbose)
+
+
+def build_vocab(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """Compile and link the vocabulary operators' library; returns its path."""
+    if not force and vocab_up_to_date():
+        return VOCAB_LIB
+    return _compile_and_link(VOCAB_LIB, vocab_sources(), os.path.join(BUILD, "vocab"), verbose,
+                             ptxas_verbose)
 
 
 def build_floor(force: bool = False) -> str:
@@ -108,4 +141,5 @@ if __name__ == "__main__":
     ap.add_argument("--ptxas", action="store_true", help="print -Xptxas -v register/spill report")
     a = ap.parse_args()
     print(build(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
+    print(build_vocab(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
     print(build_floor(force=a.force))

@@ -1,0 +1,63 @@
+// vec.cuh -- BF16 instances of the 8-element vectors of ls_device.cuh.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "../csrc/ls_device.cuh"
+
+namespace ls {
+
+using bf16 = __nv_bfloat16;
+
+template <> struct Raw8<bf16> { uint4 v; };
+
+template <> __device__ __forceinline__ Raw8<bf16> load8<bf16>(const bf16* p) {
+    return Raw8<bf16>{ld16(p)};
+}
+template <> __device__ __forceinline__ void store8<bf16>(bf16* p, const Raw8<bf16>& r) {
+    st16(p, r.v);
+}
+// A BF16 value is the upper half of the FP32 value: widening is a shift.
+__device__ __forceinline__ float2 b2f(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t f2b(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // round to nearest even
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ void unpack(const Raw8<bf16>& r, float (&f)[8]) {
+    float2 t;
+    t = b2f(r.v.x); f[0] = t.x; f[1] = t.y;
+    t = b2f(r.v.y); f[2] = t.x; f[3] = t.y;
+    t = b2f(r.v.z); f[4] = t.x; f[5] = t.y;
+    t = b2f(r.v.w); f[6] = t.x; f[7] = t.y;
+}
+template <> __device__ __forceinline__ Raw8<bf16> pack<bf16>(const float (&f)[8]) {
+    return Raw8<bf16>{make_uint4(f2b(f[0], f[1]), f2b(f[2], f[3]), f2b(f[4], f[5]),
+                                 f2b(f[6], f[7]))};
+}
+template <> __device__ __forceinline__ Raw8<bf16> zero8<bf16>() {
+    return Raw8<bf16>{make_uint4(0, 0, 0, 0)};
+}
+__device__ __forceinline__ float vmax8(const Raw8<bf16>& r) {
+    float f[8];
+    unpack(r, f);
+    return fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])),
+                 fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+}
+
+// Two values to one 32-bit word of the 16-bit storage type.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) { return f2h(a, b); }
+template <> __device__ __forceinline__ uint32_t pack2<bf16>(float a, float b) { return f2b(a, b); }
+
+// One value of the storage type.
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(bf16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ bf16 from_f32<bf16>(float x) { return __float2bfloat16_rn(x); }
+
+}  // namespace ls
