@@ -8,137 +8,513 @@
 // g = dloss (exp(z - lse) - (1 - eps) [j == y] - eps / V) rounded to the
 // storage type in the workspace, then dx += g W_piece and dW_piece = g^T x.
 //
+// All three products run in one kernel (head_kernel) on tcgen05: persistent
+// pairs of CTAs, each pair a 256 x 256 tile with FP32 accumulators in tensor
+// memory (two of them, so that one is read while the other is filled), operands
+// brought by TMA through a ring of 64-wide K blocks.  Warp 0 issues the copies,
+// warp 1 of the pair's first CTA the products, warps 2-5 take the accumulators
+// to the statistics, to g or to the outputs.  A pair, because a CTA on its own
+// needs 48 KB of operands for the 128 x 256 x 64 products that take it 512
+// cycles, more than the L2 gives an SM; each of a pair needs 32 KB.
+//
+// Operands of which M or N is the contiguous axis (W in g W; g and x in g^T x)
+// are read as they lie in memory: the matrix descriptors take either order.
+//
 // FP16 has no exponent range for dloss * p (1/rows times 1/vocab), so g is
 // stored as g * 2^s with 2^s max|dloss| <= 2^14 and the factor is taken out of
 // the FP32 sums again; BF16 has FP32's range and s = 0.
+#include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
-#include "vec.cuh"
+#include "tc.cuh"
 #include "vocab_internal.h"
 
 namespace ls {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kTileM = 256;   // of a pair; 128 rows for each CTA
+constexpr int kTileN = 256;
+constexpr int kBlockK = 64;   // 128 bytes: the swizzle's row
+constexpr int kStages = 6;
+constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 4;
+constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;          // one operand of one CTA and stage
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr uint32_t kPairBytes = 2 * kStageBytes;               // what a stage's barrier waits for
+constexpr uint32_t kStoreBytes = 32 * 128;                     // one warp's store box
+constexpr uint32_t kTmemColumns = 512;
+constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes;
+constexpr int kGroupM = 16;   // row tiles that share a sweep over the vocabulary
+constexpr int kPairs = 76;    // pairs of SMs; a constant, so that plans depend on the shapes alone
+
+enum Mode { kStats = 0, kGrad = 1, kOut = 2 };
+
 struct HeadArgs {
-    int64_t rows, hidden, vocab;
-    int64_t col0, cols;   // this piece of the vocabulary
-    int64_t ldg;
+    int rows, vocab, hidden;
+    int col0, cols;        // this piece of the vocabulary
+    int m_tiles, n_tiles;  // kStats, kGrad: rows x piece
+    int k_blocks;
     float eps;
     int32_t ignore_index;
+    // kOut
+    int x_units, w_units;  // units of dx and of dweight
+    int x_m_tiles, h_tiles;
+    int x_k_blocks, slice_blocks, w_k_blocks;
+    bool x_partial, x_add, w_f32;
+    // kStats
+    float2* part;          // [rows][n_tiles]: maximum, sum of exponentials
+    float* part_sum;       // [rows][n_tiles]
+    float* zy;             // [rows]
+    const int32_t* target;
+    const float* lse;
+    const float* dloss;
+    const float* scale;    // 2^s, 2^-s; NULL for 1
+};
+
+struct HeadMaps {
+    CUtensorMap a, b;    // kStats, kGrad: x, W;  kOut: g, W for dx
+    CUtensorMap a2, b2;  // kOut: g, x for dweight
+    CUtensorMap out, out2;
 };
 
 __device__ __forceinline__ bool used_target(int32_t y, const HeadArgs& a) {
     return y != a.ignore_index && y >= 0 && y < a.vocab;
 }
 
-// 64 x 64 tile of C = A B^T-like products with any strides: A(i, k) = a[i * ai + k * ak],
-// B(j, k) = b[j * bj + k * bk]; thread (tx, ty) owns 4 x 4 results.
-template <typename T>
-__device__ __forceinline__ void tile_product(float (&acc)[4][4], const T* a, int64_t ai, int64_t ak,
-                                             const T* b, int64_t bj, int64_t bk, int64_t m,
-                                             int64_t n, int64_t k, int64_t i0, int64_t j0) {
-    __shared__ float sa[16][kTile + 1], sb[16][kTile + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+// One unit of work of a pair.
+struct Unit {
+    int m0, n0;        // first row and column of the tile
+    int kb0, kbs;      // K blocks
+    int slice;
+    bool weight;       // kOut: a tile of dweight
+};
+
+template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const HeadArgs& a) {
+    Unit t;
+    t.weight = false;
+    t.slice = 0;
+    t.kb0 = 0;
+    if constexpr (MODE != kOut) {
+        const int g = u / (kGroupM * a.n_tiles);
+        const int first = g * kGroupM;
+        const int gm = min(kGroupM, a.m_tiles - first);
+        const int r = u - first * a.n_tiles;
+        t.n0 = (r / gm) * kTileN;
+        t.m0 = (first + r % gm) * kTileM;
+        t.kbs = a.k_blocks;
+    } else if (u < a.x_units) {
+        t.n0 = (u % a.h_tiles) * kTileN;
+        const int v = u / a.h_tiles;
+        t.m0 = (v % a.x_m_tiles) * kTileM;
+        t.slice = v / a.x_m_tiles;
+        t.kb0 = t.slice * a.slice_blocks;
+        t.kbs = min(a.slice_blocks, a.x_k_blocks - t.kb0);
+    } else {
+        const int v = u - a.x_units;
+        t.weight = true;
+        t.n0 = (v % a.h_tiles) * kTileN;
+        t.m0 = (v / a.h_tiles) * kTileM;
+        t.kbs = a.w_k_blocks;
+    }
+    return t;
+}
+template <int MODE> __device__ __forceinline__ int units_of(const HeadArgs& a) {
+    return MODE == kOut ? a.x_units + a.w_units : a.m_tiles * a.n_tiles;
+}
+
+// Bounded wait; false (and the failure flagged for the CTA and the host) when it runs out.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63) == 63 && *dead) return false;
+    }
+    flag_device_error(kDevErrWaitTimeout);
+    *dead = 1;
+    return false;
+}
+
+// 16 bytes `c` of a lane's 128-byte row in a swizzled store box.
+__device__ __forceinline__ void put16(unsigned char* box, int lane, int c, uint4 v) {
+    st16(box + lane * 128 + ((c ^ (lane & 7)) << 4), v);
+}
+
+// Statistics of 32 logits of one row: n of them exist (n >= 1).
+template <bool EDGE, bool SUM>
+__device__ __forceinline__ void add_stats(float (&z)[32], int n, float& m, float2& l, float2& s) {
+    if constexpr (SUM) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
+        for (int j = 0; j < 32; j += 2)
+            s = add2(s, make_float2(EDGE && j >= n ? 0.f : z[j], EDGE && j + 1 >= n ? 0.f : z[j + 1]));
+    }
+    if constexpr (EDGE) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[p][q] = 0.f;
-    for (int64_t k0 = 0; k0 < k; k0 += 16) {
-        for (int t = threadIdx.x; t < 16 * kTile; t += kThreads) {
-            const int kk = t & 15, r = t >> 4;
-            const bool in_k = k0 + kk < k;
-            sa[kk][r] = in_k && i0 + r < m ? to_f32(a[(i0 + r) * ai + (k0 + kk) * ak]) : 0.f;
-            sb[kk][r] = in_k && j0 + r < n ? to_f32(b[(j0 + r) * bj + (k0 + kk) * bk]) : 0.f;
+        for (int j = 0; j < 32; ++j) z[j] = j < n ? z[j] : -INFINITY;
+    }
+    float c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = fmaxf(fmaxf(z[j], z[j + 8]), fmaxf(z[j + 16], z[j + 24]));
+    const float cm = fmaxf(fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3])),
+                           fmaxf(fmaxf(c[4], c[5]), fmaxf(c[6], c[7])));
+    if (cm > m) {
+        const float f = exp2_approx((m - cm) * kLog2e);
+        l = mul2(l, make_float2(f, f));
+        m = cm;
+    }
+    const float mc = -m * kLog2e;
+    const float2 cc = make_float2(kLog2e, kLog2e), mm = make_float2(mc, mc);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float2 t = fma2(make_float2(z[j], z[j + 1]), cc, mm);
+        l = add2(l, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
+    }
+}
+
+// 32 values of a row of g: d (exp(z - lse) - q0 - [j == at] (1 - eps)).
+template <bool HIT>
+__device__ __forceinline__ void grads_of(float (&z)[32], float d, float ml, float q0, float qy, int at) {
+    const float2 cc = make_float2(kLog2e, kLog2e), mm = make_float2(ml, ml);
+    const float2 dd = make_float2(d, d), dq = make_float2(-d * q0, -d * q0);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float2 t = fma2(make_float2(z[j], z[j + 1]), cc, mm);
+        float2 p = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+        if constexpr (HIT) {  // subtracted before the product with d: p is near 1 there
+            if (at == j) p.x -= qy;
+            if (at == j + 1) p.y -= qy;
         }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[p][q] = fmaf(sa[kk][ty * 4 + p], sb[kk][tx * 4 + q], acc[p][q]);
-        __syncthreads();
+        p = fma2(p, dd, dq);
+        z[j] = p.x;
+        z[j + 1] = p.y;
     }
 }
 
-// part: [3][tiles][rows]: maximum, sum of exponentials, plain sum.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-logit_stats_kernel(float* __restrict__ part, float* __restrict__ zy, const T* __restrict__ x,
-                   const T* __restrict__ w, const int32_t* __restrict__ target,
-                   const __grid_constant__ HeadArgs a) {
-    __shared__ float z[kTile][kTile + 1];
-    pdl_enter();
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kTile;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    float acc[4][4];
-    tile_product<T>(acc, x, a.hidden, 1, w, a.hidden, 1, a.rows, a.vocab, a.hidden, i0, j0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int p = 0; p < 4; ++p)
-        for (int q = 0; q < 4; ++q) z[ty * 4 + p][tx * 4 + q] = acc[p][q];
+template <typename T, int MODE, bool SUM>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadArgs a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_at;
+    __shared__ volatile int dead;
+    // The swizzle's pattern repeats every 1024 bytes of the address.
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int units = units_of<MODE>(a);
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        dead = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(&drained, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + s, 1);
+            mbar_init(acc_empty + s, 2 * kEpilogueWarps);
+        }
+        mbar_init_fence();
+        prefetch_map(&maps.a);
+        prefetch_map(&maps.b);
+    }
+    if (warp == 1) tmem_alloc(&tmem_at, kTmemColumns);
+    tc_fence_before();
     __syncthreads();
-    const int64_t i = i0 + threadIdx.x;
-    if (threadIdx.x >= kTile || i >= a.rows) return;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kTile), a.vocab - j0));
-    float m = -INFINITY, l = 0.f, s = 0.f;
-    for (int j = 0; j < n; ++j) m = fmaxf(m, z[threadIdx.x][j]);
-    for (int j = 0; j < n; ++j) {
-        l += exp2_approx((z[threadIdx.x][j] - m) * kLog2e);
-        s += z[threadIdx.x][j];
-    }
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * a.rows;
-    float* o = part + blockIdx.x * a.rows + i;
-    o[0] = m;
-    o[stride] = l;
-    o[2 * stride] = s;
-    const int64_t y = target[i];
-    if (y >= j0 && y < j0 + n) zy[i] = z[threadIdx.x][y - j0];
-}
-
-__global__ void __launch_bounds__(kThreads)
-merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
-                   const float* __restrict__ part, const float* __restrict__ zy,
-                   const int32_t* __restrict__ target, int64_t tiles,
-                   const __grid_constant__ HeadArgs a) {
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
     pdl_enter();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= a.rows) return;
-    float m = -INFINITY, l = 0.f, s = 0.f;
-    const int64_t stride = tiles * a.rows;
-    for (int64_t t = 0; t < tiles; ++t) {
-        const float m2 = part[t * a.rows + i], l2 = part[stride + t * a.rows + i];
-        const float mm = fmaxf(m, m2);
-        l = l * exp2_approx((m - mm) * kLog2e) + l2 * exp2_approx((m2 - mm) * kLog2e);
-        m = mm;
-        s += part[2 * stride + t * a.rows + i];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int u = pair; u < units; u += pairs) {
+                const Unit t = unit_of<MODE>(u, a);
+                const int m = t.m0 + static_cast<int>(rank) * 128, n = t.n0 + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < t.kbs; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!wait_bar(empty + s, ((it / kStages) & 1) ^ 1, &dead)) break;
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, kPairBytes);
+                    const uint32_t bar = map_rank(full + s, 0);
+                    unsigned char* pa = smem + s * kStageBytes;
+                    unsigned char* pb = pa + kOperandBytes;
+                    const int k = (t.kb0 + kb) * kBlockK;
+                    if constexpr (MODE != kOut) {
+                        tma_load_2d(pa, &maps.a, k, m, bar);
+                        tma_load_2d(pb, &maps.b, k, a.col0 + n, bar);
+                    } else if (!t.weight) {
+                        tma_load_2d(pa, &maps.a, k, m, bar);
+                        tma_load_2d(pb, &maps.b, n, a.col0 + k, bar);
+                        tma_load_2d(pb + kOperandBytes / 2, &maps.b, n + 64, a.col0 + k, bar);
+                    } else {
+                        tma_load_2d(pa, &maps.a2, m, k, bar);
+                        tma_load_2d(pa + kOperandBytes / 2, &maps.a2, m + 64, k, bar);
+                        tma_load_2d(pb, &maps.b2, n, k, bar);
+                        tma_load_2d(pb + kOperandBytes / 2, &maps.b2, n + 64, k, bar);
+                    }
+                }
+                if (dead) break;
+            }
+            // After a failed wait: the copies in flight land before the CTA ends.
+            if (dead && rank == 0)
+                for (uint32_t s = 0; s < kStages && s < it; ++s) {
+                    const uint32_t uses = (it - 1 - s) / kStages;  // its last use, counted from 0
+                    for (uint32_t i = 0; i < kWaitPolls; ++i)
+                        if (mbar_try_wait(full + s, uses & 1)) break;
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr bool kBf16 = std::is_same<T, bf16>::value;
+            const uint64_t kmajor = desc_base(16), mnmajor = desc_base(kOperandBytes / 2);
+            uint32_t it = 0, tile = 0;
+            for (int u = pair; u < units; u += pairs, ++tile) {
+                const Unit t = unit_of<MODE>(u, a);
+                const uint32_t acc = tile & 1;
+                if (!wait_bar(acc_empty + acc, ((tile >> 1) & 1) ^ 1, &dead)) break;
+                tc_fence_after();
+                // Which operands have M or N as their contiguous axis.
+                const bool a_mn = MODE == kOut && t.weight, b_mn = MODE == kOut;
+                const uint32_t idesc = instr_desc(kBf16, false, false, kTileM, kTileN) |
+                                       (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+                const uint64_t da = a_mn ? mnmajor : kmajor, db = b_mn ? mnmajor : kmajor;
+                const uint32_t step_a = a_mn ? 16 * 128 : 32, step_b = b_mn ? 16 * 128 : 32;
+                for (int kb = 0; kb < t.kbs; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!wait_bar(full + s, (it / kStages) & 1, &dead)) break;
+                    tc_fence_after();
+                    const uint32_t pa = smem_u32(smem + s * kStageBytes), pb = pa + kOperandBytes;
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 16; ++k)
+                        tc_mma(tmem + acc * kTileN, desc_at(da, pa + k * step_a), desc_at(db, pb + k * step_b),
+                               idesc, kb > 0 || k > 0);
+                    tc_commit(empty + s);
+                }
+                if (dead) break;
+                tc_commit(acc_full + acc);
+            }
+            if (dead) {  // the products in flight end before their operands' memory is given back
+                tc_commit(&drained);
+                for (uint32_t i = 0; i < kWaitPolls; ++i)
+                    if (mbar_try_wait(&drained, 0)) break;
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3;  // the TMEM lanes this warp may read
+        unsigned char* box = smem + kStages * kStageBytes + (warp - 2) * 2 * kStoreBytes;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        uint32_t tile = 0;
+        int boxes = 0;  // store boxes used so far
+        for (int u = pair; u < units; u += pairs, ++tile) {
+            const Unit t = unit_of<MODE>(u, a);
+            const uint32_t acc = tile & 1;
+            const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
+            const int row = row0 + lane;
+            if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
+            tc_fence_after();
+            const uint32_t cols = lanes + acc * kTileN;
+            // The box that the lanes fill next, free to be written.
+            auto next_box = [&]() {
+                if (lane == 0) bulk_wait_read<1>();
+                __syncwarp();
+                return box + (boxes++ & 1) * kStoreBytes;
+            };
+            if constexpr (MODE == kStats) {
+                const int n = min(kTileN, a.cols - t.n0);
+                const int32_t y = row < a.rows ? a.target[row] : -1;
+                const int at = used_target(y, a) ? y - t.n0 : -1;
+                float m = -INFINITY;
+                float2 l = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int c = 0; c < n; c += 32) {
+                    float z[32];
+                    tmem_ld32(z, cols + c);
+                    tmem_ld_wait(z);
+                    if (__any_sync(0xffffffffu, at >= c && at < c + 32)) {
+                        float zy = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) zy = at == c + j ? z[j] : zy;
+                        if (at >= c && at < c + 32) a.zy[row] = zy;
+                    }
+                    if (c + 32 <= n)
+                        add_stats<false, SUM>(z, 32, m, l, s);
+                    else
+                        add_stats<true, SUM>(z, n - c, m, l, s);
+                }
+                if (row < a.rows) {
+                    const int64_t o = static_cast<int64_t>(row) * a.n_tiles + t.n0 / kTileN;
+                    a.part[o] = make_float2(m, l.x + l.y);
+                    if constexpr (SUM) a.part_sum[o] = s.x + s.y;
+                }
+            } else if constexpr (MODE == kGrad) {
+                const int n = min(kTileN, a.cols - t.n0);
+                const bool there = row < a.rows;
+                const int32_t y = there ? a.target[row] : -1;
+                const bool used = there && used_target(y, a);
+                const int at = used ? y - a.col0 - t.n0 : -1;
+                const float sc = a.scale ? a.scale[0] : 1.f;
+                const float d = used ? (a.dloss ? a.dloss[row] * sc : sc) : 0.f;
+                const float ml = there ? -a.lse[row] * kLog2e : 0.f;
+                const float q0 = a.eps / static_cast<float>(a.vocab), qy = 1.f - a.eps;
+#pragma unroll 1
+                for (int c = 0; c < n; c += 64) {
+                    unsigned char* b = next_box();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float z[32];
+                        tmem_ld32(z, cols + c + h * 32);
+                        tmem_ld_wait(z);
+                        const int rel = at - c - h * 32;
+                        if (__any_sync(0xffffffffu, rel >= 0 && rel < 32))
+                            grads_of<true>(z, d, ml, q0, qy, rel);
+                        else
+                            grads_of<false>(z, d, ml, q0, qy, rel);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            put16(b, lane, h * 4 + j,
+                                  used ? make_uint4(pack2<T>(z[8 * j], z[8 * j + 1]),
+                                                    pack2<T>(z[8 * j + 2], z[8 * j + 3]),
+                                                    pack2<T>(z[8 * j + 4], z[8 * j + 5]),
+                                                    pack2<T>(z[8 * j + 6], z[8 * j + 7]))
+                                       : make_uint4(0, 0, 0, 0));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row0 < a.rows) tma_store_2d(&maps.out, t.n0 + c, row0, b);
+                        bulk_commit();
+                    }
+                }
+            } else {
+                const bool f32 = t.weight ? a.w_f32 : a.x_partial;
+                const float sc = (t.weight || !a.x_partial) && a.scale ? a.scale[1] : 1.f;
+                const int n = min(kTileN, a.hidden - t.n0);
+                const bool there = row0 < (t.weight ? a.cols : a.rows);
+                if (f32) {
+#pragma unroll 1
+                    for (int c = 0; c < n; c += 32) {
+                        unsigned char* b = next_box();
+                        float z[32];
+                        tmem_ld32(z, cols + c);
+                        tmem_ld_wait(z);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            put16(b, lane, j,
+                                  f2u4(make_float4(z[4 * j] * sc, z[4 * j + 1] * sc, z[4 * j + 2] * sc,
+                                                   z[4 * j + 3] * sc)));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (there && t.weight)
+                                tma_add_2d(&maps.out2, t.n0 + c, a.col0 + row0, b);
+                            else if (there && a.x_add)
+                                tma_add_3d(&maps.out, t.n0 + c, row0, t.slice, b);
+                            else if (there)
+                                tma_store_3d(&maps.out, t.n0 + c, row0, t.slice, b);
+                            bulk_commit();
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < n; c += 64) {
+                        unsigned char* b = next_box();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float z[32];
+                            tmem_ld32(z, cols + c + h * 32);
+                            tmem_ld_wait(z);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                put16(b, lane, h * 4 + j,
+                                      make_uint4(pack2<T>(z[8 * j] * sc, z[8 * j + 1] * sc),
+                                                 pack2<T>(z[8 * j + 2] * sc, z[8 * j + 3] * sc),
+                                                 pack2<T>(z[8 * j + 4] * sc, z[8 * j + 5] * sc),
+                                                 pack2<T>(z[8 * j + 6] * sc, z[8 * j + 7] * sc)));
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (there && t.weight)
+                                tma_store_2d(&maps.out2, t.n0 + c, a.col0 + row0, b);
+                            else if (there)
+                                tma_store_2d(&maps.out, t.n0 + c, row0, b);
+                            bulk_commit();
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty + acc, 0));
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
-    const float lse = m + logf(l);
-    if (lse_out) lse_out[i] = lse;
-    loss[i] = used_target(target[i], a)
-                  ? (1.f - a.eps) * (lse - zy[i]) +
-                        (a.eps > 0.f ? a.eps * (lse - s / static_cast<float>(a.vocab)) : 0.f)
-                  : 0.f;
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free(tmem, kTmemColumns);
 }
 
-// scale[0] = 2^s, scale[1] = 2^-s.
+// One warp per row: the row's tiles merged.
+__global__ void __launch_bounds__(256)
+merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out, const __grid_constant__ HeadArgs a) {
+    pdl_enter();
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= a.rows) return;
+    const float2* part = a.part + static_cast<int64_t>(row) * a.n_tiles;
+    const float* part_sum = a.part_sum + static_cast<int64_t>(row) * a.n_tiles;
+    float m = -INFINITY, l = 0.f, s = 0.f;
+    auto merge = [&](float m2, float l2) {
+        const float mm = fmaxf(m, m2);
+        if (mm == -INFINITY) {
+            l += l2;
+        } else {
+            l = l * exp2_approx((m - mm) * kLog2e) + l2 * exp2_approx((m2 - mm) * kLog2e);
+            m = mm;
+        }
+    };
+#pragma unroll 4
+    for (int t = lane; t < a.n_tiles; t += 32) {
+        const float2 p = part[t];
+        merge(p.x, p.y);
+        if (a.eps > 0.f) s += part_sum[t];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        merge(m2, l2);
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    }
+    if (lane != 0) return;
+    const float lse = m + logf(l);
+    if (lse_out) lse_out[row] = lse;
+    float v = 0.f;
+    if (used_target(a.target[row], a)) {
+        v = (1.f - a.eps) * (lse - a.zy[row]);
+        if (a.eps > 0.f) v += a.eps * (lse - s / static_cast<float>(a.vocab));
+    }
+    loss[row] = v;
+}
+
+// scale[0] = 2^s, scale[1] = 2^-s with 2^s max|dloss| in (2^13, 2^14].
 __global__ void __launch_bounds__(1024)
-grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, int64_t rows,
-                  bool scaled) {
+grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, int64_t rows) {
     __shared__ float sm[32];
     pdl_enter();
-    float m = dloss ? 0.f : 1.f;
-    if (dloss && scaled)
-        for (int64_t i = threadIdx.x; i < rows; i += 1024) {
-            const float d = fabsf(dloss[i]);
-            if (d < INFINITY) m = fmaxf(m, d);
-        }
+    float m = 0.f;
+    for (int64_t i = threadIdx.x; i < rows; i += 1024) {
+        const float d = fabsf(dloss[i]);
+        if (d < INFINITY) m = fmaxf(m, d);
+    }
     m = group_max<32>(m);
     if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -146,7 +522,7 @@ grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, in
         m = group_max<32>(sm[threadIdx.x]);
         if (threadIdx.x == 0) {
             int s = 0;
-            if (scaled && m > 0.f) {
+            if (m > 0.f) {
                 int ex;
                 frexpf(m, &ex);  // m < 2^ex
                 s = min(100, max(-100, 14 - ex));
@@ -157,180 +533,219 @@ grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, in
     }
 }
 
+// dx = scale * sum over the slices' partial sums, in slice order.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-logit_grad_kernel(T* __restrict__ g, const T* __restrict__ x, const T* __restrict__ w,
-                  const int32_t* __restrict__ target, const float* __restrict__ lse,
-                  const float* __restrict__ dloss, const float* __restrict__ scale,
-                  const __grid_constant__ HeadArgs a) {
+__global__ void __launch_bounds__(256)
+join_slices_kernel(T* __restrict__ dx, const float* __restrict__ part, const float* __restrict__ scale,
+                   int slices, int64_t nvec) {
     pdl_enter();
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kTile;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    float acc[4][4];
-    tile_product<T>(acc, x, a.hidden, 1, w + a.col0 * a.hidden, a.hidden, 1, a.rows, a.cols,
-                    a.hidden, i0, j0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const float q0 = a.eps / static_cast<float>(a.vocab);
-    for (int p = 0; p < 4; ++p) {
-        const int64_t i = i0 + ty * 4 + p;
-        if (i >= a.rows) break;
-        const int64_t y = target[i];
-        const bool used = used_target(static_cast<int32_t>(y), a);
-        const float d = (dloss ? dloss[i] : 1.f) * scale[0];
-        for (int q = 0; q < 4; ++q) {
-            const int64_t j = j0 + tx * 4 + q;
-            if (j >= a.cols) break;
-            const float t = q0 + (a.col0 + j == y ? 1.f - a.eps : 0.f);
-            g[i * a.ldg + j] =
-                from_f32<T>(used ? d * (exp2_approx((acc[p][q] - lse[i]) * kLog2e) - t) : 0.f);
-        }
+    const int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (v >= nvec) return;
+    const float sc = scale ? scale[1] : 1.f;
+    float acc[kVec];
+    load8f<float>(part + v * kVec, acc);
+    for (int s = 1; s < slices; ++s) {
+        float f[kVec];
+        load8f<float>(part + (s * nvec + v) * kVec, f);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) acc[j] += f[j];
     }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) acc[j] *= sc;
+    store8f<T>(dx + v * kVec, acc);
 }
 
-// dx accumulator (FP32 [rows, hidden]) (+)= g W_piece; the last piece writes dx.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-dx_kernel(float* acc_buf, T* __restrict__ dx, const T* __restrict__ g, const T* __restrict__ w,
-          const float* __restrict__ scale, bool first, bool last,
-          const __grid_constant__ HeadArgs a) {
-    pdl_enter();
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kTile;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    float acc[4][4];
-    tile_product<T>(acc, g, a.ldg, 1, w + a.col0 * a.hidden, 1, a.hidden, a.rows, a.hidden, a.cols,
-                    i0, j0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int p = 0; p < 4; ++p) {
-        const int64_t i = i0 + ty * 4 + p;
-        for (int q = 0; q < 4; ++q) {
-            const int64_t j = j0 + tx * 4 + q;
-            if (i >= a.rows || j >= a.hidden) continue;
-            float v = acc[p][q];
-            if (!first) v += acc_buf[i * a.hidden + j];
-            if (last)
-                dx[i * a.hidden + j] = from_f32<T>(v * scale[1]);
-            else
-                acc_buf[i * a.hidden + j] = v;
-        }
-    }
-}
+// --- host ----------------------------------------------------------------------
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <typename T, typename D>
-__global__ void __launch_bounds__(kThreads)
-dweight_kernel(D* dw, const T* __restrict__ g, const T* __restrict__ x,
-               const float* __restrict__ scale, const __grid_constant__ HeadArgs a) {
-    pdl_enter();
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kTile;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    float acc[4][4];
-    tile_product<T>(acc, g, 1, a.ldg, x, 1, a.hidden, a.cols, a.hidden, a.rows, i0, j0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int p = 0; p < 4; ++p) {
-        const int64_t i = i0 + ty * 4 + p;
-        for (int q = 0; q < 4; ++q) {
-            const int64_t j = j0 + tx * 4 + q;
-            if (i >= a.cols || j >= a.hidden) continue;
-            D* o = dw + (a.col0 + i) * a.hidden + j;
-            float v = acc[p][q] * scale[1];
-            if constexpr (sizeof(D) == 4) v += *o;
-            *o = from_f32<D>(v);
-        }
-    }
-}
-
-// Pieces: gradients of the logits of `cols` vocabulary entries at a time, about 128 MB.
+// Pieces: g for `cols` vocabulary entries at a time, about 128 MB of it.
 constexpr int64_t kPieceBytes = int64_t{128} << 20;
 
+// Sizes and workspace layout; they depend on the shapes alone.
 struct HeadPlan {
-    int64_t tiles, cols;
-    size_t part, zy, scale, g, acc, fwd_bytes, bwd_bytes;
+    int64_t n_tiles;                       // of the whole vocabulary
+    int64_t cols, pieces;                  // columns of a piece (the last may have fewer)
+    int64_t slices, slice_blocks;          // dx: K blocks of a piece per slice
+    size_t part, part_sum, zy, scale, g, partial, bytes;
+    bool partial_dx;
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
-        tiles = (vocab + kTile - 1) / kTile;
+        n_tiles = ceil_div(vocab, kTileN);
         part = 0;
-        zy = static_cast<size_t>(3 * tiles * rows) * 4;
-        fwd_bytes = zy + static_cast<size_t>(rows) * 4;
-        cols = kPieceBytes / 2 / rows / 256 * 256;
-        if (cols < 2048) cols = 2048;
-        const int64_t all = (vocab + 255) / 256 * 256;
-        if (cols > all) cols = all;
+        part_sum = round256(static_cast<size_t>(rows * n_tiles) * 8);
+        zy = part_sum + round256(static_cast<size_t>(rows * n_tiles) * 4);
+        const size_t fwd = zy + static_cast<size_t>(rows) * 4;
+
+        const int64_t most = std::max<int64_t>(2048, kPieceBytes / 2 / rows / kTileN * kTileN);
+        pieces = ceil_div(vocab, most);
+        cols = ceil_div(ceil_div(vocab, pieces), kTileN) * kTileN;
+        pieces = ceil_div(vocab, cols);
+        const int64_t m_tiles = ceil_div(rows, kTileM), h_tiles = ceil_div(hidden, kTileN);
+        const int64_t kb = ceil_div(std::min(cols, vocab), kBlockK);
+        // dx: K is cut so that one unit is a small part of a pair's share of the piece's products.
+        const int64_t work = m_tiles * h_tiles * kb + ceil_div(cols, kTileM) * h_tiles * ceil_div(rows, kBlockK);
+        slice_blocks = std::max<int64_t>(8, ceil_div(work, kPairs * 3));
+        slices = std::min<int64_t>(32, ceil_div(kb, slice_blocks));
+        slice_blocks = ceil_div(kb, slices);
+        slices = ceil_div(kb, slice_blocks);
+        partial_dx = slices > 1 || pieces > 1;
         scale = 0;
         g = 256;
-        acc = g + static_cast<size_t>(rows * cols) * 2;
-        bwd_bytes = acc + (cols < vocab ? static_cast<size_t>(rows * hidden) * 4 : 0);
+        partial = g + round256(static_cast<size_t>(rows * cols) * 2);
+        const size_t bwd = partial + (partial_dx ? static_cast<size_t>(slices * rows * hidden) * 4 : 0);
+        bytes = std::max(fwd, bwd);
     }
-    size_t bytes() const { return fwd_bytes > bwd_bytes ? fwd_bytes : bwd_bytes; }
 };
 
-HeadArgs make_args(const HeadShape& sh) {
-    HeadArgs a;
-    a.rows = sh.rows;
-    a.hidden = sh.hidden;
-    a.vocab = sh.vocab;
-    a.col0 = 0;
-    a.cols = sh.vocab;
-    a.ldg = 0;
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                               cudaEnableDefault, &r);
+        return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// A row-major [depth][outer][inner] tensor in boxes of [1][box_outer][128 bytes].
+template <typename E>
+cudaError_t make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
+                     int64_t depth = 0) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const CUtensorMapDataType type = std::is_same<E, float>::value  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : std::is_same<E, bf16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t size = sizeof(E);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                                static_cast<cuuint64_t>(depth)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size,
+                                   static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(outer) * size};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_outer), 1};
+    const cuuint32_t one[3] = {1, 1, 1};
+    const CUresult r = fn(map, type, depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int MODE, bool SUM>
+cudaError_t launch_head(const HeadMaps& maps, const HeadArgs& a, int64_t units, cudaStream_t s) {
+    static int done[kMaxDevices];
+    cudaError_t e = allow_max_dynamic_smem(head_kernel<T, MODE, SUM>, done);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = std::min<int64_t>(units, kPairs);
+    return launch_pdl(head_kernel<T, MODE, SUM>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes,
+                      s, maps, a);
+}
+
+HeadArgs make_args(const HeadShape& sh, const int32_t* target) {
+    HeadArgs a = {};
+    a.rows = static_cast<int>(sh.rows);
+    a.vocab = static_cast<int>(sh.vocab);
+    a.hidden = static_cast<int>(sh.hidden);
+    a.cols = a.vocab;
+    a.m_tiles = static_cast<int>(ceil_div(sh.rows, kTileM));
+    a.n_tiles = static_cast<int>(ceil_div(sh.vocab, kTileN));
+    a.k_blocks = static_cast<int>(ceil_div(sh.hidden, kBlockK));
     a.eps = sh.eps;
     a.ignore_index = sh.ignore_index;
+    a.target = target;
     return a;
 }
 
-unsigned tiles_of(int64_t n) { return static_cast<unsigned>((n + kTile - 1) / kTile); }
+#define LS_CUDA(expr)                        \
+    do {                                     \
+        const cudaError_t _e = (expr);       \
+        if (_e != cudaSuccess) return _e;    \
+    } while (0)
 
 template <typename T>
-cudaError_t fwd(float* loss, float* lse, const void* x, const void* w, const int32_t* target,
-                const HeadShape& sh, void* workspace, cudaStream_t s) {
+cudaError_t fwd(float* loss, float* lse, const void* x, const void* w, const int32_t* target, const HeadShape& sh,
+                void* workspace, cudaStream_t s) {
     const HeadPlan p(sh.rows, sh.hidden, sh.vocab);
-    const HeadArgs a = make_args(sh);
     char* ws = static_cast<char*>(workspace);
-    float* part = reinterpret_cast<float*>(ws + p.part);
-    float* zy = reinterpret_cast<float*>(ws + p.zy);
-    cudaError_t e = launch_pdl(logit_stats_kernel<T>, dim3(tiles_of(sh.vocab), tiles_of(sh.rows)),
-                               dim3(kThreads), 0, s, part, zy, static_cast<const T*>(x),
-                               static_cast<const T*>(w), target, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(merge_stats_kernel,
-                      dim3(static_cast<unsigned>((sh.rows + kThreads - 1) / kThreads)),
-                      dim3(kThreads), 0, s, loss, lse, part, zy, target, p.tiles, a);
+    HeadArgs a = make_args(sh, target);
+    a.part = reinterpret_cast<float2*>(ws + p.part);
+    a.part_sum = reinterpret_cast<float*>(ws + p.part_sum);
+    a.zy = reinterpret_cast<float*>(ws + p.zy);
+    HeadMaps maps = {};
+    LS_CUDA(make_map<T>(&maps.a, x, sh.hidden, sh.rows, sh.hidden, 128));
+    LS_CUDA(make_map<T>(&maps.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
+    const int64_t units = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
+    if (sh.eps > 0.f)
+        LS_CUDA((launch_head<T, kStats, true>(maps, a, units, s)));
+    else
+        LS_CUDA((launch_head<T, kStats, false>(maps, a, units, s)));
+    return launch_pdl(merge_stats_kernel, dim3(static_cast<unsigned>(ceil_div(sh.rows, 8))), dim3(256), 0, s, loss,
+                      lse, a);
 }
 
 template <typename T>
-cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const void* w,
-                const int32_t* target, const float* lse, const float* dloss, const HeadShape& sh,
-                void* workspace, cudaStream_t s) {
+cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const void* w, const int32_t* target,
+                const float* lse, const float* dloss, const HeadShape& sh, void* workspace, cudaStream_t s) {
     const HeadPlan p(sh.rows, sh.hidden, sh.vocab);
-    HeadArgs a = make_args(sh);
-    a.ldg = p.cols;
     char* ws = static_cast<char*>(workspace);
-    float* scale = reinterpret_cast<float*>(ws + p.scale);
-    T* g = reinterpret_cast<T*>(ws + p.g);
-    float* acc = reinterpret_cast<float*>(ws + p.acc);
-    const T* xt = static_cast<const T*>(x);
-    const T* wt = static_cast<const T*>(w);
-    cudaError_t e = launch_pdl(grad_scale_kernel, dim3(1), dim3(1024), 0, s, scale, dloss, sh.rows,
-                               std::is_same<T, __half>::value);
-    for (int64_t c = 0; e == cudaSuccess && c < sh.vocab; c += p.cols) {
-        a.col0 = c;
-        a.cols = sh.vocab - c < p.cols ? sh.vocab - c : p.cols;
-        e = launch_pdl(logit_grad_kernel<T>, dim3(tiles_of(a.cols), tiles_of(sh.rows)),
-                       dim3(kThreads), 0, s, g, xt, wt, target, lse, dloss, scale, a);
-        if (e == cudaSuccess && dx)
-            e = launch_pdl(dx_kernel<T>, dim3(tiles_of(sh.hidden), tiles_of(sh.rows)),
-                           dim3(kThreads), 0, s, acc, static_cast<T*>(dx), g, wt, scale, c == 0,
-                           c + a.cols == sh.vocab, a);
-        const dim3 wgrid(tiles_of(sh.hidden), tiles_of(a.cols));
-        if (e == cudaSuccess && dweight)
-            e = f32_dweight ? launch_pdl(dweight_kernel<T, float>, wgrid, dim3(kThreads), 0, s,
-                                         static_cast<float*>(dweight), g, xt, scale, a)
-                            : launch_pdl(dweight_kernel<T, T>, wgrid, dim3(kThreads), 0, s,
-                                         static_cast<T*>(dweight), g, xt, scale, a);
+    float* scale = nullptr;
+    if (std::is_same<T, __half>::value && dloss) {
+        scale = reinterpret_cast<float*>(ws + p.scale);
+        LS_CUDA(launch_pdl(grad_scale_kernel, dim3(1), dim3(1024), 0, s, scale, dloss, sh.rows));
     }
-    return e;
+    T* g = reinterpret_cast<T*>(ws + p.g);
+    float* partial = reinterpret_cast<float*>(ws + p.partial);
+    HeadArgs a = make_args(sh, target);
+    a.lse = lse;
+    a.dloss = dloss;
+    a.scale = scale;
+    a.x_m_tiles = a.m_tiles;
+    a.h_tiles = static_cast<int>(ceil_div(sh.hidden, kTileN));
+    a.slice_blocks = static_cast<int>(p.slice_blocks);
+    a.w_k_blocks = static_cast<int>(ceil_div(sh.rows, kBlockK));
+    a.x_partial = p.partial_dx;
+    a.w_f32 = f32_dweight;
+    HeadMaps mz = {}, mo = {};
+    LS_CUDA(make_map<T>(&mz.a, x, sh.hidden, sh.rows, sh.hidden, 128));
+    LS_CUDA(make_map<T>(&mz.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
+    LS_CUDA(make_map<T>(&mo.b, w, sh.hidden, sh.vocab, sh.hidden, 64));
+    LS_CUDA(make_map<T>(&mo.b2, x, sh.hidden, sh.rows, sh.hidden, 64));
+    if (dx && p.partial_dx)
+        LS_CUDA(make_map<float>(&mo.out, partial, sh.hidden, sh.rows, sh.hidden, 32, p.slices));
+    else if (dx)
+        LS_CUDA(make_map<T>(&mo.out, dx, sh.hidden, sh.rows, sh.hidden, 32));
+    if (dweight && f32_dweight)
+        LS_CUDA(make_map<float>(&mo.out2, dweight, sh.hidden, sh.vocab, sh.hidden, 32));
+    else if (dweight)
+        LS_CUDA(make_map<T>(&mo.out2, dweight, sh.hidden, sh.vocab, sh.hidden, 32));
+    for (int64_t c = 0; c < sh.vocab; c += p.cols) {
+        const int64_t cols = std::min(p.cols, sh.vocab - c);
+        a.col0 = static_cast<int>(c);
+        a.cols = static_cast<int>(cols);
+        a.n_tiles = static_cast<int>(ceil_div(cols, kTileN));
+        LS_CUDA(make_map<T>(&mz.out, g, cols, sh.rows, p.cols, 32));
+        LS_CUDA((launch_head<T, kGrad, false>(mz, a, static_cast<int64_t>(a.m_tiles) * a.n_tiles, s)));
+        LS_CUDA(make_map<T>(&mo.a, g, cols, sh.rows, p.cols, 128));
+        LS_CUDA(make_map<T>(&mo.a2, g, cols, sh.rows, p.cols, 64));
+        a.x_k_blocks = static_cast<int>(ceil_div(cols, kBlockK));
+        a.x_add = c > 0;
+        a.x_units = dx ? static_cast<int>(ceil_div(a.x_k_blocks, a.slice_blocks)) * a.x_m_tiles * a.h_tiles : 0;
+        a.w_units = dweight ? static_cast<int>(ceil_div(cols, kTileM)) * a.h_tiles : 0;
+        LS_CUDA((launch_head<T, kOut, false>(mo, a, static_cast<int64_t>(a.x_units) + a.w_units, s)));
+    }
+    if (!dx || !p.partial_dx) return cudaSuccess;
+    const int64_t nvec = sh.rows * sh.hidden / kVec;
+    return launch_pdl(join_slices_kernel<T>, dim3(static_cast<unsigned>(ceil_div(nvec, 256))), dim3(256), 0, s,
+                      static_cast<T*>(dx), partial, scale, static_cast<int>(p.slices), nvec);
 }
 
 }  // namespace
 
 size_t linear_ce_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab) {
-    return HeadPlan(rows, hidden, vocab).bytes();
+    return HeadPlan(rows, hidden, vocab).bytes;
 }
 
 cudaError_t launch_linear_ce_fwd(ls_dtype dt, float* loss, float* lse, const void* x,

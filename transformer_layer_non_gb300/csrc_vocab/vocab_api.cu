@@ -63,6 +63,9 @@ ls_status check_head(const char* fn, ls_dtype dt, int64_t rows, int64_t hidden, 
     LS_TRY(check_size(fn, "hidden", hidden, 1, ls::kMaxHeadHidden));
     LS_TRY(check_multiple_of_8(fn, "hidden", hidden));
     LS_TRY(check_size(fn, "vocab", vocab, 1, ls::kMaxVocab));
+    if (rows * vocab > (int64_t{1} << 46) || vocab * hidden > (int64_t{1} << 40))
+        return fail(LS_ERR_UNSUPPORTED_SHAPE, "%s: %lld rows of %lld logits too large", fn,
+                    (long long)rows, (long long)vocab);
     if (!(eps >= 0.f && eps < 1.f))
         return fail(LS_ERR_INVALID_ARGUMENT, "%s: label_smoothing = %g is not in [0, 1)", fn,
                     static_cast<double>(eps));
