@@ -12,7 +12,7 @@
 // pairs of CTAs, each pair a 256 x 256 tile with FP32 accumulators in tensor
 // memory (two of them, so that one is read while the other is filled), operands
 // brought by TMA through a ring of 64-wide K blocks.  Warp 0 issues the copies,
-// warp 1 of the pair's first CTA the products, warps 2-5 take the accumulators
+// warp 1 of the pair's first CTA the products, warps 2-9 take the accumulators
 // to the statistics, to g or to the outputs.  A pair, because a CTA on its own
 // needs 48 KB of operands for the 128 x 256 x 64 products that take it 512
 // cycles, more than the L2 gives an SM; each of a pair needs 32 KB.
@@ -41,14 +41,14 @@ constexpr int kTileM = 256;   // of a pair; 128 rows for each CTA
 constexpr int kTileN = 256;
 constexpr int kBlockK = 64;   // 128 bytes: the swizzle's row
 constexpr int kStages = 6;
-constexpr int kThreads = 192;
-constexpr int kEpilogueWarps = 4;
+constexpr int kEpilogueWarps = 8;  // two for each quarter of the tensor memory's lanes, half the columns each
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kWarpColumns = kTileN / 2;
 constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;          // one operand of one CTA and stage
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
-constexpr uint32_t kPairBytes = 2 * kStageBytes;               // what a stage's barrier waits for
 constexpr uint32_t kStoreBytes = 32 * 128;                     // one warp's store box
 constexpr uint32_t kTmemColumns = 512;
-constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes;
+constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * kStoreBytes;
 constexpr int kGroupM = 16;   // row tiles that share a sweep over the vocabulary
 constexpr int kPairs = 76;    // pairs of SMs; a constant, so that plans depend on the shapes alone
 
@@ -67,8 +67,8 @@ struct HeadArgs {
     int x_k_blocks, slice_blocks, w_k_blocks;
     bool x_partial, x_add, w_f32;
     // kStats
-    float2* part;          // [rows][n_tiles]: maximum, sum of exponentials
-    float* part_sum;       // [rows][n_tiles]
+    float2* part;          // [rows][2 n_tiles]: maximum, sum of exponentials of a warp's columns
+    float* part_sum;       // [rows][2 n_tiles]
     float* zy;             // [rows]
     const int32_t* target;
     const float* lse;
@@ -127,11 +127,12 @@ template <int MODE> __device__ __forceinline__ int units_of(const HeadArgs& a) {
     return MODE == kOut ? a.x_units + a.w_units : a.m_tiles * a.n_tiles;
 }
 
-// Bounded wait; false (and the failure flagged for the CTA and the host) when it runs out.
+// Bounded wait of a converged warp; false (and the failure flagged for the CTA
+// and the host) when it runs out.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead) {
     for (uint32_t i = 0; i < kWaitPolls; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63) == 63 && *dead) return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 63) == 63 && __any_sync(0xffffffffu, *dead)) return false;
     }
     flag_device_error(kDevErrWaitTimeout);
     *dead = 1;
@@ -193,6 +194,31 @@ __device__ __forceinline__ void grads_of(float (&z)[32], float d, float ml, floa
     }
 }
 
+template <typename T> __device__ __forceinline__ uint4 pack8(const float (&z)[32], int j, float sc) {
+    return make_uint4(pack2<T>(z[j] * sc, z[j + 1] * sc), pack2<T>(z[j + 2] * sc, z[j + 3] * sc),
+                      pack2<T>(z[j + 4] * sc, z[j + 5] * sc), pack2<T>(z[j + 6] * sc, z[j + 7] * sc));
+}
+
+// f(c, z) for the warp's four groups of 32 accumulator columns, the next group
+// on its way while f works; release() once all of them are in registers.
+template <typename R, typename F>
+__device__ __forceinline__ void sweep(uint32_t cols, R&& release, F&& f) {
+    float za[32], zb[32];
+    tmem_ld32(za, cols);
+    tmem_ld_wait(za);
+    tmem_ld32(zb, cols + 32);
+    f(0, za);
+    tmem_ld_wait(zb);
+    tmem_ld32(za, cols + 64);
+    f(1, zb);
+    tmem_ld_wait(za);
+    tmem_ld32(zb, cols + 96);
+    f(2, za);
+    tmem_ld_wait(zb);
+    release();
+    f(3, zb);
+}
+
 template <typename T, int MODE, bool SUM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadArgs a) {
@@ -230,16 +256,17 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
     const uint32_t tmem = tmem_at;
     pdl_enter();
 
+    // The copying and the multiplying warp stay converged: all lanes wait, one elected lane issues.
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int u = pair; u < units; u += pairs) {
-                const Unit t = unit_of<MODE>(u, a);
-                const int m = t.m0 + static_cast<int>(rank) * 128, n = t.n0 + static_cast<int>(rank) * 128;
-                for (int kb = 0; kb < t.kbs; ++kb, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!wait_bar(empty + s, ((it / kStages) & 1) ^ 1, &dead)) break;
-                    if (rank == 0) mbar_arrive_expect_tx(full + s, kPairBytes);
+        uint32_t it = 0;
+        for (int u = pair; u < units; u += pairs) {
+            const Unit t = unit_of<MODE>(u, a);
+            const int m = t.m0 + static_cast<int>(rank) * 128, n = t.n0 + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < t.kbs; ++kb, ++it) {
+                const uint32_t s = it % kStages;
+                if (!wait_bar(empty + s, ((it / kStages) & 1) ^ 1, &dead)) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * kStageBytes);  // both CTAs' copies
                     const uint32_t bar = map_rank(full + s, 0);
                     unsigned char* pa = smem + s * kStageBytes;
                     unsigned char* pb = pa + kOperandBytes;
@@ -258,19 +285,20 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         tma_load_2d(pb + kOperandBytes / 2, &maps.b2, n + 64, k, bar);
                     }
                 }
-                if (dead) break;
+                __syncwarp();
             }
-            // After a failed wait: the copies in flight land before the CTA ends.
-            if (dead && rank == 0)
-                for (uint32_t s = 0; s < kStages && s < it; ++s) {
-                    const uint32_t uses = (it - 1 - s) / kStages;  // its last use, counted from 0
-                    for (uint32_t i = 0; i < kWaitPolls; ++i)
-                        if (mbar_try_wait(full + s, uses & 1)) break;
-                }
+            if (dead) break;
         }
+        // After a failed wait: the copies in flight land before the CTA ends.
+        if (dead && rank == 0)
+            for (uint32_t s = 0; s < kStages && s < it; ++s) {
+                const uint32_t uses = (it - 1 - s) / kStages;  // its last use, counted from 0
+                for (uint32_t i = 0; i < kWaitPolls; ++i)
+                    if (mbar_try_wait(full + s, uses & 1)) break;
+            }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr bool kBf16 = std::is_same<T, bf16>::value;
             const uint64_t kmajor = desc_base(16), mnmajor = desc_base(kOperandBytes / 2);
             uint32_t it = 0, tile = 0;
@@ -283,176 +311,159 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 const bool a_mn = MODE == kOut && t.weight, b_mn = MODE == kOut;
                 const uint32_t idesc = instr_desc(kBf16, false, false, kTileM, kTileN) |
                                        (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-                const uint64_t da = a_mn ? mnmajor : kmajor, db = b_mn ? mnmajor : kmajor;
-                const uint32_t step_a = a_mn ? 16 * 128 : 32, step_b = b_mn ? 16 * 128 : 32;
+                const uint64_t da = desc_at(a_mn ? mnmajor : kmajor, smem_u32(smem));
+                const uint64_t db = desc_at(b_mn ? mnmajor : kmajor, smem_u32(smem) + kOperandBytes);
+                // 16 values of K further on, in the descriptors' units of 16 bytes
+                const uint32_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
+                const uint32_t d = tmem + acc * kTileN;
                 for (int kb = 0; kb < t.kbs; ++kb, ++it) {
                     const uint32_t s = it % kStages;
                     if (!wait_bar(full + s, (it / kStages) & 1, &dead)) break;
                     tc_fence_after();
-                    const uint32_t pa = smem_u32(smem + s * kStageBytes), pb = pa + kOperandBytes;
+                    if (elect_one()) {
+                        const uint32_t at = s * (kStageBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < kBlockK / 16; ++k)
-                        tc_mma(tmem + acc * kTileN, desc_at(da, pa + k * step_a), desc_at(db, pb + k * step_b),
-                               idesc, kb > 0 || k > 0);
-                    tc_commit(empty + s);
+                        for (int k = 0; k < kBlockK / 16; ++k)
+                            tc_mma(d, da + (at + k * step_a), db + (at + k * step_b), idesc, kb + k > 0);
+                        tc_commit(empty + s);
+                    }
+                    __syncwarp();
                 }
                 if (dead) break;
-                tc_commit(acc_full + acc);
+                if (elect_one()) tc_commit(acc_full + acc);
+                __syncwarp();
             }
             if (dead) {  // the products in flight end before their operands' memory is given back
-                tc_commit(&drained);
+                if (elect_one()) tc_commit(&drained);
+                __syncwarp();
                 for (uint32_t i = 0; i < kWaitPolls; ++i)
                     if (mbar_try_wait(&drained, 0)) break;
             }
         }
         __syncwarp();
     } else {
-        const int quad = warp & 3;  // the TMEM lanes this warp may read
-        unsigned char* box = smem + kStages * kStageBytes + (warp - 2) * 2 * kStoreBytes;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const int quad = warp & 3;          // the TMEM lanes this warp may read
+        const int half = (warp - 2) >> 2;   // its half of the tile's columns
+        unsigned char* box = smem + kStages * kStageBytes + (warp - 2) * kStoreBytes;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kWarpColumns;
         uint32_t tile = 0;
-        int boxes = 0;  // store boxes used so far
         for (int u = pair; u < units; u += pairs, ++tile) {
             const Unit t = unit_of<MODE>(u, a);
             const uint32_t acc = tile & 1;
             const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
             const int row = row0 + lane;
+            const int n0 = t.n0 + half * kWarpColumns;                         // and column
             if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
             tc_fence_after();
             const uint32_t cols = lanes + acc * kTileN;
-            // The box that the lanes fill next, free to be written.
-            auto next_box = [&]() {
-                if (lane == 0) bulk_wait_read<1>();
+            auto release = [&]() {  // the accumulator has been read
+                tc_fence_before();
                 __syncwarp();
-                return box + (boxes++ & 1) * kStoreBytes;
+                if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty + acc, 0));
+            };
+            // The store box, free to be written; and on its way to memory.
+            auto open_box = [&]() {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+            };
+            auto close_box = [&](auto&& store) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    store();
+                    bulk_commit();
+                }
             };
             if constexpr (MODE == kStats) {
-                const int n = min(kTileN, a.cols - t.n0);
+                const int n = a.cols - n0;  // columns that exist
                 const int32_t y = row < a.rows ? a.target[row] : -1;
-                const int at = used_target(y, a) ? y - t.n0 : -1;
+                const int at = used_target(y, a) ? y - n0 : -1;
                 float m = -INFINITY;
                 float2 l = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
-#pragma unroll 1
-                for (int c = 0; c < n; c += 32) {
-                    float z[32];
-                    tmem_ld32(z, cols + c);
-                    tmem_ld_wait(z);
-                    if (__any_sync(0xffffffffu, at >= c && at < c + 32)) {
+                sweep(cols, release, [&](int c, float (&z)[32]) {
+                    const int rel = at - c * 32;
+                    if (__any_sync(0xffffffffu, rel >= 0 && rel < 32)) {
                         float zy = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) zy = at == c + j ? z[j] : zy;
-                        if (at >= c && at < c + 32) a.zy[row] = zy;
+                        for (int j = 0; j < 32; ++j) zy = rel == j ? z[j] : zy;
+                        if (rel >= 0 && rel < 32) a.zy[row] = zy;
                     }
-                    if (c + 32 <= n)
+                    if (c * 32 + 32 <= n)
                         add_stats<false, SUM>(z, 32, m, l, s);
-                    else
-                        add_stats<true, SUM>(z, n - c, m, l, s);
-                }
+                    else if (c * 32 < n)
+                        add_stats<true, SUM>(z, n - c * 32, m, l, s);
+                });
                 if (row < a.rows) {
-                    const int64_t o = static_cast<int64_t>(row) * a.n_tiles + t.n0 / kTileN;
+                    const int64_t o = static_cast<int64_t>(row) * (2 * a.n_tiles) + n0 / kWarpColumns;
                     a.part[o] = make_float2(m, l.x + l.y);
                     if constexpr (SUM) a.part_sum[o] = s.x + s.y;
                 }
             } else if constexpr (MODE == kGrad) {
-                const int n = min(kTileN, a.cols - t.n0);
+                const int n = a.cols - n0;
                 const bool there = row < a.rows;
                 const int32_t y = there ? a.target[row] : -1;
                 const bool used = there && used_target(y, a);
-                const int at = used ? y - a.col0 - t.n0 : -1;
+                const int at = used ? y - a.col0 - n0 : -1;
                 const float sc = a.scale ? a.scale[0] : 1.f;
                 const float d = used ? (a.dloss ? a.dloss[row] * sc : sc) : 0.f;
                 const float ml = there ? -a.lse[row] * kLog2e : 0.f;
                 const float q0 = a.eps / static_cast<float>(a.vocab), qy = 1.f - a.eps;
-#pragma unroll 1
-                for (int c = 0; c < n; c += 64) {
-                    unsigned char* b = next_box();
+                sweep(cols, release, [&](int c, float (&z)[32]) {
+                    if (c * 32 >= n) return;
+                    if ((c & 1) == 0) open_box();
+                    const int rel = at - c * 32;
+                    if (__any_sync(0xffffffffu, rel >= 0 && rel < 32))
+                        grads_of<true>(z, d, ml, q0, qy, rel);
+                    else
+                        grads_of<false>(z, d, ml, q0, qy, rel);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float z[32];
-                        tmem_ld32(z, cols + c + h * 32);
-                        tmem_ld_wait(z);
-                        const int rel = at - c - h * 32;
-                        if (__any_sync(0xffffffffu, rel >= 0 && rel < 32))
-                            grads_of<true>(z, d, ml, q0, qy, rel);
-                        else
-                            grads_of<false>(z, d, ml, q0, qy, rel);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            put16(b, lane, h * 4 + j,
-                                  used ? make_uint4(pack2<T>(z[8 * j], z[8 * j + 1]),
-                                                    pack2<T>(z[8 * j + 2], z[8 * j + 3]),
-                                                    pack2<T>(z[8 * j + 4], z[8 * j + 5]),
-                                                    pack2<T>(z[8 * j + 6], z[8 * j + 7]))
-                                       : make_uint4(0, 0, 0, 0));
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 v = pack8<T>(z, 8 * j, 1.f);
+                        put16(box, lane, (c & 1) * 4 + j, used ? v : make_uint4(0, 0, 0, 0));
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (row0 < a.rows) tma_store_2d(&maps.out, t.n0 + c, row0, b);
-                        bulk_commit();
-                    }
-                }
+                    if ((c & 1) == 1 || c * 32 + 32 >= n)
+                        close_box([&] {
+                            if (row0 < a.rows) tma_store_2d(&maps.out, n0 + (c & ~1) * 32, row0, box);
+                        });
+                });
             } else {
                 const bool f32 = t.weight ? a.w_f32 : a.x_partial;
                 const float sc = (t.weight || !a.x_partial) && a.scale ? a.scale[1] : 1.f;
-                const int n = min(kTileN, a.hidden - t.n0);
+                const int n = a.hidden - n0;
                 const bool there = row0 < (t.weight ? a.cols : a.rows);
-                if (f32) {
-#pragma unroll 1
-                    for (int c = 0; c < n; c += 32) {
-                        unsigned char* b = next_box();
-                        float z[32];
-                        tmem_ld32(z, cols + c);
-                        tmem_ld_wait(z);
+                if (f32)
+                    sweep(cols, release, [&](int c, float (&z)[32]) {
+                        if (c * 32 >= n) return;
+                        open_box();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            put16(b, lane, j,
+                            put16(box, lane, j,
                                   f2u4(make_float4(z[4 * j] * sc, z[4 * j + 1] * sc, z[4 * j + 2] * sc,
                                                    z[4 * j + 3] * sc)));
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
+                        close_box([&] {
                             if (there && t.weight)
-                                tma_add_2d(&maps.out2, t.n0 + c, a.col0 + row0, b);
+                                tma_add_2d(&maps.out2, n0 + c * 32, a.col0 + row0, box);
                             else if (there && a.x_add)
-                                tma_add_3d(&maps.out, t.n0 + c, row0, t.slice, b);
+                                tma_add_3d(&maps.out, n0 + c * 32, row0, t.slice, box);
                             else if (there)
-                                tma_store_3d(&maps.out, t.n0 + c, row0, t.slice, b);
-                            bulk_commit();
-                        }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < n; c += 64) {
-                        unsigned char* b = next_box();
+                                tma_store_3d(&maps.out, n0 + c * 32, row0, t.slice, box);
+                        });
+                    });
+                else
+                    sweep(cols, release, [&](int c, float (&z)[32]) {
+                        if (c * 32 >= n) return;
+                        if ((c & 1) == 0) open_box();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float z[32];
-                            tmem_ld32(z, cols + c + h * 32);
-                            tmem_ld_wait(z);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                put16(b, lane, h * 4 + j,
-                                      make_uint4(pack2<T>(z[8 * j] * sc, z[8 * j + 1] * sc),
-                                                 pack2<T>(z[8 * j + 2] * sc, z[8 * j + 3] * sc),
-                                                 pack2<T>(z[8 * j + 4] * sc, z[8 * j + 5] * sc),
-                                                 pack2<T>(z[8 * j + 6] * sc, z[8 * j + 7] * sc)));
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (there && t.weight)
-                                tma_store_2d(&maps.out2, t.n0 + c, a.col0 + row0, b);
-                            else if (there)
-                                tma_store_2d(&maps.out, t.n0 + c, row0, b);
-                            bulk_commit();
-                        }
-                    }
-                }
+                        for (int j = 0; j < 4; ++j) put16(box, lane, (c & 1) * 4 + j, pack8<T>(z, 8 * j, sc));
+                        if ((c & 1) == 1 || c * 32 + 32 >= n)
+                            close_box([&] {
+                                if (there && t.weight)
+                                    tma_store_2d(&maps.out2, n0 + (c & ~1) * 32, a.col0 + row0, box);
+                                else if (there)
+                                    tma_store_2d(&maps.out, n0 + (c & ~1) * 32, row0, box);
+                            });
+                    });
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty + acc, 0));
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -470,8 +481,9 @@ merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out, const 
     pdl_enter();
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= a.rows) return;
-    const float2* part = a.part + static_cast<int64_t>(row) * a.n_tiles;
-    const float* part_sum = a.part_sum + static_cast<int64_t>(row) * a.n_tiles;
+    const int parts = 2 * a.n_tiles;
+    const float2* part = a.part + static_cast<int64_t>(row) * parts;
+    const float* part_sum = a.part_sum + static_cast<int64_t>(row) * parts;
     float m = -INFINITY, l = 0.f, s = 0.f;
     auto merge = [&](float m2, float l2) {
         const float mm = fmaxf(m, m2);
@@ -483,7 +495,7 @@ merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out, const 
         }
     };
 #pragma unroll 4
-    for (int t = lane; t < a.n_tiles; t += 32) {
+    for (int t = lane; t < parts; t += 32) {
         const float2 p = part[t];
         merge(p.x, p.y);
         if (a.eps > 0.f) s += part_sum[t];
@@ -559,8 +571,25 @@ join_slices_kernel(T* __restrict__ dx, const float* __restrict__ part, const flo
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Pieces: g for `cols` vocabulary entries at a time, about 128 MB of it.
+// Pieces: g for `cols` vocabulary entries at a time, at most about 128 MB of it
+// (never fewer than 2048 entries).
 constexpr int64_t kPieceBytes = int64_t{128} << 20;
+constexpr int64_t kMaxSlices = 16;
+// The plan below counts time in K blocks of a pair's tile (256 x 256 x 64
+// products, about 0.25 us).  A launch costs about kLaunchBlocks of them until
+// its tiles run and until the last is written, a unit about one.
+constexpr int64_t kLaunchBlocks = 24;
+
+// Time of `a` units of length p and then `b` of length q, dealt to the pairs in turn.
+int64_t dealt(int64_t a, int64_t p, int64_t b, int64_t q) {
+    auto share = [](int64_t n, int64_t i) { return n > i ? (n - i - 1) / kPairs + 1 : 0; };
+    int64_t most = 0;
+    for (const int64_t i : {int64_t{0}, a % kPairs, (a + b) % kPairs}) {
+        const int64_t na = share(a, i);
+        most = std::max(most, na * p + (share(a + b, i) - na) * q);
+    }
+    return most;
+}
 
 // Sizes and workspace layout; they depend on the shapes alone.
 struct HeadPlan {
@@ -572,22 +601,38 @@ struct HeadPlan {
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
         n_tiles = ceil_div(vocab, kTileN);
         part = 0;
-        part_sum = round256(static_cast<size_t>(rows * n_tiles) * 8);
-        zy = part_sum + round256(static_cast<size_t>(rows * n_tiles) * 4);
+        part_sum = round256(static_cast<size_t>(rows * n_tiles) * 16);
+        zy = part_sum + round256(static_cast<size_t>(rows * n_tiles) * 8);
         const size_t fwd = zy + static_cast<size_t>(rows) * 4;
 
+        // The number of pieces, and of slices that cut dx's long K (the vocabulary) into units about
+        // as long as dweight's (K is the rows): those whose tiles deal out evenly to the pairs.
         const int64_t most = std::max<int64_t>(2048, kPieceBytes / 2 / rows / kTileN * kTileN);
-        pieces = ceil_div(vocab, most);
-        cols = ceil_div(ceil_div(vocab, pieces), kTileN) * kTileN;
-        pieces = ceil_div(vocab, cols);
+        const int64_t fewest = ceil_div(vocab, most);
         const int64_t m_tiles = ceil_div(rows, kTileM), h_tiles = ceil_div(hidden, kTileN);
-        const int64_t kb = ceil_div(std::min(cols, vocab), kBlockK);
-        // dx: K is cut so that one unit is a small part of a pair's share of the piece's products.
-        const int64_t work = m_tiles * h_tiles * kb + ceil_div(cols, kTileM) * h_tiles * ceil_div(rows, kBlockK);
-        slice_blocks = std::max<int64_t>(8, ceil_div(work, kPairs * 3));
-        slices = std::min<int64_t>(32, ceil_div(kb, slice_blocks));
-        slice_blocks = ceil_div(kb, slices);
-        slices = ceil_div(kb, slice_blocks);
+        const int64_t row_blocks = ceil_div(rows, kBlockK), h_blocks = ceil_div(hidden, kBlockK);
+        int64_t best = INT64_MAX;
+        for (int64_t n = fewest; n <= fewest + (fewest > 1 ? 4 : 0); ++n) {
+            const int64_t c = ceil_div(ceil_div(vocab, n), kTileN) * kTileN;
+            const int64_t np = ceil_div(vocab, c), kb = ceil_div(std::min(c, vocab), kBlockK);
+            const int64_t grad = ceil_div(m_tiles * (c / kTileN), kPairs) * (h_blocks + 1);
+            for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
+                const int64_t len = ceil_div(kb, s);
+                if (ceil_div(kb, len) != s) continue;
+                const int64_t out = dealt(s * m_tiles * h_tiles, len + 1 + (s > 1 || np > 1),
+                                          (c / kTileM) * h_tiles, row_blocks + 1);
+                // joining the slices: their bytes at about 1.7 MB for a K block's time
+                const int64_t join = s > 1 || np > 1 ? 12 + s * rows * hidden * 4 / 1700000 : 0;
+                const int64_t t = np * (grad + out + 2 * kLaunchBlocks) + join;
+                if (t < best) {
+                    best = t;
+                    cols = c;
+                    pieces = np;
+                    slices = s;
+                    slice_blocks = len;
+                }
+            }
+        }
         partial_dx = slices > 1 || pieces > 1;
         scale = 0;
         g = 256;

@@ -16,7 +16,7 @@ import ctypes
 import os
 
 from . import build as _build
-from .ls_ops import LS_F16, LS_F32, LS_OK, LsError, _nbytes, _ptr, _stream
+from .ls_ops import LS_F16, LS_F32, LS_OK, LsError, _stream
 
 LS_BF16 = 2
 
@@ -110,24 +110,33 @@ def _check(status: int):
 
 
 # --- argument checks --------------------------------------------------------
+# A call on a few rows takes less time on the GPU than its checks in Python
+# could: one comparison decides per tensor, and the reason is only looked for
+# when it fails.
+_codes = None
+
+
 def _storage_code(t) -> int:
-    import torch
+    global _codes
+    if _codes is None:
+        import torch
 
-    codes = {torch.float16: LS_F16, torch.bfloat16: LS_BF16, torch.float32: LS_F32}
-    if t.dtype not in codes:
+        _codes = {torch.float16: LS_F16, torch.bfloat16: LS_BF16, torch.float32: LS_F32}
+    code = _codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported storage dtype {t.dtype}; use float16, bfloat16 or float32")
-    return codes[t.dtype]
+    return code
 
 
-def _tensor(name: str, t, shape, dtype, optional: bool = False):
-    """A contiguous tensor of this shape and dtype on the current CUDA device."""
-    import torch
-
-    if t is None and optional:
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+def _tensor(name: str, t, shape, dtype, device: int) -> int:
+    """Address of a contiguous tensor of this shape and dtype on this CUDA device."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == device):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}") from None
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -135,29 +144,57 @@ def _tensor(name: str, t, shape, dtype, optional: bool = False):
         raise ValueError(f"{name} must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _workspace(t):
-    import torch
+def _optional(name: str, t, shape, dtype, device: int):
+    return None if t is None else _tensor(name, t, shape, dtype, device)
 
+
+def _workspace(t, device: int):
+    """(address, bytes) of the workspace."""
     if t is None:
-        return
-    if not isinstance(t, torch.Tensor) or not t.is_contiguous():
-        raise TypeError("workspace must be a contiguous tensor")
-    _tensor("workspace", t, t.shape, t.dtype)
+        return None, 0
+    return _tensor("workspace", t, getattr(t, "shape", None), getattr(t, "dtype", None),
+                   device), t.numel() * t.element_size()
 
 
 def _dims(name: str, t, n: int):
+    shape = getattr(t, "shape", None)
+    if shape is None:
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {len(shape)}")
+    return shape
+
+
+_have_cuda = False
+
+
+def _device() -> int:
+    """The current CUDA device, or -2 (no tensor's device) without one."""
+    global _have_cuda
     import torch
 
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
-    return t.shape
+    _have_cuda = _have_cuda or torch.cuda.is_available()
+    return torch.cuda.current_device() if _have_cuda else -2
+
+
+_raw_stream = None
+
+
+def _stream_of(stream, device: int):
+    """The stream's handle; None is torch's current stream on `device`."""
+    global _raw_stream
+    if stream is not None:
+        return _stream(stream)
+    if _raw_stream is None:
+        import torch
+
+        # the handle alone, where this torch offers it: a Stream object costs microseconds
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 # --- operators --------------------------------------------------------------
@@ -168,18 +205,19 @@ def ls_linear_cross_entropy_fwd(loss, lse, x, weight, target, label_smoothing: f
     The logits are not kept."""
     import torch
 
+    dev = _device()
     rows, hidden = _dims("x", x, 2)
     vocab = _dims("weight", weight, 2)[0]
-    _tensor("x", x, (rows, hidden), x.dtype)
-    _tensor("weight", weight, (vocab, hidden), x.dtype)
-    _tensor("target", target, (rows,), torch.int32)
-    _tensor("loss", loss, (rows,), torch.float32)
-    _tensor("lse", lse, (rows,), torch.float32, optional=True)
-    _workspace(workspace)
+    dtype, per_row = x.dtype, (rows,)
+    px = _tensor("x", x, (rows, hidden), dtype, dev)
+    pw = _tensor("weight", weight, (vocab, hidden), dtype, dev)
+    pt = _tensor("target", target, per_row, torch.int32, dev)
+    ploss = _tensor("loss", loss, per_row, torch.float32, dev)
+    plse = _optional("lse", lse, per_row, torch.float32, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_linear_cross_entropy_fwd(
-        _storage_code(x), _ptr(loss), _ptr(lse), _ptr(x), _ptr(weight), _ptr(target), rows, hidden,
-        vocab, label_smoothing, ignore_index, _ptr(workspace), _nbytes(workspace),
-        _stream(stream)))
+        _storage_code(x), ploss, plse, px, pw, pt, rows, hidden, vocab, label_smoothing,
+        ignore_index, ws, ws_bytes, _stream_of(stream, dev)))
 
 
 def ls_linear_cross_entropy_bwd(dx, dweight, x, weight, target, lse, dloss=None,
@@ -189,36 +227,38 @@ def ls_linear_cross_entropy_bwd(dx, dweight, x, weight, target, lse, dloss=None,
     storage dtype is written; a float32 dweight is added to."""
     import torch
 
+    dev = _device()
     rows, hidden = _dims("x", x, 2)
     vocab = _dims("weight", weight, 2)[0]
-    _tensor("x", x, (rows, hidden), x.dtype)
-    _tensor("weight", weight, (vocab, hidden), x.dtype)
-    _tensor("target", target, (rows,), torch.int32)
-    _tensor("lse", lse, (rows,), torch.float32)
-    _tensor("dloss", dloss, (rows,), torch.float32, optional=True)
-    _tensor("dx", dx, (rows, hidden), x.dtype, optional=True)
-    wcode = _storage_code(x)
+    dtype, per_row = x.dtype, (rows,)
+    px = _tensor("x", x, (rows, hidden), dtype, dev)
+    pw = _tensor("weight", weight, (vocab, hidden), dtype, dev)
+    pt = _tensor("target", target, per_row, torch.int32, dev)
+    plse = _tensor("lse", lse, per_row, torch.float32, dev)
+    pg = _optional("dloss", dloss, per_row, torch.float32, dev)
+    pdx = _optional("dx", dx, (rows, hidden), dtype, dev)
+    code = wcode = _storage_code(x)
+    pdw = None
     if dweight is not None:
         wcode = _storage_code(dweight)
-        _tensor("dweight", dweight, (vocab, hidden),
-                torch.float32 if wcode == LS_F32 else x.dtype)
-    _workspace(workspace)
+        pdw = _tensor("dweight", dweight, (vocab, hidden),
+                      torch.float32 if wcode == LS_F32 else dtype, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_linear_cross_entropy_bwd(
-        _storage_code(x), _ptr(dx), _ptr(dweight), wcode, _ptr(x), _ptr(weight), _ptr(target),
-        _ptr(lse), _ptr(dloss), rows, hidden, vocab, label_smoothing, ignore_index,
-        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        code, pdx, pdw, wcode, px, pw, pt, plse, pg, rows, hidden, vocab, label_smoothing,
+        ignore_index, ws, ws_bytes, _stream_of(stream, dev)))
 
 
-def _distill_shapes(logits, teacher_index, teacher_logits, teacher_lse):
+def _distill_inputs(logits, teacher_index, teacher_logits, teacher_lse, dev):
     import torch
 
     rows, vocab = _dims("logits", logits, 2)
     k = _dims("teacher_index", teacher_index, 2)[1]
-    _tensor("logits", logits, (rows, vocab), logits.dtype)
-    _tensor("teacher_index", teacher_index, (rows, k), torch.int32)
-    _tensor("teacher_logits", teacher_logits, (rows, k), logits.dtype)
-    _tensor("teacher_lse", teacher_lse, (rows,), torch.float32, optional=True)
-    return rows, vocab, k
+    dtype = logits.dtype
+    return (rows, vocab, k, _tensor("logits", logits, (rows, vocab), dtype, dev),
+            _tensor("teacher_index", teacher_index, (rows, k), torch.int32, dev),
+            _tensor("teacher_logits", teacher_logits, (rows, k), dtype, dev),
+            _optional("teacher_lse", teacher_lse, (rows,), torch.float32, dev))
 
 
 def ls_distill_topk_fwd(loss, lse, logits, teacher_index, teacher_logits, teacher_lse=None,
@@ -228,12 +268,13 @@ def ls_distill_topk_fwd(loss, lse, logits, teacher_index, teacher_logits, teache
     lse at that temperature (FP32 [rows] or None)."""
     import torch
 
-    rows, vocab, k = _distill_shapes(logits, teacher_index, teacher_logits, teacher_lse)
-    _tensor("loss", loss, (rows,), torch.float32)
-    _tensor("lse", lse, (rows,), torch.float32, optional=True)
-    _check(load().ls_distill_topk_fwd(
-        _storage_code(logits), _ptr(loss), _ptr(lse), _ptr(logits), _ptr(teacher_index),
-        _ptr(teacher_logits), _ptr(teacher_lse), rows, vocab, k, temperature, _stream(stream)))
+    dev = _device()
+    rows, vocab, k, pz, pi, pt, ptl = _distill_inputs(logits, teacher_index, teacher_logits,
+                                                      teacher_lse, dev)
+    ploss = _tensor("loss", loss, (rows,), torch.float32, dev)
+    plse = _optional("lse", lse, (rows,), torch.float32, dev)
+    _check(load().ls_distill_topk_fwd(_storage_code(logits), ploss, plse, pz, pi, pt, ptl, rows,
+                                      vocab, k, temperature, _stream_of(stream, dev)))
 
 
 def ls_distill_topk_bwd(dlogits, logits, teacher_index, teacher_logits, lse, teacher_lse=None,
@@ -241,27 +282,28 @@ def ls_distill_topk_bwd(dlogits, logits, teacher_index, teacher_logits, lse, tea
     """Gradient of the student's logits (dlogits may be logits)."""
     import torch
 
-    rows, vocab, k = _distill_shapes(logits, teacher_index, teacher_logits, teacher_lse)
-    _tensor("dlogits", dlogits, (rows, vocab), logits.dtype)
-    _tensor("lse", lse, (rows,), torch.float32)
-    _tensor("dloss", dloss, (rows,), torch.float32, optional=True)
-    _check(load().ls_distill_topk_bwd(
-        _storage_code(logits), _ptr(dlogits), _ptr(logits), _ptr(teacher_index),
-        _ptr(teacher_logits), _ptr(lse), _ptr(teacher_lse), _ptr(dloss), rows, vocab, k,
-        temperature, _stream(stream)))
+    dev = _device()
+    rows, vocab, k, pz, pi, pt, ptl = _distill_inputs(logits, teacher_index, teacher_logits,
+                                                      teacher_lse, dev)
+    pdz = _tensor("dlogits", dlogits, (rows, vocab), logits.dtype, dev)
+    plse = _tensor("lse", lse, (rows,), torch.float32, dev)
+    pg = _optional("dloss", dloss, (rows,), torch.float32, dev)
+    _check(load().ls_distill_topk_bwd(_storage_code(logits), pdz, pz, pi, pt, plse, ptl, pg, rows,
+                                      vocab, k, temperature, _stream_of(stream, dev)))
 
 
 def ls_embedding_lookup_fwd(y, tokens, table, scale: float = 1.0, stream=None):
     """y [tokens, hidden] = scale * table[tokens] for int32 tokens [tokens]."""
     import torch
 
+    dev = _device()
     vocab, hidden = _dims("table", table, 2)
     (n,) = _dims("tokens", tokens, 1)
-    _tensor("tokens", tokens, (n,), torch.int32)
-    _tensor("table", table, (vocab, hidden), table.dtype)
-    _tensor("y", y, (n, hidden), table.dtype)
-    _check(load().ls_embedding_lookup_fwd(_storage_code(table), _ptr(y), _ptr(tokens),
-                                          _ptr(table), n, hidden, vocab, scale, _stream(stream)))
+    pt = _tensor("tokens", tokens, (n,), torch.int32, dev)
+    pe = _tensor("table", table, (vocab, hidden), table.dtype, dev)
+    py = _tensor("y", y, (n, hidden), table.dtype, dev)
+    _check(load().ls_embedding_lookup_fwd(_storage_code(table), py, pt, pe, n, hidden, vocab, scale,
+                                          _stream_of(stream, dev)))
 
 
 def ls_embedding_lookup_bwd(d_table, dy, tokens, scale: float = 1.0, padding_id: int = -1,
@@ -270,13 +312,14 @@ def ls_embedding_lookup_bwd(d_table, dy, tokens, scale: float = 1.0, padding_id:
     written whole, or added to d_table with accumulate."""
     import torch
 
+    dev = _device()
     vocab, hidden = _dims("d_table", d_table, 2)
     (n,) = _dims("tokens", tokens, 1)
-    _tensor("d_table", d_table, (vocab, hidden), torch.float32)
     _dims("dy", dy, 2)
-    _tensor("dy", dy, (n, hidden), dy.dtype)
-    _tensor("tokens", tokens, (n,), torch.int32)
-    _workspace(workspace)
-    _check(load().ls_embedding_lookup_bwd(
-        _storage_code(dy), _ptr(d_table), _ptr(dy), _ptr(tokens), n, hidden, vocab, scale,
-        padding_id, int(bool(accumulate)), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    pd = _tensor("d_table", d_table, (vocab, hidden), torch.float32, dev)
+    pdy = _tensor("dy", dy, (n, hidden), dy.dtype, dev)
+    pt = _tensor("tokens", tokens, (n,), torch.int32, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(load().ls_embedding_lookup_bwd(_storage_code(dy), pd, pdy, pt, n, hidden, vocab, scale,
+                                          padding_id, int(bool(accumulate)), ws, ws_bytes,
+                                          _stream_of(stream, dev)))
