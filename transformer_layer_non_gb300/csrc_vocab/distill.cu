@@ -9,10 +9,15 @@
 //   dz_j    = dloss tau (p_j Q - sum_{e: index(e) = j} q_e),   Q = sum_e q_e
 //
 // The forward reads each row once (online maximum and sum per thread, merged
-// across the CTA and its cluster); the backward reads it once and writes it
-// once, from the forward's lse.  Both are bound by memory for rows of many
-// CTAs.  The k entries are a few hundred bytes: every CTA of a row computes
-// their q for itself.
+// across the CTA and its cluster), the backward reads it once and writes it
+// once, from the forward's lse: bound by memory when the rows fill the GPU.
+// Few rows are cut over more CTAs: a cluster of up to 8 per row in the
+// forward, any number of slices in the backward, which needs no merging.
+//
+// The k entries are a few hundred bytes.  Warp 0 works them out by shuffles
+// while the row's first vectors are on their way to all warps; with
+//   A = sum_e q_e (log q_e - z_index(e) / tau)   the forward's   loss = tau^2 (A + Q lse)
+// needs one barrier, the merging of the warps' sums.
 #include <math.h>
 
 #include "vec.cuh"
@@ -21,17 +26,17 @@
 namespace ls {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;  // vectors per thread in flight
-constexpr int kMaxK = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
+// Vectors per thread in flight.
+template <typename T> constexpr int unroll_fwd() { return sizeof(T) == 2 ? 4 : 2; }
+template <typename T> constexpr int unroll_bwd() { return sizeof(T) == 2 ? 8 : 4; }
 
 struct DistillArgs {
     int64_t vocab;
     int k;
     int nvec;       // vocab / 8
     int slice;      // vectors per CTA of a row
+    int table;      // backward: slots of the hash table, a power of two >= 2 k
     float tau;
     float c;        // log2(e) / tau
 };
@@ -46,100 +51,143 @@ __device__ __forceinline__ void merge(float& m, float& l, float m2, float l2, fl
     m = mm;
 }
 
-// Sum or maximum over the CTA, the same value in every thread; `sm` holds kWarps floats.
-__device__ __forceinline__ float cta_sum(float v, float* sm) {
-    v = group_sum<32>(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
+constexpr int kBatch = 4;  // entries per lane whose loads are in flight together
+
+// The student's logits at a lane's entries e0, e0 + 32, ... (0 where ix is -1 or the entry does not exist).
+template <typename T>
+__device__ __forceinline__ void gather(float (&f)[kBatch], const T* z, const int* ix, int e0, int k) {
+    T w[kBatch];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += sm[w];
-    return s;
-}
-__device__ __forceinline__ float cta_max(float v, float* sm) {
-    v = group_max<32>(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = sm[0];
+    for (int u = 0; u < kBatch; ++u) w[u] = z[max(0, ix[min(e0 + 32 * u, k - 1)])];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) s = fmaxf(s, sm[w]);
-    return s;
+    for (int u = 0; u < kBatch; ++u) f[u] = to_f32(w[u]);
 }
 
-// The row's entries: sm_logq[e] = log q_e (-inf where q is 0) and sm_ix[e]
-// (-1 where the entry is not valid).
+// log q of the row's entries: e = lane, lane + 32, ... of warp 0.  ix[e] gets
+// the index, -1 where the entry has q = 0; logq[e] the value.
 template <typename T>
-__device__ __forceinline__ void load_entries(float* sm_logq, int* sm_ix, float* sm_red,
-                                             const int32_t* index, const T* teacher,
-                                             const float* teacher_lse, int64_t row,
-                                             const DistillArgs& a) {
+__device__ __forceinline__ void load_entries(float* logq, int* ix, const int32_t* index,
+                                             const T* teacher, const float* teacher_lse,
+                                             int64_t row, const DistillArgs& a) {
+    const int lane = threadIdx.x & 31;
+    index += row * a.k;
+    teacher += row * a.k;
     float tmax = -INFINITY;
-    for (int e = threadIdx.x; e < a.k; e += kThreads) {
-        const int32_t j = index[row * a.k + e];
-        const bool there = j >= 0 && j < a.vocab;
-        const float t = there ? to_f32(teacher[row * a.k + e]) / a.tau : -INFINITY;
-        sm_ix[e] = there ? j : -1;
-        sm_logq[e] = t;
-        tmax = t != t ? INFINITY : fmaxf(tmax, t);  // a NaN reaches q either way
+    for (int e0 = lane; e0 < a.k; e0 += 32 * kBatch) {
+        int32_t j[kBatch];
+        T w[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int e = min(e0 + 32 * u, a.k - 1);
+            j[u] = index[e];
+            w[u] = teacher[e];
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int e = e0 + 32 * u;
+            if (e >= a.k) break;
+            const bool there = j[u] >= 0 && j[u] < a.vocab;
+            const float t = there ? to_f32(w[u]) / a.tau : -INFINITY;
+            logq[e] = t;
+            ix[e] = t == -INFINITY ? -1 : j[u];
+            tmax = t != t ? INFINITY : fmaxf(tmax, t);  // a NaN reaches q either way
+        }
     }
-    float base;
+    float base = 0.f;
     if (teacher_lse) {
         base = teacher_lse[row];
     } else {
-        tmax = cta_max(tmax, sm_red);
-        float s = 0.f;
-        if (tmax > -INFINITY)
-            for (int e = threadIdx.x; e < a.k; e += kThreads) s += expf(sm_logq[e] - tmax);
-        s = cta_sum(s, sm_red);
-        base = tmax > -INFINITY ? tmax + logf(s) : 0.f;
+        tmax = group_max<32>(tmax);
+        if (tmax > -INFINITY) {
+            float s = 0.f;
+            for (int e = lane; e < a.k; e += 32) s += expf(logq[e] - tmax);
+            base = tmax + logf(group_sum<32>(s));
+        }
     }
-    for (int e = threadIdx.x; e < a.k; e += kThreads)
-        if (sm_ix[e] >= 0 && sm_logq[e] != -INFINITY) sm_logq[e] -= base;
-    __syncthreads();
+    for (int e = lane; e < a.k; e += 32) {
+        logq[e] -= base;
+        if (expf(logq[e]) == 0.f) ix[e] = -1;
+    }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+// The vectors v, v + THREADS, ... of a row below hi, into registers.
+template <typename T, int U, int THREADS>
+__device__ __forceinline__ void load_batch(Raw8<T> (&r)[U], const T* z, int v0, int hi) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * THREADS;
+        if (v < hi) r[u] = load8<T>(z + static_cast<int64_t>(v) * kVec);
+    }
+}
+
+// Dynamic shared memory: logq [k], ix [k].
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS)
 distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
                    const T* __restrict__ logits, const int32_t* __restrict__ index,
                    const T* __restrict__ teacher, const float* __restrict__ teacher_lse,
-                   const __grid_constant__ DistillArgs a) {
-    __shared__ float sm_m[kWarps], sm_l[kWarps], sm_red[kWarps];
-    __shared__ float sm_logq[kMaxK];
-    __shared__ int sm_ix[kMaxK];
+                   const __grid_constant__ DistillArgs a, int cluster) {
+    constexpr int U = unroll_fwd<T>(), kWarps = THREADS / 32;
+    extern __shared__ float sm_k[];
+    __shared__ float sm_m[kWarps], sm_l[kWarps];
+    __shared__ float sm_part[2];
     pdl_enter();
-    const int64_t row = blockIdx.x;
+    const int64_t row = blockIdx.x / cluster;
+    const int rank = static_cast<int>(blockIdx.x - row * cluster);
     const T* z = logits + row * a.vocab;
-    float m = -INFINITY, l = 0.f;
-    for (int v0 = threadIdx.x; v0 < a.nvec; v0 += kThreads * kUnroll) {
-        Raw8<T> r[kUnroll];
+    const int lo = rank * a.slice, hi = min(a.nvec, lo + a.slice);
+    Raw8<T> r[U];
+    int v0 = lo + threadIdx.x;
+    load_batch<T, U, THREADS>(r, z, v0, hi);
+    float A = 0.f, Q = 0.f;
+    if (rank == 0 && threadIdx.x < 32) {
+        float* logq = sm_k;
+        int* ix = reinterpret_cast<int*>(sm_k + a.k);
+        load_entries(logq, ix, index, teacher, teacher_lse, row, a);
+        __syncwarp();
+        for (int e0 = threadIdx.x; e0 < a.k; e0 += 32 * kBatch) {
+            float f[kBatch];
+            gather(f, z, ix, e0, a.k);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int v = v0 + u * kThreads;
-            if (v < a.nvec) r[u] = load8<T>(z + static_cast<int64_t>(v) * kVec);
+            for (int u = 0; u < kBatch; ++u) {
+                const int e = e0 + 32 * u;
+                if (e >= a.k || ix[e] < 0) continue;
+                const float q = expf(logq[e]);
+                Q += q;
+                A += q * (logq[e] - f[u] / a.tau);
+            }
         }
+    }
+    float m = -INFINITY, l = 0.f, l1 = 0.f;
+    while (v0 < hi) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (v0 + u * kThreads >= a.nvec) break;
+        for (int u = 0; u < U; ++u) {
+            if (v0 + u * THREADS >= hi) break;
             float f[kVec];
             unpack(r[u], f);
             const float vm = vmax8(r[u]);
             if (vm > m) {
-                l *= exp2_approx((m - vm) * a.c);
+                const float c = exp2_approx((m - vm) * a.c);
+                l *= c;
+                l1 *= c;
                 m = vm;
             }
             const float mc = m * a.c;
             if (fabsf(mc) < INFINITY) {
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) l += exp2_approx(fmaf(f[j], a.c, -mc));
+                for (int j = 0; j < kVec; j += 2) {
+                    l += exp2_approx(fmaf(f[j], a.c, -mc));
+                    l1 += exp2_approx(fmaf(f[j + 1], a.c, -mc));
+                }
             } else if (m != -INFINITY) {  // m is finite and m c is not (FP32's lowest values as a mask)
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) l += exp2_approx((f[j] - m) * a.c);
             }
         }
+        v0 += U * THREADS;
+        load_batch<T, U, THREADS>(r, z, v0, hi);
     }
+    l += l1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
@@ -150,52 +198,115 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
         sm_m[threadIdx.x >> 5] = m;
         sm_l[threadIdx.x >> 5] = l;
     }
-    load_entries(sm_logq, sm_ix, sm_red, index, teacher, teacher_lse, row, a);
+    __syncthreads();
+    if (threadIdx.x >= 32 && cluster == 1) return;
     m = sm_m[0];
     l = sm_l[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) merge(m, l, sm_m[w], sm_l[w], a.c);
-    const float lse = m / a.tau + logf(l);
-    float s = 0.f;
-    for (int e = threadIdx.x; e < a.k; e += kThreads) {
-        const float lq = sm_logq[e];
-        const float q = expf(lq);
-        if (sm_ix[e] < 0 || q == 0.f) continue;
-        s += q * (lq - (to_f32(z[sm_ix[e]]) / a.tau - lse));
+    if (cluster > 1) {
+        if (threadIdx.x == 0) {
+            sm_part[0] = m;
+            sm_part[1] = l;
+        }
+        cluster_sync();
+        if (rank == 0)
+            for (int c = 1; c < cluster; ++c) {
+                const uint32_t p = map_rank(sm_part, c);
+                merge(m, l, ld_cluster(p), ld_cluster(p + 4), a.c);
+            }
+        cluster_sync();  // a CTA's shared memory lives until the first one has read it
+        if (rank != 0 || threadIdx.x >= 32) return;
     }
-    s = cta_sum(s, sm_red);
+    A = group_sum<32>(A);
+    Q = group_sum<32>(Q);
     if (threadIdx.x == 0) {
-        loss[row] = a.tau * a.tau * s;
+        const float lse = m / a.tau + logf(l);
+        loss[row] = Q == 0.f ? 0.f : a.tau * a.tau * (A + Q * lse);
         if (lse_out) lse_out[row] = lse;
     }
 }
 
-// CTA (row, slice): the slice's vectors of the row, then the entries that fall into it.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+// CTA (row, slice): the slice's vectors of the row, then the entries that fall
+// into it.  Rows run from the last to the first: the forward, which runs the
+// other way, has left the last ones in L2.
+// Dynamic shared memory: q, z, ix, slot [k]; hash table, twice [table].
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ index,
                    const T* __restrict__ teacher, const float* __restrict__ lse,
                    const float* __restrict__ teacher_lse, const float* __restrict__ dloss,
                    const __grid_constant__ DistillArgs a) {
-    __shared__ float sm_red[kWarps];
-    __shared__ float sm_q[kMaxK], sm_z[kMaxK];
-    __shared__ int sm_ix[kMaxK];
+    constexpr int U = unroll_bwd<T>();
+    extern __shared__ float sm_k[];
+    __shared__ float sm_sum;
+    __shared__ int sm_any_twice;
+    float* sm_q = sm_k;
+    float* sm_z = sm_k + a.k;
+    int* sm_ix = reinterpret_cast<int*>(sm_k + 2 * a.k);
+    int* sm_slot = sm_ix + a.k;
+    int* sm_table = sm_slot + a.k;
+    int* sm_twice = sm_table + a.table;  // [table]: the slot's index came more than once
     pdl_enter();
-    const int64_t row = blockIdx.x;
+    const int64_t row = gridDim.x - 1 - blockIdx.x;
     const T* z = logits + row * a.vocab;
     T* dz = dlogits + row * a.vocab;
-    load_entries(sm_q, sm_ix, sm_red, index, teacher, teacher_lse, row, a);
-    float Q = 0.f;
-    for (int e = threadIdx.x; e < a.k; e += kThreads) {
-        const float q = sm_ix[e] >= 0 ? expf(sm_q[e]) : 0.f;
-        sm_q[e] = q;
-        sm_z[e] = q != 0.f ? to_f32(z[sm_ix[e]]) : 0.f;  // before the slice is overwritten (in place)
-        Q += q;
-    }
-    Q = cta_sum(Q, sm_red);  // its barriers also put every gather before the first store
-    const float g = a.tau * (dloss ? dloss[row] : 1.f);
-    const float gq = g * Q;
+    const int lo = blockIdx.y * a.slice, hi = min(a.nvec, lo + a.slice);
+    Raw8<T> r[U];
+    int v0 = lo + threadIdx.x;
+    load_batch<T, U, THREADS>(r, z, v0, hi);
     const float row_lse = lse[row];
+    const float g = a.tau * (dloss ? dloss[row] : 1.f);
+    if (threadIdx.x < 32) {
+        for (int t = threadIdx.x; t < a.table; t += 32) {
+            sm_table[t] = -1;
+            sm_twice[t] = 0;
+        }
+        load_entries(sm_q, sm_ix, index, teacher, teacher_lse, row, a);
+        __syncwarp();
+        float Q = 0.f;
+        bool any_twice = false;
+        for (int e0 = threadIdx.x; e0 < a.k; e0 += 32 * kBatch) {
+            // The entries' logits are read before the slice is overwritten (in place).
+            float f[kBatch];
+            gather(f, z, sm_ix, e0, a.k);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int e = e0 + 32 * u;
+                if (e >= a.k) continue;
+                const int j = sm_ix[e];
+                const float q = j >= 0 ? expf(sm_q[e]) : 0.f;
+                Q += q;
+                sm_q[e] = q;
+                sm_z[e] = f[u];
+                // Only this slice's entries matter from here on.
+                if (j < 0 || j / kVec < lo || j / kVec >= hi) {
+                    sm_ix[e] = -1;
+                    continue;
+                }
+                uint32_t h = ((static_cast<uint32_t>(j) * 2654435761u) >> 16) & (a.table - 1);
+                for (;; h = (h + 1) & (a.table - 1)) {  // at most k of the table's 2 k slots are taken
+                    const int was = atomicCAS(sm_table + h, -1, j);
+                    if (was == -1) break;
+                    if (was == j) {
+                        sm_twice[h] = 1;
+                        any_twice = true;
+                        break;
+                    }
+                }
+                sm_slot[e] = h;
+            }
+        }
+        Q = group_sum<32>(Q);
+        any_twice = __any_sync(0xffffffffu, any_twice);
+        if (threadIdx.x == 0) {
+            sm_sum = Q;
+            sm_any_twice = any_twice;
+        }
+    }
+    __syncthreads();  // Q is there, and every gather of an entry's logit before the first store
+    const float Q = sm_sum;
+    const float gq = g * Q;
     const bool some = Q != 0.f;
     // exp(z / tau - lse) by one FMA, unless the FMA's terms overflow (FP32's
     // lowest values in a whole row).
@@ -204,80 +315,116 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
     auto prob = [&](float f) {
         return exp2_approx(tame ? fmaf(f, a.c, -ll) : (f / a.tau - row_lse) * kLog2e);
     };
-    const int lo = blockIdx.y * a.slice;
-    const int hi = min(a.nvec, lo + a.slice);
-    for (int v0 = lo + threadIdx.x; v0 < hi; v0 += kThreads * kUnroll) {
-        Raw8<T> r[kUnroll];
+    while (v0 < hi) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int v = v0 + u * kThreads;
-            if (v < hi && some) r[u] = load8<T>(z + static_cast<int64_t>(v) * kVec);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int v = v0 + u * kThreads;
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * THREADS;
             if (v >= hi) break;
             float o[kVec];
             if (some) {
                 float f[kVec];
                 unpack(r[u], f);
+                if (tame) {
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) o[j] = gq * prob(f[j]);
+                    for (int j = 0; j < kVec; ++j) o[j] = gq * exp2_approx(fmaf(f[j], a.c, -ll));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) o[j] = gq * prob(f[j]);
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) o[j] = 0.f;
             }
             store8f<T>(dz + static_cast<int64_t>(v) * kVec, o);
         }
+        v0 += U * THREADS;
+        load_batch<T, U, THREADS>(r, z, v0, hi);
     }
     if (!some) return;
     __syncthreads();
-    // The entries' columns again, from the FP32 values.  The first of several
-    // entries with one index writes it, with their q added in entry order.
-    for (int e = threadIdx.x; e < a.k; e += kThreads) {
-        const int j = sm_ix[e];
-        if (j < 0 || j / kVec < lo || j / kVec >= hi || sm_q[e] == 0.f) continue;
-        float q = 0.f;
-        bool first = true;
-        for (int f = 0; f < a.k; ++f) {
-            if (sm_ix[f] != j || sm_q[f] == 0.f) continue;
-            if (f < e) {
-                first = false;
-                break;
+    // The entries' columns again, from the FP32 values.  Where a row holds an
+    // index more than once, its first entry writes the sum of their q, added in
+    // entry order by the whole warp.
+    const int lane = threadIdx.x & 31;
+    for (int e0 = threadIdx.x - lane; e0 < a.k; e0 += THREADS) {
+        const int e = e0 + lane;
+        const int j = e < a.k ? sm_ix[e] : -1;
+        bool mine = j >= 0;
+        float q = mine ? sm_q[e] : 0.f;
+        unsigned twice = __ballot_sync(0xffffffffu, sm_any_twice && mine && sm_twice[sm_slot[e]]);
+        for (; twice; twice &= twice - 1) {
+            const int l = __ffs(twice) - 1;
+            const int jl = __shfl_sync(0xffffffffu, j, l);
+            float sum = 0.f;
+            bool first = true;
+            for (int f0 = 0; f0 < a.k && first; f0 += 32) {
+                unsigned same = __ballot_sync(0xffffffffu, f0 + lane < a.k && sm_ix[f0 + lane] == jl);
+                if (same && f0 + __ffs(same) - 1 < e0 + l) first = false;
+                for (; same && first; same &= same - 1) sum += sm_q[f0 + __ffs(same) - 1];
             }
-            q += sm_q[f];
+            if (lane == l) {
+                q = sum;
+                mine = first;
+            }
         }
-        if (first) dz[j] = from_f32<T>(g * (Q * prob(sm_z[e]) - q));
+        if (mine) dz[j] = from_f32<T>(g * (Q * prob(sm_z[e]) - q));
     }
 }
 
-DistillArgs make_args(const DistillShape& sh) {
+// A row is cut into `parts` slices.
+DistillArgs make_args(const DistillShape& sh, int parts) {
     DistillArgs a;
     a.vocab = sh.vocab;
     a.k = sh.k;
     a.nvec = static_cast<int>(sh.vocab / kVec);
-    a.slice = a.nvec;
+    a.slice = (a.nvec + parts - 1) / parts;
+    a.table = 2;
+    while (a.table < 2 * sh.k) a.table *= 2;
     a.tau = sh.tau;
     a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(sh.tau));
     return a;
+}
+
+// Threads of a CTA: 128, and 256 for slices of 64K values or more (measured at
+// 4096 x 30528 FP16: forward 47 us with 128, 51 with 256; 2047 x 131072 BF16: 104 and 92).
+int threads_of(const DistillArgs& a) { return a.slice >= 8192 ? 256 : 128; }
+
+// Slices of a row, for about `ctas` CTAs in all; none below two vectors for a thread.
+int parts_of(const DistillShape& sh, int ctas, int most) {
+    const int64_t want = ctas / sh.rows;
+    const int64_t can = sh.vocab / kVec / 256;
+    int64_t n = 1;
+    while (2 * n <= want && 2 * n <= can && 2 * n <= most) n *= 2;
+    return static_cast<int>(n);
 }
 
 template <typename T>
 cudaError_t fwd(float* loss, float* lse, const void* logits, const int32_t* index,
                 const void* teacher, const float* teacher_lse, const DistillShape& sh,
                 cudaStream_t s) {
-    return launch_pdl(distill_fwd_kernel<T>, dim3(static_cast<unsigned>(sh.rows)), dim3(kThreads),
-                      0, s, loss, lse, static_cast<const T*>(logits), index,
-                      static_cast<const T*>(teacher), teacher_lse, make_args(sh));
+    // A grid's x extent ends at 2^31 - 1 CTAs.
+    const int cluster = sh.rows > (1 << 20) ? 1 : parts_of(sh, 608, 8);
+    const DistillArgs a = make_args(sh, cluster);
+    const int threads = threads_of(a);
+    return launch_cluster(threads == 128 ? distill_fwd_kernel<T, 128> : distill_fwd_kernel<T, 256>,
+                          dim3(static_cast<unsigned>(sh.rows * cluster)), cluster, dim3(threads),
+                          static_cast<size_t>(sh.k) * 8, s, loss, lse, static_cast<const T*>(logits),
+                          index, static_cast<const T*>(teacher), teacher_lse, a, cluster);
 }
 
 template <typename T>
 cudaError_t bwd(void* dlogits, const void* logits, const int32_t* index, const void* teacher,
                 const float* lse, const float* teacher_lse, const float* dloss,
                 const DistillShape& sh, cudaStream_t s) {
-    return launch_pdl(distill_bwd_kernel<T>, dim3(static_cast<unsigned>(sh.rows)), dim3(kThreads),
-                      0, s, static_cast<T*>(dlogits), static_cast<const T*>(logits), index,
-                      static_cast<const T*>(teacher), lse, teacher_lse, dloss, make_args(sh));
+    // Each slice reads and writes its own columns alone, in place too.
+    const int parts = parts_of(sh, 1216, 64);
+    const DistillArgs a = make_args(sh, parts);
+    const int threads = threads_of(a);
+    return launch_pdl(threads == 128 ? distill_bwd_kernel<T, 128> : distill_bwd_kernel<T, 256>,
+                      dim3(static_cast<unsigned>(sh.rows), static_cast<unsigned>(parts)),
+                      dim3(threads), static_cast<size_t>(4 * sh.k + 2 * a.table) * 4, s,
+                      static_cast<T*>(dlogits), static_cast<const T*>(logits), index,
+                      static_cast<const T*>(teacher), lse, teacher_lse, dloss, a);
 }
 
 }  // namespace
