@@ -28,7 +28,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 // Vectors per thread in flight.
-template <typename T> constexpr int unroll_fwd() { return sizeof(T) == 2 ? 4 : 2; }
+template <typename T> constexpr int unroll_fwd() { return sizeof(T) == 2 ? 6 : 3; }
 template <typename T> constexpr int unroll_bwd() { return sizeof(T) == 2 ? 8 : 4; }
 
 struct DistillArgs {
@@ -110,19 +110,19 @@ __device__ __forceinline__ void load_entries(float* logq, int* ix, const int32_t
     }
 }
 
-// The vectors v, v + THREADS, ... of a row below hi, into registers.
+// The vectors v, v + THREADS, ... of a row below hi, into registers; -inf behind it.
 template <typename T, int U, int THREADS>
 __device__ __forceinline__ void load_batch(Raw8<T> (&r)[U], const T* z, int v0, int hi) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int v = v0 + u * THREADS;
-        if (v < hi) r[u] = load8<T>(z + static_cast<int64_t>(v) * kVec);
+        r[u] = v < hi ? load8<T>(z + static_cast<int64_t>(v) * kVec) : lowest8<T>();
     }
 }
 
 // Dynamic shared memory: logq [k], ix [k].
 template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1536 / THREADS)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
                    const T* __restrict__ logits, const int32_t* __restrict__ index,
                    const T* __restrict__ teacher, const float* __restrict__ teacher_lse,
@@ -158,36 +158,41 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
             }
         }
     }
-    float m = -INFINITY, l = 0.f, l1 = 0.f;
-    while (v0 < hi) {
+    float m = -INFINITY;
+    float2 l2 = make_float2(0.f, 0.f);
+    const float2 cc = make_float2(a.c, a.c);
+    for (; v0 < hi; v0 += U * THREADS) {
+        Raw8<T> top = r[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) top = vmax(top, r[u]);
+        const float bm = vmax8(top);
+        if (bm > m) {  // rescale the running sum to the new maximum
+            const float c = exp2_approx((m - bm) * a.c);
+            l2 = mul2(l2, make_float2(c, c));
+            m = bm;
+        }
+        const float mc = m * a.c;
+        const bool tame = fabsf(mc) < INFINITY;
+        const float2 mm = make_float2(-mc, -mc);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (v0 + u * THREADS >= hi) break;
             float f[kVec];
             unpack(r[u], f);
-            const float vm = vmax8(r[u]);
-            if (vm > m) {
-                const float c = exp2_approx((m - vm) * a.c);
-                l *= c;
-                l1 *= c;
-                m = vm;
-            }
-            const float mc = m * a.c;
-            if (fabsf(mc) < INFINITY) {
+            // The next vector into this one's place at once: U loads stay in flight.
+            const int next = v0 + (U + u) * THREADS;
+            r[u] = next < hi ? load8<T>(z + static_cast<int64_t>(next) * kVec) : lowest8<T>();
+            if (tame) {
 #pragma unroll
                 for (int j = 0; j < kVec; j += 2) {
-                    l += exp2_approx(fmaf(f[j], a.c, -mc));
-                    l1 += exp2_approx(fmaf(f[j + 1], a.c, -mc));
+                    const float2 t = fma2(make_float2(f[j], f[j + 1]), cc, mm);
+                    l2 = add2(l2, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
                 }
             } else if (m != -INFINITY) {  // m is finite and m c is not (FP32's lowest values as a mask)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) l += exp2_approx((f[j] - m) * a.c);
+                for (int j = 0; j < kVec; ++j) l2.x += exp2_approx((f[j] - m) * a.c);
             }
         }
-        v0 += U * THREADS;
-        load_batch<T, U, THREADS>(r, z, v0, hi);
     }
-    l += l1;
+    float l = l2.x + l2.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
@@ -315,30 +320,34 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
     auto prob = [&](float f) {
         return exp2_approx(tame ? fmaf(f, a.c, -ll) : (f / a.tau - row_lse) * kLog2e);
     };
-    while (v0 < hi) {
+    if (some && tame) {
+        const float2 cc = make_float2(a.c, a.c), mm = make_float2(-ll, -ll), gg = make_float2(gq, gq);
+        for (; v0 < hi; v0 += U * THREADS) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = v0 + u * THREADS;
-            if (v >= hi) break;
-            float o[kVec];
-            if (some) {
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + u * THREADS;
+                if (v >= hi) break;
                 float f[kVec];
                 unpack(r[u], f);
-                if (tame) {
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) o[j] = gq * exp2_approx(fmaf(f[j], a.c, -ll));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) o[j] = gq * prob(f[j]);
+                for (int j = 0; j < kVec; j += 2) {
+                    const float2 t = fma2(make_float2(f[j], f[j + 1]), cc, mm);
+                    const float2 o = mul2(make_float2(exp2_approx(t.x), exp2_approx(t.y)), gg);
+                    f[j] = o.x;
+                    f[j + 1] = o.y;
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) o[j] = 0.f;
+                store8f<T>(dz + static_cast<int64_t>(v) * kVec, f);
             }
-            store8f<T>(dz + static_cast<int64_t>(v) * kVec, o);
+            load_batch<T, U, THREADS>(r, z, v0 + U * THREADS, hi);
         }
-        v0 += U * THREADS;
-        load_batch<T, U, THREADS>(r, z, v0, hi);
+    } else {
+#pragma unroll 1
+        for (; v0 < hi; v0 += THREADS) {
+            float f[kVec];
+            load8f<T>(z + static_cast<int64_t>(v0) * kVec, f);
+            for (int j = 0; j < kVec; ++j) f[j] = some ? gq * prob(f[j]) : 0.f;
+            store8f<T>(dz + static_cast<int64_t>(v0) * kVec, f);
+        }
     }
     if (!some) return;
     __syncthreads();

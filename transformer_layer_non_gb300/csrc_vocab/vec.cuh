@@ -39,11 +39,45 @@ template <> __device__ __forceinline__ Raw8<bf16> pack<bf16>(const float (&f)[8]
 template <> __device__ __forceinline__ Raw8<bf16> zero8<bf16>() {
     return Raw8<bf16>{make_uint4(0, 0, 0, 0)};
 }
+// Element-wise maximum of two vectors.
+__device__ __forceinline__ uint32_t hmax2u(uint32_t a, uint32_t b) {
+    const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t bmax2u(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m =
+        __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ Raw8<__half> vmax(const Raw8<__half>& a, const Raw8<__half>& b) {
+    return Raw8<__half>{make_uint4(hmax2u(a.v.x, b.v.x), hmax2u(a.v.y, b.v.y),
+                                   hmax2u(a.v.z, b.v.z), hmax2u(a.v.w, b.v.w))};
+}
+__device__ __forceinline__ Raw8<bf16> vmax(const Raw8<bf16>& a, const Raw8<bf16>& b) {
+    return Raw8<bf16>{make_uint4(bmax2u(a.v.x, b.v.x), bmax2u(a.v.y, b.v.y),
+                                 bmax2u(a.v.z, b.v.z), bmax2u(a.v.w, b.v.w))};
+}
+__device__ __forceinline__ Raw8<float> vmax(const Raw8<float>& a, const Raw8<float>& b) {
+    return Raw8<float>{make_float4(fmaxf(a.a.x, b.a.x), fmaxf(a.a.y, b.a.y), fmaxf(a.a.z, b.a.z),
+                                   fmaxf(a.a.w, b.a.w)),
+                       make_float4(fmaxf(a.b.x, b.b.x), fmaxf(a.b.y, b.b.y), fmaxf(a.b.z, b.b.z),
+                                   fmaxf(a.b.w, b.b.w))};
+}
 __device__ __forceinline__ float vmax8(const Raw8<bf16>& r) {
-    float f[8];
-    unpack(r, f);
-    return fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])),
-                 fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+    const float2 m = b2f(bmax2u(bmax2u(r.v.x, r.v.y), bmax2u(r.v.z, r.v.w)));
+    return fmaxf(m.x, m.y);
+}
+// A vector of -inf.
+template <typename T> __device__ __forceinline__ Raw8<T> lowest8();
+template <> __device__ __forceinline__ Raw8<__half> lowest8<__half>() {
+    return Raw8<__half>{make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u)};
+}
+template <> __device__ __forceinline__ Raw8<bf16> lowest8<bf16>() {
+    return Raw8<bf16>{make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)};
+}
+template <> __device__ __forceinline__ Raw8<float> lowest8<float>() {
+    const float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    return Raw8<float>{f, f};
 }
 
 // launch_pdl with thread-block clusters of `cluster` CTAs along x.
