@@ -68,9 +68,9 @@ ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, c
  *   g[i,j]       = dloss[i] * (exp(z[i,j] - lse[i]) - (1 - eps) * [j == target[i]] - eps / vocab)
  *   dx[i,c]      = sum_j g[i,j] * weight[j,c]
  *   dweight[j,c] = sum_i g[i,j] * x[i,c]
- * g is rounded once to the storage dtype for the two products (FP16: scaled
- * by a power of two to the format's upper range first, so that probabilities
- * down to 2^-38 of the largest dloss survive); the sums are FP32.
+ * g is rounded once to the storage dtype for the two products, after a
+ * division by max|dloss| (1 - eps) which the FP32 sums undo (FP16 keeps
+ * values down to 2^-38 of the largest dloss that way).
  * dloss: FP32 [rows] or NULL for 1.  Rows with an ignored target contribute
  * nothing and get a zero dx.
  * dx: [rows, hidden] in the storage dtype, written, or NULL.

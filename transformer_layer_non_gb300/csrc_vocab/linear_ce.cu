@@ -20,9 +20,12 @@
 // Operands of which M or N is the contiguous axis (W in g W; g and x in g^T x)
 // are read as they lie in memory: the matrix descriptors take either order.
 //
-// FP16 has no exponent range for dloss * p (1/rows times 1/vocab), so g is
-// stored as g * 2^s with 2^s max|dloss| <= 2^14 and the factor is taken out of
-// the FP32 sums again; BF16 has FP32's range and s = 0.
+// g is stored divided by D = max|dloss| (1 - eps), and the FP32 sums are
+// multiplied by D again.  The entries at the targets, which carry most of a
+// row's gradient, are then near -1, which both formats hold exactly; dloss
+// itself (1/rows, say) would be off by the same half step in every row, and
+// with it the whole gradient.  FP16, which has no exponent range for 1/rows
+// times 1/vocab, also gets a factor of 2^14.
 #include <cuda.h>
 #include <math.h>
 
@@ -58,6 +61,7 @@ struct HeadArgs {
     int rows, vocab, hidden;
     int col0, cols;        // this piece of the vocabulary
     int m_tiles, n_tiles;  // kStats, kGrad: rows x piece
+    int row_box;           // rows of the copies of x and g with rows as M: 128, or all where there are fewer
     int k_blocks;
     float eps;
     int32_t ignore_index;
@@ -67,14 +71,29 @@ struct HeadArgs {
     int x_k_blocks, slice_blocks, w_k_blocks;
     bool x_partial, x_add, w_f32;
     // kStats
-    float2* part;          // [rows][2 n_tiles]: maximum, sum of exponentials of a warp's columns
-    float* part_sum;       // [rows][2 n_tiles]
+    int parts;             // partial statistics of a row: two for each tile, or one for each CTA
+    float2* part;          // [rows][parts]: maximum, sum of exponentials
+    float* part_sum;       // [rows][parts]: sum
     float* zy;             // [rows]
     const int32_t* target;
     const float* lse;
     const float* dloss;
-    const float* scale;    // 2^s, 2^-s; NULL for 1
+    float* scale;          // [2] in the workspace: g's factor and its inverse, if dloss is given
+    float2 fixed_scale;    // the same if not
+    bool find_scale;       // kGrad: from dloss, by every CTA (and left in `scale`)
 };
+
+// g's factor and its inverse for the largest finite |dloss|.
+template <typename T> __host__ __device__ __forceinline__ float2 scale_for(float largest, float eps) {
+    const float up = std::is_same<T, __half>::value ? 16384.f : 1.f;
+    // 1 - eps is left out where p / (1 - eps) would leave FP16's range.
+    float d = largest * (eps <= 0.5f ? 1.f - eps : 1.f);
+    if (!(d > 0x1p-100f)) d = largest > 0.f ? 0x1p-100f : 1.f;
+    return make_float2(up / d, d / up);
+}
+__device__ __forceinline__ float2 scale_of(const HeadArgs& a) {
+    return a.dloss ? make_float2(a.scale[0], a.scale[1]) : a.fixed_scale;
+}
 
 struct HeadMaps {
     CUtensorMap a, b;    // kStats, kGrad: x, W;  kOut: g, W for dx
@@ -226,6 +245,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
+    __shared__ float largest[kEpilogueWarps];
     // The swizzle's pattern repeats every 1024 bytes of the address.
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -262,20 +282,28 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
         for (int u = pair; u < units; u += pairs) {
             const Unit t = unit_of<MODE>(u, a);
             const int m = t.m0 + static_cast<int>(rank) * 128, n = t.n0 + static_cast<int>(rank) * 128;
+            // Rows behind the last one are not copied (filling them with zeros costs a copy of 1 row
+            // 10 us in 40): what the shared memory holds there reaches rows of the accumulator that
+            // nothing reads.
+            auto a_bytes = [&](int first) -> uint32_t {
+                return t.weight ? kOperandBytes : first < a.rows ? static_cast<uint32_t>(a.row_box) * 128 : 0;
+            };
+            const uint32_t bytes = 2 * kOperandBytes + a_bytes(t.m0) + a_bytes(t.m0 + 128);  // of both CTAs
+            const bool has_a = a_bytes(m) > 0;
             for (int kb = 0; kb < t.kbs; ++kb, ++it) {
                 const uint32_t s = it % kStages;
                 if (!wait_bar(empty + s, ((it / kStages) & 1) ^ 1, &dead)) break;
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * kStageBytes);  // both CTAs' copies
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
                     const uint32_t bar = map_rank(full + s, 0);
                     unsigned char* pa = smem + s * kStageBytes;
                     unsigned char* pb = pa + kOperandBytes;
                     const int k = (t.kb0 + kb) * kBlockK;
                     if constexpr (MODE != kOut) {
-                        tma_load_2d(pa, &maps.a, k, m, bar);
+                        if (has_a) tma_load_2d(pa, &maps.a, k, m, bar);
                         tma_load_2d(pb, &maps.b, k, a.col0 + n, bar);
                     } else if (!t.weight) {
-                        tma_load_2d(pa, &maps.a, k, m, bar);
+                        if (has_a) tma_load_2d(pa, &maps.a, k, m, bar);
                         tma_load_2d(pb, &maps.b, n, a.col0 + k, bar);
                         tma_load_2d(pb + kOperandBytes / 2, &maps.b, n + 64, a.col0 + k, bar);
                     } else {
@@ -347,6 +375,31 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
         unsigned char* box = smem + kStages * kStageBytes + (warp - 2) * kStoreBytes;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kWarpColumns;
         uint32_t tile = 0;
+        float2 scale = make_float2(1.f, 1.f);
+        if constexpr (MODE == kGrad) {
+            if (a.find_scale) {  // while the first tile's products run
+                const int id = threadIdx.x - 64;
+                float m = 0.f;
+                for (int i = id; i < a.rows; i += 32 * kEpilogueWarps) {
+                    const float d = fabsf(a.dloss[i]);
+                    if (d < INFINITY) m = fmaxf(m, d);
+                }
+                m = group_max<32>(m);
+                if (lane == 0) largest[warp - 2] = m;
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
+                m = largest[0];
+#pragma unroll
+                for (int w = 1; w < kEpilogueWarps; ++w) m = fmaxf(m, largest[w]);
+                scale = scale_for<T>(m, a.eps);
+                if (blockIdx.x == 0 && id == 0) {
+                    a.scale[0] = scale.x;
+                    a.scale[1] = scale.y;
+                }
+            } else {
+                scale = scale_of(a);
+            }
+        }
+        if constexpr (MODE == kOut) scale = scale_of(a);
         for (int u = pair; u < units; u += pairs, ++tile) {
             const Unit t = unit_of<MODE>(u, a);
             const uint32_t acc = tile & 1;
@@ -394,7 +447,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         add_stats<true, SUM>(z, n - c * 32, m, l, s);
                 });
                 if (row < a.rows) {
-                    const int64_t o = static_cast<int64_t>(row) * (2 * a.n_tiles) + n0 / kWarpColumns;
+                    const int64_t o = static_cast<int64_t>(row) * a.parts + n0 / kWarpColumns;
                     a.part[o] = make_float2(m, l.x + l.y);
                     if constexpr (SUM) a.part_sum[o] = s.x + s.y;
                 }
@@ -404,8 +457,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 const int32_t y = there ? a.target[row] : -1;
                 const bool used = there && used_target(y, a);
                 const int at = used ? y - a.col0 - n0 : -1;
-                const float sc = a.scale ? a.scale[0] : 1.f;
-                const float d = used ? (a.dloss ? a.dloss[row] * sc : sc) : 0.f;
+                const float d = used ? (a.dloss ? a.dloss[row] * scale.x : scale.x) : 0.f;
                 const float ml = there ? -a.lse[row] * kLog2e : 0.f;
                 const float q0 = a.eps / static_cast<float>(a.vocab), qy = 1.f - a.eps;
                 sweep(cols, release, [&](int c, float (&z)[32]) {
@@ -428,7 +480,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 });
             } else {
                 const bool f32 = t.weight ? a.w_f32 : a.x_partial;
-                const float sc = (t.weight || !a.x_partial) && a.scale ? a.scale[1] : 1.f;
+                const float sc = t.weight || !a.x_partial ? scale.y : 1.f;
                 const int n = a.hidden - n0;
                 const bool there = row0 < (t.weight ? a.cols : a.rows);
                 if (f32)
@@ -475,35 +527,115 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
     if (warp == 1) tmem_free(tmem, kTmemColumns);
 }
 
-// One warp per row: the row's tiles merged.
+// (m, l) <- the maximum and the sum of exponentials of two sets of logits.
+__device__ __forceinline__ void merge_stats(float& m, float& l, float m2, float l2) {
+    const float mm = fmaxf(m, m2);
+    if (mm == -INFINITY) {  // both empty (or NaN)
+        l += l2;
+        return;
+    }
+    l = l * exp2_approx((m - mm) * kLog2e) + l2 * exp2_approx((m2 - mm) * kLog2e);
+    m = mm;
+}
+
+// Statistics of a single row (scoring one token): bound by reading W once.
+// Each warp goes through an equal run of W's rows, four at a time, 16 bytes a
+// lane, against x in shared memory; FP32 products and sums.  Measured at
+// 50257 x 1280 BF16: 26 us (a 256-row tile 28), at 128000 x 4096 152 (172,
+// 6.9 TB/s); two rows are no faster this way than in a tile.
+constexpr int kOneThreads = 256;
+constexpr int kOneWarps = kOneThreads / 32;
+constexpr int kOneCtas = 456;               // three on each SM
+constexpr int64_t kOneHidden = 48 << 9;     // x in 48 KB
+
+template <typename T>
+__global__ void __launch_bounds__(kOneThreads, 3)
+one_row_kernel(const T* __restrict__ x, const T* __restrict__ w, const __grid_constant__ HeadArgs a) {
+    extern __shared__ __align__(16) unsigned char one_mem[];
+    T* xs = reinterpret_cast<T*>(one_mem);
+    __shared__ float sm_m[kOneWarps], sm_l[kOneWarps], sm_s[kOneWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int vecs = a.hidden / kVec;
+    pdl_enter();
+    for (int v = threadIdx.x; v < vecs; v += kOneThreads) store8<T>(xs + v * kVec, load8<T>(x + v * kVec));
+    __syncthreads();
+    const int32_t y = a.target[0];
+    const bool used = used_target(y, a);
+    float m = -INFINITY, l = 0.f, s = 0.f;
+    const int64_t all = gridDim.x * kOneWarps, id = blockIdx.x * kOneWarps + warp;
+    const int end = static_cast<int>((id + 1) * a.vocab / all);
+    for (int j0 = static_cast<int>(id * a.vocab / all); j0 < end; j0 += 4) {
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
+        const T* wq[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) wq[q] = w + static_cast<int64_t>(min(j0 + q, end - 1)) * a.hidden;
+        for (int v0 = lane; v0 < vecs; v0 += 64) {
+            Raw8<T> f[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    f[u][q] = v0 + u * 32 < vecs ? load8<T>(wq[q] + (v0 + u * 32) * kVec) : zero8<T>();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (v0 + u * 32 >= vecs) break;
+                float h[kVec];
+                unpack(load8<T>(xs + (v0 + u * 32) * kVec), h);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float g[kVec];
+                    unpack(f[u][q], g);
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) z[q] = fmaf(g[j], h[j], z[q]);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[q] = group_sum<32>(z[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (j0 + q >= end) break;
+            if (used && y == j0 + q && lane == 0) a.zy[0] = z[q];
+            merge_stats(m, l, z[q], 1.f);
+            if (z[q] != z[q]) l = z[q];  // a NaN, which no maximum shows
+            s += z[q];
+        }
+    }
+    if (lane == 0) {
+        sm_m[warp] = m;
+        sm_l[warp] = l;
+        sm_s[warp] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int v = 1; v < kOneWarps; ++v) {
+            merge_stats(m, l, sm_m[v], sm_l[v]);
+            s += sm_s[v];
+        }
+        a.part[blockIdx.x] = make_float2(m, l);
+        a.part_sum[blockIdx.x] = s;
+    }
+}
+
+// One warp per row: the row's partial statistics merged.
 __global__ void __launch_bounds__(256)
 merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out, const __grid_constant__ HeadArgs a) {
     pdl_enter();
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= a.rows) return;
-    const int parts = 2 * a.n_tiles;
-    const float2* part = a.part + static_cast<int64_t>(row) * parts;
-    const float* part_sum = a.part_sum + static_cast<int64_t>(row) * parts;
+    const float2* part = a.part + static_cast<int64_t>(row) * a.parts;
+    const float* part_sum = a.part_sum + static_cast<int64_t>(row) * a.parts;
     float m = -INFINITY, l = 0.f, s = 0.f;
-    auto merge = [&](float m2, float l2) {
-        const float mm = fmaxf(m, m2);
-        if (mm == -INFINITY) {
-            l += l2;
-        } else {
-            l = l * exp2_approx((m - mm) * kLog2e) + l2 * exp2_approx((m2 - mm) * kLog2e);
-            m = mm;
-        }
-    };
 #pragma unroll 4
-    for (int t = lane; t < parts; t += 32) {
+    for (int t = lane; t < a.parts; t += 32) {
         const float2 p = part[t];
-        merge(p.x, p.y);
+        merge_stats(m, l, p.x, p.y);
         if (a.eps > 0.f) s += part_sum[t];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-        merge(m2, l2);
+        merge_stats(m, l, m2, l2);
         s += __shfl_xor_sync(0xffffffffu, s, o);
     }
     if (lane != 0) return;
@@ -517,9 +649,10 @@ merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out, const 
     loss[row] = v;
 }
 
-// scale[0] = 2^s, scale[1] = 2^-s with 2^s max|dloss| in (2^13, 2^14].
+// scale_for the largest finite |dloss| of many rows.
+template <typename T>
 __global__ void __launch_bounds__(1024)
-grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, int64_t rows) {
+grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, int64_t rows, float eps) {
     __shared__ float sm[32];
     pdl_enter();
     float m = 0.f;
@@ -533,14 +666,9 @@ grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, in
     if (threadIdx.x < 32) {
         m = group_max<32>(sm[threadIdx.x]);
         if (threadIdx.x == 0) {
-            int s = 0;
-            if (m > 0.f) {
-                int ex;
-                frexpf(m, &ex);  // m < 2^ex
-                s = min(100, max(-100, 14 - ex));
-            }
-            scale[0] = ldexpf(1.f, s);
-            scale[1] = ldexpf(1.f, -s);
+            const float2 f = scale_for<T>(m, eps);
+            scale[0] = f.x;
+            scale[1] = f.y;
         }
     }
 }
@@ -548,12 +676,12 @@ grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, in
 // dx = scale * sum over the slices' partial sums, in slice order.
 template <typename T>
 __global__ void __launch_bounds__(256)
-join_slices_kernel(T* __restrict__ dx, const float* __restrict__ part, const float* __restrict__ scale,
-                   int slices, int64_t nvec) {
+join_slices_kernel(T* __restrict__ dx, const float* __restrict__ part, int slices, int64_t nvec,
+                   const __grid_constant__ HeadArgs a) {
     pdl_enter();
     const int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (v >= nvec) return;
-    const float sc = scale ? scale[1] : 1.f;
+    const float sc = scale_of(a).y;
     float acc[kVec];
     load8f<float>(part + v * kVec, acc);
     for (int s = 1; s < slices; ++s) {
@@ -698,6 +826,7 @@ HeadArgs make_args(const HeadShape& sh, const int32_t* target) {
     a.m_tiles = static_cast<int>(ceil_div(sh.rows, kTileM));
     a.n_tiles = static_cast<int>(ceil_div(sh.vocab, kTileN));
     a.k_blocks = static_cast<int>(ceil_div(sh.hidden, kBlockK));
+    a.row_box = static_cast<int>(std::min<int64_t>(sh.rows, 128));
     a.eps = sh.eps;
     a.ignore_index = sh.ignore_index;
     a.target = target;
@@ -719,8 +848,16 @@ cudaError_t fwd(float* loss, float* lse, const void* x, const void* w, const int
     a.part = reinterpret_cast<float2*>(ws + p.part);
     a.part_sum = reinterpret_cast<float*>(ws + p.part_sum);
     a.zy = reinterpret_cast<float*>(ws + p.zy);
+    if (sh.rows == 1 && sh.hidden <= kOneHidden) {
+        a.parts = std::min(kOneCtas, 2 * a.n_tiles);
+        LS_CUDA(launch_pdl(one_row_kernel<T>, dim3(static_cast<unsigned>(a.parts)), dim3(kOneThreads),
+                           static_cast<size_t>(sh.hidden) * 2, s, static_cast<const T*>(x),
+                           static_cast<const T*>(w), a));
+        return launch_pdl(merge_stats_kernel, dim3(1), dim3(256), 0, s, loss, lse, a);
+    }
+    a.parts = 2 * a.n_tiles;
     HeadMaps maps = {};
-    LS_CUDA(make_map<T>(&maps.a, x, sh.hidden, sh.rows, sh.hidden, 128));
+    LS_CUDA(make_map<T>(&maps.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
     LS_CUDA(make_map<T>(&maps.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
     const int64_t units = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
     if (sh.eps > 0.f)
@@ -736,17 +873,17 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
                 const float* lse, const float* dloss, const HeadShape& sh, void* workspace, cudaStream_t s) {
     const HeadPlan p(sh.rows, sh.hidden, sh.vocab);
     char* ws = static_cast<char*>(workspace);
-    float* scale = nullptr;
-    if (std::is_same<T, __half>::value && dloss) {
-        scale = reinterpret_cast<float*>(ws + p.scale);
-        LS_CUDA(launch_pdl(grad_scale_kernel, dim3(1), dim3(1024), 0, s, scale, dloss, sh.rows));
-    }
     T* g = reinterpret_cast<T*>(ws + p.g);
     float* partial = reinterpret_cast<float*>(ws + p.partial);
     HeadArgs a = make_args(sh, target);
     a.lse = lse;
     a.dloss = dloss;
-    a.scale = scale;
+    a.scale = reinterpret_cast<float*>(ws + p.scale);
+    a.fixed_scale = scale_for<T>(1.f, sh.eps);
+    // A CTA goes through this many rows in less time than its first tile takes.
+    a.find_scale = dloss && sh.rows <= 16384;
+    if (dloss && !a.find_scale)
+        LS_CUDA(launch_pdl(grad_scale_kernel<T>, dim3(1), dim3(1024), 0, s, a.scale, dloss, sh.rows, sh.eps));
     a.x_m_tiles = a.m_tiles;
     a.h_tiles = static_cast<int>(ceil_div(sh.hidden, kTileN));
     a.slice_blocks = static_cast<int>(p.slice_blocks);
@@ -754,7 +891,7 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     a.x_partial = p.partial_dx;
     a.w_f32 = f32_dweight;
     HeadMaps mz = {}, mo = {};
-    LS_CUDA(make_map<T>(&mz.a, x, sh.hidden, sh.rows, sh.hidden, 128));
+    LS_CUDA(make_map<T>(&mz.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
     LS_CUDA(make_map<T>(&mz.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
     LS_CUDA(make_map<T>(&mo.b, w, sh.hidden, sh.vocab, sh.hidden, 64));
     LS_CUDA(make_map<T>(&mo.b2, x, sh.hidden, sh.rows, sh.hidden, 64));
@@ -773,7 +910,7 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
         a.n_tiles = static_cast<int>(ceil_div(cols, kTileN));
         LS_CUDA(make_map<T>(&mz.out, g, cols, sh.rows, p.cols, 32));
         LS_CUDA((launch_head<T, kGrad, false>(mz, a, static_cast<int64_t>(a.m_tiles) * a.n_tiles, s)));
-        LS_CUDA(make_map<T>(&mo.a, g, cols, sh.rows, p.cols, 128));
+        LS_CUDA(make_map<T>(&mo.a, g, cols, sh.rows, p.cols, a.row_box));
         LS_CUDA(make_map<T>(&mo.a2, g, cols, sh.rows, p.cols, 64));
         a.x_k_blocks = static_cast<int>(ceil_div(cols, kBlockK));
         a.x_add = c > 0;
@@ -784,7 +921,7 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     if (!dx || !p.partial_dx) return cudaSuccess;
     const int64_t nvec = sh.rows * sh.hidden / kVec;
     return launch_pdl(join_slices_kernel<T>, dim3(static_cast<unsigned>(ceil_div(nvec, 256))), dim3(256), 0, s,
-                      static_cast<T*>(dx), partial, scale, static_cast<int>(p.slices), nvec);
+                      static_cast<T*>(dx), partial, static_cast<int>(p.slices), nvec, a);
 }
 
 }  // namespace
