@@ -158,6 +158,40 @@ def test_non_finite_rows_stay_in_their_row():
     assert torch.equal(dx[rest], good[2][rest])
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_garbage_in_ignored_rows_stays_there(dtype):
+    """Padding rows may hold anything: NaN, infinities, a huge dloss."""
+    require_gpu()
+    x, w, t, d = inputs(300, 72, 1001, dtype, 14)
+    t[::3] = -100
+    good = run(x, w, t, d, 0.1)
+    x2, d2 = x.clone(), d.clone()
+    x2[::3] = float("nan")
+    x2[::6] = float("inf")
+    d2[::3] = 1e30
+    d2[::6] = float("nan")
+    loss, lse, dx, dw = run(x2, w, t, d2, 0.1)
+    used = torch.ones(300, dtype=torch.bool, device="cuda")
+    used[::3] = False
+    assert torch.equal(loss, good[0]) and torch.equal(lse[used], good[1][used])
+    assert torch.equal(dx, good[2]) and torch.equal(dw, good[3])
+
+
+def test_many_rows_of_dloss():
+    """More rows than a CTA looks through for the largest dloss."""
+    require_gpu()
+    x, w, t, d = inputs(16390, 64, 300, F16, 15)
+    d[16385] = 3.0
+    compare(run(x, w, t, d), x, w, t, d, 0.0, "many rows")
+
+
+@pytest.mark.parametrize("eps", [0.3, 0.5, 0.7, 0.95])
+def test_any_label_smoothing(eps):
+    require_gpu()
+    x, w, t, d = inputs(96, 64, 400, F16, 16, spread=8.0)
+    compare(run(x, w, t, d, eps), x, w, t, d, eps, f"eps {eps}")
+
+
 def test_repeats_bit_for_bit_and_in_a_graph_on_another_stream():
     require_gpu()
     x, w, t, d = inputs(333, 136, 5003, BF16, 12)

@@ -12,7 +12,7 @@
 // pairs of CTAs, each pair a 256 x 256 tile with FP32 accumulators in tensor
 // memory (two of them, so that one is read while the other is filled), operands
 // brought by TMA through a ring of 64-wide K blocks.  Warp 0 issues the copies,
-// warp 1 of the pair's first CTA the products, warps 2-9 take the accumulators
+// warp 1 of the pair's first CTA the products, the other warps take the accumulators
 // to the statistics, to g or to the outputs.  A pair, because a CTA on its own
 // needs 48 KB of operands for the 128 x 256 x 64 products that take it 512
 // cycles, more than the L2 gives an SM; each of a pair needs 32 KB.
@@ -43,15 +43,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTileM = 256;   // of a pair; 128 rows for each CTA
 constexpr int kTileN = 256;
 constexpr int kBlockK = 64;   // 128 bytes: the swizzle's row
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kEpilogueWarps = 8;  // two for each quarter of the tensor memory's lanes, half the columns each
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kWarpColumns = kTileN / 2;
+constexpr int kWarpBoxes = 2;      // a warp's store boxes: one is filled while the other is on its way
 constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;          // one operand of one CTA and stage
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr uint32_t kStoreBytes = 32 * 128;                     // one warp's store box
 constexpr uint32_t kTmemColumns = 512;
-constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * kStoreBytes;
+constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * kWarpBoxes * kStoreBytes;
 constexpr int kGroupM = 16;   // row tiles that share a sweep over the vocabulary
 constexpr int kPairs = 76;    // pairs of SMs; a constant, so that plans depend on the shapes alone
 
@@ -81,9 +82,11 @@ struct HeadArgs {
     float* scale;          // [2] in the workspace: g's factor and its inverse, if dloss is given
     float2 fixed_scale;    // the same if not
     bool find_scale;       // kGrad: from dloss, by every CTA (and left in `scale`)
+    const void* x;         // kGrad: copied to used_x, if that is given, with zeros for the rows that are
+    void* used_x;          //        not used: what they hold (a NaN, say) stays out of g^T x
 };
 
-// g's factor and its inverse for the largest finite |dloss|.
+// g's factor and its inverse for the largest finite |dloss| of the rows that are used.
 template <typename T> __host__ __device__ __forceinline__ float2 scale_for(float largest, float eps) {
     const float up = std::is_same<T, __half>::value ? 16384.f : 1.f;
     // 1 - eps is left out where p / (1 - eps) would leave FP16's range.
@@ -238,8 +241,11 @@ __device__ __forceinline__ void sweep(uint32_t cols, R&& release, F&& f) {
     f(3, zb);
 }
 
+// kGrad has two more warps, which write used_x.
+template <int MODE> constexpr int threads_of() { return MODE == kGrad ? kThreads + 64 : kThreads; }
+
 template <typename T, int MODE, bool SUM>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 1)
 head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadArgs a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
@@ -369,11 +375,23 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
             }
         }
         __syncwarp();
+    } else if (MODE == kGrad && warp >= kThreads / 32) {
+        const T* x = static_cast<const T*>(a.x);
+        T* used_x = static_cast<T*>(a.used_x);
+        if (used_x)
+            for (int row = blockIdx.x * 2 + warp - kThreads / 32; row < a.rows; row += 2 * gridDim.x) {
+                const bool used = used_target(a.target[row], a);
+                const int64_t first = static_cast<int64_t>(row) * a.hidden;
+                for (int c = lane * kVec; c < a.hidden; c += 32 * kVec)
+                    store8<T>(used_x + first + c, used ? load8<T>(x + first + c) : zero8<T>());
+            }
     } else {
         const int quad = warp & 3;          // the TMEM lanes this warp may read
-        const int half = (warp - 2) >> 2;   // its half of the tile's columns
-        unsigned char* box = smem + kStages * kStageBytes + (warp - 2) * kStoreBytes;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kWarpColumns;
+        const int part = (warp - 2) >> 2;   // its part of the tile's columns
+        unsigned char* const boxes = smem + kStages * kStageBytes + (warp - 2) * kWarpBoxes * kStoreBytes;
+        unsigned char* box = boxes;
+        uint32_t opened = 0;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kWarpColumns;
         uint32_t tile = 0;
         float2 scale = make_float2(1.f, 1.f);
         if constexpr (MODE == kGrad) {
@@ -382,7 +400,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 float m = 0.f;
                 for (int i = id; i < a.rows; i += 32 * kEpilogueWarps) {
                     const float d = fabsf(a.dloss[i]);
-                    if (d < INFINITY) m = fmaxf(m, d);
+                    if (d < INFINITY && used_target(a.target[i], a)) m = fmaxf(m, d);
                 }
                 m = group_max<32>(m);
                 if (lane == 0) largest[warp - 2] = m;
@@ -405,7 +423,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
             const uint32_t acc = tile & 1;
             const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
             const int row = row0 + lane;
-            const int n0 = t.n0 + half * kWarpColumns;                         // and column
+            const int n0 = t.n0 + part * kWarpColumns;                         // and column
             if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
             tc_fence_after();
             const uint32_t cols = lanes + acc * kTileN;
@@ -414,9 +432,10 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty + acc, 0));
             };
-            // The store box, free to be written; and on its way to memory.
+            // The next store box, free to be written; and on its way to memory.
             auto open_box = [&]() {
-                if (lane == 0) bulk_wait_read<0>();
+                box = boxes + (opened++ % kWarpBoxes) * kStoreBytes;
+                if (lane == 0) bulk_wait_read<kWarpBoxes - 1>();
                 __syncwarp();
             };
             auto close_box = [&](auto&& store) {
@@ -651,14 +670,13 @@ merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out, const 
 
 // scale_for the largest finite |dloss| of many rows.
 template <typename T>
-__global__ void __launch_bounds__(1024)
-grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, int64_t rows, float eps) {
+__global__ void __launch_bounds__(1024) grad_scale_kernel(const __grid_constant__ HeadArgs a) {
     __shared__ float sm[32];
     pdl_enter();
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < rows; i += 1024) {
-        const float d = fabsf(dloss[i]);
-        if (d < INFINITY) m = fmaxf(m, d);
+    for (int i = threadIdx.x; i < a.rows; i += 1024) {
+        const float d = fabsf(a.dloss[i]);
+        if (d < INFINITY && used_target(a.target[i], a)) m = fmaxf(m, d);
     }
     m = group_max<32>(m);
     if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
@@ -666,9 +684,9 @@ grad_scale_kernel(float* __restrict__ scale, const float* __restrict__ dloss, in
     if (threadIdx.x < 32) {
         m = group_max<32>(sm[threadIdx.x]);
         if (threadIdx.x == 0) {
-            const float2 f = scale_for<T>(m, eps);
-            scale[0] = f.x;
-            scale[1] = f.y;
+            const float2 f = scale_for<T>(m, a.eps);
+            a.scale[0] = f.x;
+            a.scale[1] = f.y;
         }
     }
 }
@@ -724,7 +742,7 @@ struct HeadPlan {
     int64_t n_tiles;                       // of the whole vocabulary
     int64_t cols, pieces;                  // columns of a piece (the last may have fewer)
     int64_t slices, slice_blocks;          // dx: K blocks of a piece per slice
-    size_t part, part_sum, zy, scale, g, partial, bytes;
+    size_t part, part_sum, zy, scale, g, used_x, partial, bytes;
     bool partial_dx;
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
         n_tiles = ceil_div(vocab, kTileN);
@@ -764,7 +782,8 @@ struct HeadPlan {
         partial_dx = slices > 1 || pieces > 1;
         scale = 0;
         g = 256;
-        partial = g + round256(static_cast<size_t>(rows * cols) * 2);
+        used_x = g + round256(static_cast<size_t>(rows * cols) * 2);
+        partial = used_x + round256(static_cast<size_t>(rows * hidden) * 2);
         const size_t bwd = partial + (partial_dx ? static_cast<size_t>(slices * rows * hidden) * 4 : 0);
         bytes = std::max(fwd, bwd);
     }
@@ -813,7 +832,7 @@ cudaError_t launch_head(const HeadMaps& maps, const HeadArgs& a, int64_t units, 
     cudaError_t e = allow_max_dynamic_smem(head_kernel<T, MODE, SUM>, done);
     if (e != cudaSuccess) return e;
     const int64_t pairs = std::min<int64_t>(units, kPairs);
-    return launch_pdl(head_kernel<T, MODE, SUM>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes,
+    return launch_pdl(head_kernel<T, MODE, SUM>, dim3(static_cast<unsigned>(2 * pairs)), dim3(threads_of<MODE>()), kSmemBytes,
                       s, maps, a);
 }
 
@@ -883,7 +902,7 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     // A CTA goes through this many rows in less time than its first tile takes.
     a.find_scale = dloss && sh.rows <= 16384;
     if (dloss && !a.find_scale)
-        LS_CUDA(launch_pdl(grad_scale_kernel<T>, dim3(1), dim3(1024), 0, s, a.scale, dloss, sh.rows, sh.eps));
+        LS_CUDA(launch_pdl(grad_scale_kernel<T>, dim3(1), dim3(1024), 0, s, a));
     a.x_m_tiles = a.m_tiles;
     a.h_tiles = static_cast<int>(ceil_div(sh.hidden, kTileN));
     a.slice_blocks = static_cast<int>(p.slice_blocks);
@@ -894,7 +913,7 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     LS_CUDA(make_map<T>(&mz.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
     LS_CUDA(make_map<T>(&mz.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
     LS_CUDA(make_map<T>(&mo.b, w, sh.hidden, sh.vocab, sh.hidden, 64));
-    LS_CUDA(make_map<T>(&mo.b2, x, sh.hidden, sh.rows, sh.hidden, 64));
+    LS_CUDA(make_map<T>(&mo.b2, ws + p.used_x, sh.hidden, sh.rows, sh.hidden, 64));
     if (dx && p.partial_dx)
         LS_CUDA(make_map<float>(&mo.out, partial, sh.hidden, sh.rows, sh.hidden, 32, p.slices));
     else if (dx)
@@ -908,6 +927,8 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
         a.col0 = static_cast<int>(c);
         a.cols = static_cast<int>(cols);
         a.n_tiles = static_cast<int>(ceil_div(cols, kTileN));
+        a.x = x;
+        a.used_x = dweight && c == 0 ? ws + p.used_x : nullptr;
         LS_CUDA(make_map<T>(&mz.out, g, cols, sh.rows, p.cols, 32));
         LS_CUDA((launch_head<T, kGrad, false>(mz, a, static_cast<int64_t>(a.m_tiles) * a.n_tiles, s)));
         LS_CUDA(make_map<T>(&mo.a, g, cols, sh.rows, p.cols, a.row_box));

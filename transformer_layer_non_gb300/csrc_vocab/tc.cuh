@@ -15,8 +15,11 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // --- cluster ------------------------------------------------------------------
+// Arrives on a barrier of either CTA of the pair.  The release is CTA-wide: what it announces here is
+// the end of tensor-memory reads, which tcgen05.wait::ld has already seen; a cluster-wide one would
+// wait for this thread's stores to global memory.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // --- tensor-map copies ----------------------------------------------------------
