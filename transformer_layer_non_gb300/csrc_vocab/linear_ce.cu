@@ -424,6 +424,17 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
             const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
             const int row = row0 + lane;
             const int n0 = t.n0 + part * kWarpColumns;                         // and column
+            // The row's values, on their way while the products end.
+            const bool there = row < a.rows;
+            int32_t y = -1;
+            float row_lse = 0.f, row_dloss = 1.f;
+            if (MODE != kOut && there) {
+                y = a.target[row];
+                if constexpr (MODE == kGrad) {
+                    row_lse = a.lse[row];
+                    if (a.dloss) row_dloss = a.dloss[row];
+                }
+            }
             if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
             tc_fence_after();
             const uint32_t cols = lanes + acc * kTileN;
@@ -448,7 +459,6 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
             };
             if constexpr (MODE == kStats) {
                 const int n = a.cols - n0;  // columns that exist
-                const int32_t y = row < a.rows ? a.target[row] : -1;
                 const int at = used_target(y, a) ? y - n0 : -1;
                 float m = -INFINITY;
                 float2 l = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
@@ -472,12 +482,10 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 }
             } else if constexpr (MODE == kGrad) {
                 const int n = a.cols - n0;
-                const bool there = row < a.rows;
-                const int32_t y = there ? a.target[row] : -1;
                 const bool used = there && used_target(y, a);
                 const int at = used ? y - a.col0 - n0 : -1;
-                const float d = used ? (a.dloss ? a.dloss[row] * scale.x : scale.x) : 0.f;
-                const float ml = there ? -a.lse[row] * kLog2e : 0.f;
+                const float d = used ? row_dloss * scale.x : 0.f;
+                const float ml = -row_lse * kLog2e;
                 const float q0 = a.eps / static_cast<float>(a.vocab), qy = 1.f - a.eps;
                 sweep(cols, release, [&](int c, float (&z)[32]) {
                     if (c * 32 >= n) return;
@@ -501,7 +509,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 const bool f32 = t.weight ? a.w_f32 : a.x_partial;
                 const float sc = t.weight || !a.x_partial ? scale.y : 1.f;
                 const int n = a.hidden - n0;
-                const bool there = row0 < (t.weight ? a.cols : a.rows);
+                const bool stores = row0 < (t.weight ? a.cols : a.rows);
                 if (f32)
                     sweep(cols, release, [&](int c, float (&z)[32]) {
                         if (c * 32 >= n) return;
@@ -512,11 +520,11 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                                   f2u4(make_float4(z[4 * j] * sc, z[4 * j + 1] * sc, z[4 * j + 2] * sc,
                                                    z[4 * j + 3] * sc)));
                         close_box([&] {
-                            if (there && t.weight)
+                            if (stores && t.weight)
                                 tma_add_2d(&maps.out2, n0 + c * 32, a.col0 + row0, box);
-                            else if (there && a.x_add)
+                            else if (stores && a.x_add)
                                 tma_add_3d(&maps.out, n0 + c * 32, row0, t.slice, box);
-                            else if (there)
+                            else if (stores)
                                 tma_store_3d(&maps.out, n0 + c * 32, row0, t.slice, box);
                         });
                     });
@@ -528,9 +536,9 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         for (int j = 0; j < 4; ++j) put16(box, lane, (c & 1) * 4 + j, pack8<T>(z, 8 * j, sc));
                         if ((c & 1) == 1 || c * 32 + 32 >= n)
                             close_box([&] {
-                                if (there && t.weight)
+                                if (stores && t.weight)
                                     tma_store_2d(&maps.out2, n0 + (c & ~1) * 32, a.col0 + row0, box);
-                                else if (there)
+                                else if (stores)
                                     tma_store_2d(&maps.out, n0 + (c & ~1) * 32, row0, box);
                             });
                     });
