@@ -90,6 +90,15 @@ def test_three_and_four_digit_vocabularies():
         compare(run(*a, 1.0), *a, 1.0, f"vocab {vocab}")
 
 
+@pytest.mark.parametrize("n,hidden,vocab", [(40, 1024, 40001), (5000, 2048, 20011), (20000, 1024, 50000)])
+def test_tables_of_many_bytes(n, hidden, vocab):
+    """Zeros for the ids that no token has come from two launches, and none may fall on a sum."""
+    require_gpu()
+    a = inputs(n, hidden, vocab, F16, "uniform")
+    a[1][0], a[1][-1] = 0, vocab - 1
+    compare(run(*a, 1.0, vocab // 2), *a, 1.0, f"{n}x{hidden} of {vocab}", vocab // 2)
+
+
 def test_padding_and_adding():
     require_gpu()
     table, tok, dy = inputs(700, 136, 90, F16)

@@ -153,7 +153,8 @@ constexpr int kRounds = 4;
 constexpr int64_t kClusterTokens = kMaxCluster * kSortThreads * kRounds;
 
 struct ClusterSortArgs {
-    int64_t zero_vecs;  // 16-byte vectors of d_table to write zeros to
+    int64_t zero_vecs;  // 16-byte vectors of d_table to write zeros to, from its first row on
+    uint32_t* present;  // if given, bit w: some token has the id w
     int n;
     int passes, cluster, rounds;
     int vocab, padding_id;
@@ -191,6 +192,9 @@ cluster_sort_kernel(int2* buf0, int2* buf1, const int32_t* __restrict__ tokens, 
     const int base = rank * tile + warp * a.rounds * 32 + lane;          // a warp's are consecutive
     // Four threads for each digit, each with eight warps' counts.
     const int digit = threadIdx.x >> 2, part = threadIdx.x & 3;
+    if (a.present)  // a barrier of every CTA of the cluster follows before the first bit is set
+        for (int i = rank * kSortThreads + threadIdx.x; i <= a.vocab / 32; i += a.cluster * kSortThreads)
+            a.present[i] = 0;
     for (int pass = 0; pass < a.passes; ++pass) {
         const int2* src = pass & 1 ? buf0 : buf1;
         int2* dst = pass & 1 ? buf1 : buf0;
@@ -285,6 +289,8 @@ cluster_sort_kernel(int2* buf0, int2* buf1, const int32_t* __restrict__ tokens, 
             for (int j = threadIdx.x; j < mine; j += kSortThreads) {
                 const int2 p = stage[j];
                 dst[shift_of[(p.x >> shift) & (kDigits - 1)] + j] = p;
+                if (a.present && pass == a.passes - 1 && p.x < a.vocab && (j == 0 || stage[j - 1].x != p.x))
+                    atomicOr(a.present + p.x / 32, 1u << (p.x & 31));
             }
         if (a.cluster > 1)
             cluster_sync();  // the pairs are there; cta_hist, hist and stage have been read
@@ -411,6 +417,11 @@ struct SumArgs {
     int col_blocks;
     float scale;
     bool accumulate;
+    // window_sum_kernel: the CTAs behind the first `sum_blocks` write zeros to the rows from zero_row
+    // on that no token has.
+    int64_t sum_blocks;
+    int zero_row;
+    const uint32_t* present;
 };
 
 __device__ __forceinline__ void put_row(float* d_table, int32_t w, int c, const float (&acc)[kVec],
@@ -436,10 +447,20 @@ __global__ void __launch_bounds__(kThreads)
 window_sum_kernel(float* d_table, float* __restrict__ partial, const T* __restrict__ dy,
                   const int2* __restrict__ pairs, const __grid_constant__ SumArgs a) {
     pdl_enter();
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x >= a.sum_blocks) {
+        const int step = static_cast<int>(gridDim.x - a.sum_blocks) * kWarps;
+        for (int row = a.zero_row + static_cast<int>(blockIdx.x - a.sum_blocks) * kWarps + (threadIdx.x >> 5);
+             row < a.vocab; row += step) {
+            if (a.present[row / 32] >> (row & 31) & 1) continue;
+            float* p = d_table + static_cast<int64_t>(row) * a.hidden;
+            for (int c = lane * 4; c < a.hidden; c += 128) st16(p + c, make_uint4(0, 0, 0, 0));
+        }
+        return;
+    }
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int64_t w = item / a.col_blocks;
     if (w >= a.windows) return;
-    const int lane = threadIdx.x & 31;
     const int c = static_cast<int>(item - w * a.col_blocks) * kBlockCols + lane * kVec;
     const int64_t base = w * a.window;
     const int count = static_cast<int>(min(static_cast<int64_t>(a.window), a.n - base));
@@ -592,10 +613,13 @@ join_windows_kernel(float* d_table, const float* __restrict__ partial,
 // --- workspace ----------------------------------------------------------------
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
+constexpr int64_t kMostPresent = 1 << 20;  // ids with a presence bit: one cluster clears them in no time
+
 struct LookupPlan {
     int64_t n, windows, blocks;
     int passes, window, cluster;          // cluster: CTAs of the one-launch sort, 0 for the other
-    size_t pairs[2], counts, partial, bytes;  // byte offsets
+    int64_t early_rows;                   // rows whose zeros are written beside the sort (the rest: the sums)
+    size_t pairs[2], counts, present, partial, bytes;  // byte offsets
     LookupPlan(int64_t tokens, int64_t hidden, int64_t vocab) {
         n = tokens;
         // Short windows where there are few: a window's rows are read one batch after the other.
@@ -616,6 +640,17 @@ struct LookupPlan {
         }
         counts = at;
         if (!cluster) at += round16(static_cast<size_t>(blocks + 1) * kDigits * 4);
+        present = at;
+        early_rows = vocab;
+        // The one-launch sort takes 6 to 16 us; that many bytes of zeros cost nothing beside it.  Where
+        // there are more, the rest is left to the launch of the sums, which then has to know the rows
+        // that it must not touch (4096 x 1280 of 50257: 52 us with all of them beside the sort, 47).
+        const int64_t early =
+            ((int64_t{40} << 20) + std::min<int64_t>(n, 8192) * 8192) / (hidden * 4);
+        if (cluster && vocab <= kMostPresent && vocab > early + early / 4) {
+            early_rows = early;
+            at += round16(static_cast<size_t>(vocab / 32 + 1) * 4);
+        }
         partial = at;
         at += static_cast<size_t>(2 * windows * hidden) * 4;
         bytes = at;
@@ -644,10 +679,9 @@ cudaError_t fwd(void* y, const int32_t* tokens, const void* table, int64_t n, in
 template <typename T>
 cudaError_t sums(float* d_table, float* partial, const void* dy, const int2* pairs,
                  const SumArgs& a, cudaStream_t s) {
-    const int64_t items = a.windows * a.col_blocks;
-    return launch_pdl(window_sum_kernel<T>,
-                      dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)), dim3(kThreads), 0,
-                      s, d_table, partial, static_cast<const T*>(dy), pairs, a);
+    const int64_t zeros = a.zero_row < a.vocab ? std::min((a.vocab - a.zero_row + kWarps - 1) / kWarps, 2432) : 0;
+    return launch_pdl(window_sum_kernel<T>, dim3(static_cast<unsigned>(a.sum_blocks + zeros)), dim3(kThreads),
+                      0, s, d_table, partial, static_cast<const T*>(dy), pairs, a);
 }
 
 // Pairs sorted by id, by a launch for each step of each pass; each writes its
@@ -710,12 +744,14 @@ cudaError_t launch_embedding_lookup_bwd(ls_dtype dt, float* d_table, const void*
                             reinterpret_cast<int2*>(ws + p.pairs[1])};
     float* partial = reinterpret_cast<float*>(ws + p.partial);
     const int64_t zero_vecs = accumulate ? 0 : vocab * hidden / 4;
+    uint32_t* present = reinterpret_cast<uint32_t*>(ws + p.present);
     cudaError_t e = cudaSuccess;
     if (p.cluster) {
         ClusterSortArgs a;
         a.n = static_cast<int>(n);
         a.rounds = static_cast<int>((n + p.cluster * kSortThreads - 1) / (p.cluster * kSortThreads));
-        a.zero_vecs = zero_vecs;
+        a.zero_vecs = accumulate ? 0 : p.early_rows * hidden / 4;
+        a.present = accumulate || p.early_rows == vocab ? nullptr : present;
         a.passes = p.passes;
         a.cluster = p.cluster;
         a.vocab = static_cast<int>(vocab);
@@ -723,7 +759,7 @@ cudaError_t launch_embedding_lookup_bwd(ls_dtype dt, float* d_table, const void*
         static int done[kMaxDevices];
         e = allow_max_dynamic_smem(cluster_sort_kernel, done);
         if (e != cudaSuccess) return e;
-        const int64_t want = (zero_vecs + kSortThreads * 4 - 1) / (kSortThreads * 4);
+        const int64_t want = (a.zero_vecs + kSortThreads * 4 - 1) / (kSortThreads * 4);
         const int64_t zeros = want < 296 ? want : 296;
         const int64_t grid = p.cluster + (zeros + p.cluster - 1) / p.cluster * p.cluster;
         e = launch_cluster(cluster_sort_kernel, dim3(static_cast<unsigned>(grid)), p.cluster,
@@ -743,6 +779,9 @@ cudaError_t launch_embedding_lookup_bwd(ls_dtype dt, float* d_table, const void*
     a.col_blocks = static_cast<int>((hidden + kBlockCols - 1) / kBlockCols);
     a.scale = scale;
     a.accumulate = accumulate;
+    a.sum_blocks = (a.windows * a.col_blocks + kWarps - 1) / kWarps;
+    a.zero_row = static_cast<int>(accumulate ? vocab : p.early_rows);
+    a.present = present;
     if (dt == LS_F16) e = sums<__half>(d_table, partial, dy, sorted, a, s);
     else if (dt == LS_BF16) e = sums<bf16>(d_table, partial, dy, sorted, a, s);
     else e = sums<float>(d_table, partial, dy, sorted, a, s);
