@@ -72,7 +72,7 @@ ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, c
  * division by max|dloss| (1 - eps) which the FP32 sums undo (FP16 keeps
  * values down to 2^-38 of the largest dloss that way).
  * dloss: FP32 [rows] or NULL for 1.  Rows with an ignored target contribute
- * nothing and get a zero dx.
+ * nothing and get a zero dx, whatever they and their dloss hold (NaN too).
  * dx: [rows, hidden] in the storage dtype, written, or NULL.
  * dweight: [vocab, hidden], or NULL; with dweight_dtype == dtype it is
  * written; with dweight_dtype == LS_F32 the gradient is ADDED to it, as
