@@ -398,9 +398,14 @@ DistillArgs make_args(const DistillShape& sh, int parts) {
     return a;
 }
 
-// Threads of a CTA: 128, and 256 for slices of 64K values or more (measured at
+// One warp for slices below 8K values: rows that short spend their time on the
+// entries' latencies, and an SM then has 32 of them at once (8192 x 4096 FP16,
+// k = 32: step 62 us with 128 threads, 38 with 32; 8192 x 1000: 54 and 23).
+constexpr int kShortSlice = 1024;
+
+// Threads of a CTA otherwise: 128, and 256 for slices of 64K values or more (measured at
 // 4096 x 30528 FP16: forward 47 us with 128, 51 with 256; 2047 x 131072 BF16: 104 and 92).
-int threads_of(const DistillArgs& a) { return a.slice >= 8192 ? 256 : 128; }
+int threads_of(const DistillArgs& a) { return a.slice >= 8192 ? 256 : a.slice >= kShortSlice ? 128 : 32; }
 
 // Slices of a row, for about `ctas` CTAs in all; none below two vectors for a thread.
 int parts_of(const DistillShape& sh, int ctas, int most) {
@@ -419,7 +424,9 @@ cudaError_t fwd(float* loss, float* lse, const void* logits, const int32_t* inde
     const int cluster = sh.rows > (1 << 20) ? 1 : parts_of(sh, 608, 8);
     const DistillArgs a = make_args(sh, cluster);
     const int threads = threads_of(a);
-    return launch_cluster(threads == 128 ? distill_fwd_kernel<T, 128> : distill_fwd_kernel<T, 256>,
+    return launch_cluster(threads == 32    ? distill_fwd_kernel<T, 32>
+                          : threads == 128 ? distill_fwd_kernel<T, 128>
+                                           : distill_fwd_kernel<T, 256>,
                           dim3(static_cast<unsigned>(sh.rows * cluster)), cluster, dim3(threads),
                           static_cast<size_t>(sh.k) * 8, s, loss, lse, static_cast<const T*>(logits),
                           index, static_cast<const T*>(teacher), teacher_lse, a, cluster);
@@ -434,7 +441,9 @@ cudaError_t bwd(void* dlogits, const void* logits, const int32_t* index, const v
     const int parts = parts_of(sh, sizeof(T) == 4 ? 3648 : 1216, 64);
     const DistillArgs a = make_args(sh, parts);
     const int threads = threads_of(a);
-    return launch_pdl(threads == 128 ? distill_bwd_kernel<T, 128> : distill_bwd_kernel<T, 256>,
+    return launch_pdl(threads == 32    ? distill_bwd_kernel<T, 32>
+                      : threads == 128 ? distill_bwd_kernel<T, 128>
+                                       : distill_bwd_kernel<T, 256>,
                       dim3(static_cast<unsigned>(sh.rows), static_cast<unsigned>(parts)),
                       dim3(threads), static_cast<size_t>(4 * sh.k + 2 * a.table) * 4, s,
                       static_cast<T*>(dlogits), static_cast<const T*>(logits), index,
