@@ -67,7 +67,9 @@ struct HeadArgs {
     float eps;
     int32_t ignore_index;
     // kOut
-    int x_units, w_units;  // units of dx and of dweight
+    int slices;            // of the piece's columns (K of dx, M of dweight)
+    int x_units, w_units;  // units of dx and of dweight in a slice
+    int units;             // in all
     int x_m_tiles, h_tiles;
     int x_k_blocks, slice_blocks, w_k_blocks;
     bool x_partial, x_add, w_f32;
@@ -129,24 +131,34 @@ template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const HeadArg
         t.n0 = (r / gm) * kTileN;
         t.m0 = (first + r % gm) * kTileM;
         t.kbs = a.k_blocks;
-    } else if (u < a.x_units) {
-        t.n0 = (u % a.h_tiles) * kTileN;
-        const int v = u / a.h_tiles;
-        t.m0 = (v % a.x_m_tiles) * kTileM;
-        t.slice = v / a.x_m_tiles;
-        t.kb0 = t.slice * a.slice_blocks;
-        t.kbs = min(a.slice_blocks, a.x_k_blocks - t.kb0);
     } else {
-        const int v = u - a.x_units;
-        t.weight = true;
-        t.n0 = (v % a.h_tiles) * kTileN;
-        t.m0 = (v / a.h_tiles) * kTileM;
-        t.kbs = a.w_k_blocks;
+        // One slice of g after the other, for dx and then for dweight, so that the second reading finds
+        // it in L2; the last slice, which may be narrower, first: it was written last.
+        const int first = a.units - (a.slices - 1) * (a.x_units + a.w_units);
+        int r = u, q = 0;
+        if (u >= first) {
+            q = (u - first) / (a.x_units + a.w_units);
+            r = u - first - q * (a.x_units + a.w_units);
+            ++q;
+        }
+        t.slice = a.slices - 1 - q;
+        t.kb0 = t.slice * a.slice_blocks;
+        t.weight = r >= a.x_units;
+        if (t.weight) r -= a.x_units;
+        t.n0 = (r % a.h_tiles) * kTileN;
+        t.m0 = (r / a.h_tiles) * kTileM;
+        if (t.weight) {
+            t.m0 += t.kb0 * kBlockK;
+            t.kb0 = 0;
+            t.kbs = a.w_k_blocks;
+        } else {
+            t.kbs = min(a.slice_blocks, a.x_k_blocks - t.kb0);
+        }
     }
     return t;
 }
 template <int MODE> __device__ __forceinline__ int units_of(const HeadArgs& a) {
-    return MODE == kOut ? a.x_units + a.w_units : a.m_tiles * a.n_tiles;
+    return MODE == kOut ? a.units : a.m_tiles * a.n_tiles;
 }
 
 // Bounded wait of a converged warp; false (and the failure flagged for the CTA
@@ -734,17 +746,6 @@ constexpr int64_t kMaxSlices = 16;
 // its tiles run and until the last is written, a unit about one.
 constexpr int64_t kLaunchBlocks = 24;
 
-// Time of `a` units of length p and then `b` of length q, dealt to the pairs in turn.
-int64_t dealt(int64_t a, int64_t p, int64_t b, int64_t q) {
-    auto share = [](int64_t n, int64_t i) { return n > i ? (n - i - 1) / kPairs + 1 : 0; };
-    int64_t most = 0;
-    for (const int64_t i : {int64_t{0}, a % kPairs, (a + b) % kPairs}) {
-        const int64_t na = share(a, i);
-        most = std::max(most, na * p + (share(a + b, i) - na) * q);
-    }
-    return most;
-}
-
 // Sizes and workspace layout; they depend on the shapes alone.
 struct HeadPlan {
     int64_t n_tiles;                       // of the whole vocabulary
@@ -771,10 +772,14 @@ struct HeadPlan {
             const int64_t np = ceil_div(vocab, c), kb = ceil_div(std::min(c, vocab), kBlockK);
             const int64_t grad = ceil_div(m_tiles * (c / kTileN), kPairs) * (h_blocks + 1);
             for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
-                const int64_t len = ceil_div(kb, s);
+                const int64_t len = ceil_div(ceil_div(kb, s), kTileM / kBlockK) * (kTileM / kBlockK);
                 if (ceil_div(kb, len) != s) continue;
-                const int64_t out = dealt(s * m_tiles * h_tiles, len + 1 + (s > 1 || np > 1),
-                                          (c / kTileM) * h_tiles, row_blocks + 1);
+                // Units of dx (a slice's K blocks long) and of dweight (the rows'), dealt to the pairs in turn.
+                const int64_t x_units = s * m_tiles * h_tiles, w_units = (c / kTileM) * h_tiles;
+                const int64_t x_len = std::min(len, kb) + 1 + (s > 1 || np > 1), w_len = row_blocks + 1;
+                const int64_t units = x_units + w_units;
+                const int64_t out = ceil_div(units, kPairs) * (x_units * x_len + w_units * w_len) / units +
+                                    std::max(x_len, w_len) - std::min(x_len, w_len);
                 // joining the slices: their bytes at about 1.7 MB for a K block's time
                 const int64_t join = s > 1 || np > 1 ? 12 + s * rows * hidden * 4 / 1700000 : 0;
                 const int64_t t = np * (grad + out + 2 * kLaunchBlocks) + join;
@@ -943,9 +948,11 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
         LS_CUDA(make_map<T>(&mo.a2, g, cols, sh.rows, p.cols, 64));
         a.x_k_blocks = static_cast<int>(ceil_div(cols, kBlockK));
         a.x_add = c > 0;
-        a.x_units = dx ? static_cast<int>(ceil_div(a.x_k_blocks, a.slice_blocks)) * a.x_m_tiles * a.h_tiles : 0;
-        a.w_units = dweight ? static_cast<int>(ceil_div(cols, kTileM)) * a.h_tiles : 0;
-        LS_CUDA((launch_head<T, kOut, false>(mo, a, static_cast<int64_t>(a.x_units) + a.w_units, s)));
+        a.slices = static_cast<int>(ceil_div(a.x_k_blocks, a.slice_blocks));
+        a.x_units = dx ? a.x_m_tiles * a.h_tiles : 0;
+        a.w_units = dweight ? a.slice_blocks / (kTileM / kBlockK) * a.h_tiles : 0;
+        a.units = a.slices * a.x_units + (dweight ? static_cast<int>(ceil_div(cols, kTileM)) * a.h_tiles : 0);
+        LS_CUDA((launch_head<T, kOut, false>(mo, a, a.units, s)));
     }
     if (!dx || !p.partial_dx) return cudaSuccess;
     const int64_t nvec = sh.rows * sh.hidden / kVec;
