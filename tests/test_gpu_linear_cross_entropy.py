@@ -57,7 +57,8 @@ def compare(got, x, w, t, d, eps, what, wtype=None, ignore=-100):
 
 SHAPES = [(1, 8, 1), (1, 64, 7), (3, 8, 130), (17, 72, 255), (64, 64, 256), (65, 136, 257),
           (128, 128, 1000), (129, 264, 1023), (200, 512, 513), (255, 200, 4099), (300, 1032, 777),
-          (1, 1280, 5003), (2, 1280, 5003), (1, 24584, 300)]
+          (1, 1280, 5003), (2, 1280, 5003), (1, 24584, 300),
+          (1, 2048, 700), (1, 2056, 700), (1, 6152, 333), (1, 12288, 50), (1, 12296, 50), (1, 1024, 3)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
