@@ -130,6 +130,16 @@ def test_no_tokens():
                                      torch.ones(3, 16, device="cuda", dtype=F16))
 
 
+def test_an_empty_table():
+    require_gpu()
+    table = torch.empty(0, 16, device="cuda", dtype=F16)
+    tok = torch.tensor([0, -1, 5], device="cuda", dtype=torch.int32)
+    y = torch.ones(3, 16, device="cuda", dtype=F16)
+    ls_vocab.ls_embedding_lookup_fwd(y, tok, table, 2.0)
+    assert (y == 0).all()
+    ls_vocab.ls_embedding_lookup_bwd(torch.empty(0, 16, device="cuda"), y, tok)
+
+
 def test_non_finite_rows_reach_their_id_alone():
     require_gpu()
     table, tok, dy = inputs(500, 64, 40, F16, "uniform")

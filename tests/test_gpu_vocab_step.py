@@ -111,3 +111,101 @@ def test_distillation_beside_the_criterion():
     got = s.dz.double() + z2.double()
     # two FP16 roundings of values up to 4, and FP16's smallest step
     assert ((got - zz.grad).abs() <= 2.0 ** -10 * (s.dz.double().abs() + z2.double().abs()) + 2.0 ** -23).all()
+
+
+def test_calls_at_the_same_time_on_two_streams():
+    """Two steps on two streams, each with its own buffers, give the bits of the steps one by one."""
+    require_gpu()
+    steps = [Step(700, 264, 5003, 8, torch.bfloat16), Step(1300, 520, 9001, 8, torch.bfloat16)]
+    want = []
+    for s in steps:
+        s()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (s.loss, s.lse, s.dh, s.d_table)])
+        for t in (s.loss, s.lse, s.dh, s.d_table, s.h):
+            t.view(torch.uint8).fill_(0x5A)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for s, stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                s()
+    torch.cuda.synchronize()
+    assert ls_vocab.check_device_errors() == 0
+    for s, w in zip(steps, want):
+        for a, b in zip((s.loss, s.lse, s.dh, s.d_table), w):
+            assert torch.equal(a, b)
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Replays that are ordered may share one workspace; a stream given by its handle is used."""
+    require_gpu()
+    steps = [Step(333, 136, 2003, 8, torch.float16), Step(65, 72, 901, 8, torch.float16)]
+    shared = max((s.ws for s in steps), key=lambda t: t.numel())
+    graphs, want = [], []
+    for s in steps:
+        s.ws = shared
+        s()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (s.loss, s.dh, s.d_table)])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s()
+        graphs.append(g)
+    for _ in range(3):
+        for s, g in zip(steps, graphs):
+            s.d_table.fill_(7.0)
+            g.replay()
+    torch.cuda.synchronize()
+    for s, w in zip(steps, want):
+        for a, b in zip((s.loss, s.dh, s.d_table), w):
+            assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    s = steps[0]
+    y = torch.empty_like(s.h)
+    torch.cuda.synchronize()
+    ls_vocab.ls_embedding_lookup_fwd(y, s.tokens, s.table, s.scale, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(y, s.h)
+
+
+_FIRST_CALLS = r"""
+import sys
+sys.path.insert(0, ROOT)
+import torch
+from tests.test_gpu_vocab_step import Step
+from transformer_layer_non_gb300 import ls_vocab
+s = Step(200, 136, 1001, 8, torch.bfloat16)
+z = torch.randn(200, 1008, device="cuda", dtype=torch.bfloat16)
+dz, one = torch.empty_like(z), torch.randn(1, 136, device="cuda", dtype=torch.bfloat16)
+torch.cuda.synchronize()
+
+def calls():
+    s()
+    ls_vocab.ls_linear_cross_entropy_fwd(s.kd[:1], None, one, s.table, s.target[:1], workspace=s.ws)
+    ls_vocab.ls_distill_topk_fwd(s.kd, s.kd_lse, z, s.index, s.teacher)
+    ls_vocab.ls_distill_topk_bwd(dz, z, s.index, s.teacher, s.kd_lse)
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):       # the process's first calls of the library
+    calls()
+g.replay()
+torch.cuda.synchronize()
+a = [t.clone() for t in (s.loss, s.dh, s.d_table, s.kd, dz)]
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(a, (s.loss, s.dh, s.d_table, s.kd, dz)))
+print("captured first")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+
+    require_gpu()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", "ROOT = " + repr(root) + "\n" + _FIRST_CALLS],
+                       capture_output=True, text=True, timeout=600, cwd=root)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
