@@ -226,3 +226,10 @@ def test_full_vocabularies(rows, hidden, vocab, dtype):
     if dtype == F16:
         d = d * 4096
     compare(run(x, w, t, d, 0.1), x, w, t, d, 0.1, f"{rows}x{hidden}x{vocab}")
+
+
+@pytest.mark.parametrize("hidden", [24440, 24448, 24456, 24536, 24576])
+def test_one_row_as_long_as_shared_memory(hidden):
+    require_gpu()
+    x, w, t, d = inputs(1, hidden, 70, BF16, 17)
+    compare(run(x, w, t, d, 0.1), x, w, t, d, 0.1, f"hidden {hidden}")

@@ -585,7 +585,7 @@ __device__ __forceinline__ void merge_stats(float& m, float& l, float m2, float 
 constexpr int kOneThreads = 256;
 constexpr int kOneWarps = kOneThreads / 32;
 constexpr int kOneCtas = 456;               // three on each SM
-constexpr int64_t kOneHidden = 48 << 9;     // x in 48 KB
+constexpr int64_t kOneHidden = (48 << 9) - 128;  // x in the 48 KB that every launch may have, less the warps' sums
 
 template <typename T>
 __global__ void __launch_bounds__(kOneThreads, 3)
