@@ -233,3 +233,23 @@ def test_one_row_as_long_as_shared_memory(hidden):
     require_gpu()
     x, w, t, d = inputs(1, hidden, 70, BF16, 17)
     compare(run(x, w, t, d, 0.1), x, w, t, d, 0.1, f"hidden {hidden}")
+
+
+@pytest.mark.parametrize("rows", [1, 5, 130])
+def test_vocabulary_entries_of_minus_infinity(rows):
+    """Whole tiles of logits of -inf have the probability 0; a NaN among them stays."""
+    require_gpu()
+    x, w, t, _ = inputs(rows, 64, 1000, BF16, 18)
+    x = x.abs() + 0.125
+    w[256:600] = -float("inf")
+    t[:] = torch.randint(0, 256, (rows,), device="cuda", dtype=torch.int32)
+    ws = ls_vocab.new_workspace(ls_vocab.linear_cross_entropy_workspace_bytes(rows, 64, 1000))
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ls_vocab.ls_linear_cross_entropy_fwd(loss, lse, x, w, t, workspace=ws)
+    keep = torch.cat([w[:256], w[600:]])
+    ref, bound = vocab_ref.linear_cross_entropy(x, keep, t)
+    vocab_ref.check(loss, ref[0], bound[0], "loss")
+    vocab_ref.check(lse, ref[1], bound[1], "lse")
+    w[300] = float("nan")
+    ls_vocab.ls_linear_cross_entropy_fwd(loss, lse, x, w, t, workspace=ws)
+    assert torch.isnan(loss).all() and torch.isnan(lse).all()

@@ -200,7 +200,7 @@ __device__ __forceinline__ void add_stats(float (&z)[32], int n, float& m, float
         l = mul2(l, make_float2(f, f));
         m = cm;
     }
-    const float mc = -m * kLog2e;
+    const float mc = m == -INFINITY ? 0.f : -m * kLog2e;  // nothing but -inf (or NaN) so far
     const float2 cc = make_float2(kLog2e, kLog2e), mm = make_float2(mc, mc);
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
