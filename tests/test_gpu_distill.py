@@ -173,3 +173,19 @@ def test_a_row_of_lowest_values():
             want, bound = vocab_ref.distill(flat, ix[6:7], t[6:7], None, 1.0, d[6:7])
             rounding = 65504.0 * 2.0 ** -24 * (want[2].abs() + d[6].double() / 1024)
             vocab_ref.check(dz[6:7], want[2], bound[2] + rounding, "uniform")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_nan_among_masked_logits(dtype):
+    """A NaN shows where all that its thread reads besides is masked, or NaN too."""
+    require_gpu()
+    z, ix, t, tl, d = inputs(8, 50264, 5, dtype, False, 1.0, 7)
+    z[4, 4096:] = -INF
+    z[5, 4096:] = -INF
+    z[5, 30001] = float("nan")
+    z[6] = float("nan")
+    ix[4:6] = torch.arange(5, device="cuda", dtype=torch.int32)
+    loss, lse, dz = run(z, ix, t, tl, d, 1.0)
+    assert torch.isfinite(loss[4]) and torch.isfinite(lse[4])
+    assert torch.isnan(loss[5:7]).all() and torch.isnan(lse[5:7]).all()
+    assert torch.isnan(dz[6]).all()

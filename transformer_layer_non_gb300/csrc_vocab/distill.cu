@@ -187,8 +187,9 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
                     const float2 t = fma2(make_float2(f[j], f[j + 1]), cc, mm);
                     l2 = add2(l2, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
                 }
-            } else if (m != -INFINITY) {  // m is finite and m c is not (FP32's lowest values as a mask)
-                for (int j = 0; j < kVec; ++j) l2.x += exp2_approx((f[j] - m) * a.c);
+            } else {  // m c is infinite (FP32's lowest values as a mask), or m is: -inf adds nothing, a NaN stays
+                for (int j = 0; j < kVec; ++j)
+                    if (f[j] != -INFINITY) l2.x += exp2_approx((f[j] - m) * a.c);
             }
         }
     }
