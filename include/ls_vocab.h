@@ -94,7 +94,7 @@ size_t ls_linear_cross_entropy_workspace_bytes(int64_t rows, int64_t hidden, int
  * student (LS_F32, LS_F16 or LS_BF16; vocab a multiple of 8), teacher_index:
  * int32 [rows, k] and teacher_logits: [rows, k] in the same storage dtype, the
  * k vocabulary entries that the teacher gave for the row, in any order.  With
- * temperature tau > 0 and, for the valid entries e (index in [0, vocab)),
+ * temperature tau, 2^-60 to 2^60, and, for the valid entries e (index in [0, vocab)),
  *   log q[e] = t[e] / tau - teacher_lse[row]     or, with teacher_lse == NULL,
  *   log q[e] = t[e] / tau - log sum_valid exp(t / tau)     (renormalised over the entries)
  *   log p[j] = z[j] / tau - lse[row],  lse[row] = log sum_j exp(z[j] / tau)

@@ -111,6 +111,15 @@ def test_distill_refusals(status, bad):
     assert distill_bwd(**bad) == status, ls_vocab.last_error()
 
 
+def test_distill_temperatures():
+    """tau^2 and log2(e) / tau are FP32 factors: temperatures that overflow or lose them are refused."""
+    for tau in (3e38, 2e19, 2.0 ** 61, 2.0 ** -61, 3e-39, 5e-39):
+        assert distill_fwd(tau=tau) == distill_bwd(tau=tau) == INVALID
+        assert "temperature" in ls_vocab.last_error()
+    for tau in (2.0 ** 60, 2.0 ** -60):
+        assert distill_fwd(rows=0, tau=tau) == distill_bwd(rows=0, tau=tau) == ls_ops.LS_OK
+
+
 def test_distill_refusals_of_one_direction():
     assert distill_fwd(loss=None) == INVALID
     assert distill_fwd(lse=P[0]) == INVALID

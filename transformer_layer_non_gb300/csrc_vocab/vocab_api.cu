@@ -79,8 +79,8 @@ ls_status check_distill(const char* fn, ls_dtype dt, int64_t rows, int64_t vocab
     LS_TRY(check_size(fn, "vocab", vocab, 1, ls::kMaxVocab));
     LS_TRY(check_multiple_of_8(fn, "vocab", vocab));
     LS_TRY(check_size(fn, "k", k, 1, ls::kMaxTeacherEntries));
-    if (!(tau > 0.f && isfinite(tau)) || !isfinite(1.f / tau))
-        return fail(LS_ERR_INVALID_ARGUMENT, "%s: temperature = %g is not positive and finite", fn,
+    if (!(tau >= 0x1p-60f && tau <= 0x1p60f))  // 1/tau and tau^2 are FP32 factors
+        return fail(LS_ERR_INVALID_ARGUMENT, "%s: temperature = %g is not in [2^-60, 2^60]", fn,
                     static_cast<double>(tau));
     return LS_OK;
 }
