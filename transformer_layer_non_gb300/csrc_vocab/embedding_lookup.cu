@@ -8,9 +8,9 @@
 //     digit radix sort, 8 bits a pass, as many passes as the vocabulary needs.
 //     Tokens that add nothing (padding, ids outside the table) get the key
 //     `vocab` and end up last.  Up to kClusterTokens tokens are sorted by one
-//     cluster of CTAs in one launch, while the launch's other CTAs write the
-//     zeros of a dE that is not accumulated into; more by a launch for each
-//     step of each pass.
+//     cluster of CTAs in one launch; more by three launches a pass.  The
+//     launches' other CTAs write the zeros of a dE that is not accumulated
+//     into; what is more than fits beside a one-launch sort is left to step 2.
 //  2. One warp per window of sorted positions and 256 columns walks its
 //     positions in order and keeps the running sum of the current id in FP32
 //     registers.  An id whose positions all lie in the window is written at
