@@ -113,15 +113,32 @@ def _check(status: int):
 # A call on a few rows takes less time on the GPU than its checks in Python
 # could: one comparison decides per tensor, and the reason is only looked for
 # when it fails.
+_torch = _int32 = _float32 = None
 _codes = None
+_get_device = None  # the current CUDA device, once there is one
+
+
+def _device() -> int:
+    """The current CUDA device, or -2 (no tensor's device) without one."""
+    if _get_device is not None:
+        return _get_device()
+    return _first_device()
+
+
+def _first_device() -> int:
+    global _torch, _int32, _float32, _codes, _get_device
+    import torch
+
+    _torch, _int32, _float32 = torch, torch.int32, torch.float32
+    _codes = {torch.float16: LS_F16, torch.bfloat16: LS_BF16, torch.float32: LS_F32}
+    if not torch.cuda.is_available():
+        return -2
+    device = torch.cuda.current_device()  # initialises CUDA
+    _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return device
 
 
 def _storage_code(t) -> int:
-    global _codes
-    if _codes is None:
-        import torch
-
-        _codes = {torch.float16: LS_F16, torch.bfloat16: LS_BF16, torch.float32: LS_F32}
     code = _codes.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported storage dtype {t.dtype}; use float16, bfloat16 or float32")
@@ -147,6 +164,21 @@ def _tensor(name: str, t, shape, dtype, device: int) -> int:
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
+def _shaped(name: str, t, dims: int, dtype, device: int):
+    """(address, shape) of a contiguous tensor with that many dimensions, whose sizes are the
+    call's (dtype None: any)."""
+    try:
+        shape = t.shape
+        if (len(shape) == dims and t.is_contiguous() and t.get_device() == device
+                and (dtype is None or t.dtype is dtype)):
+            return t.data_ptr(), shape
+    except AttributeError:
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}") from None
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    return _tensor(name, t, shape, dtype or t.dtype, device), shape
+
+
 def _optional(name: str, t, shape, dtype, device: int):
     return None if t is None else _tensor(name, t, shape, dtype, device)
 
@@ -155,29 +187,13 @@ def _workspace(t, device: int):
     """(address, bytes) of the workspace."""
     if t is None:
         return None, 0
-    return _tensor("workspace", t, getattr(t, "shape", None), getattr(t, "dtype", None),
-                   device), t.numel() * t.element_size()
-
-
-def _dims(name: str, t, n: int):
-    shape = getattr(t, "shape", None)
-    if shape is None:
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if len(shape) != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {len(shape)}")
-    return shape
-
-
-_have_cuda = False
-
-
-def _device() -> int:
-    """The current CUDA device, or -2 (no tensor's device) without one."""
-    global _have_cuda
-    import torch
-
-    _have_cuda = _have_cuda or torch.cuda.is_available()
-    return torch.cuda.current_device() if _have_cuda else -2
+    try:
+        if t.is_contiguous() and t.get_device() == device:
+            return t.data_ptr(), t.nbytes
+        shape, dtype = t.shape, t.dtype
+    except AttributeError:
+        raise TypeError(f"workspace must be a tensor, got {type(t).__name__}") from None
+    return _tensor("workspace", t, shape, dtype, device), t.nbytes
 
 
 _raw_stream = None
@@ -189,8 +205,7 @@ def _stream_of(stream, device: int):
     if stream is not None:
         return _stream(stream)
     if _raw_stream is None:
-        import torch
-
+        torch = _torch
         # the handle alone, where this torch offers it: a Stream object costs microseconds
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda d: torch.cuda.current_stream(d).cuda_stream)
@@ -203,17 +218,15 @@ def ls_linear_cross_entropy_fwd(loss, lse, x, weight, target, label_smoothing: f
     """Per-row loss (FP32 [rows]) and lse (FP32 [rows] or None) of the logits
     x weight^T against int32 targets: x [rows, hidden], weight [vocab, hidden].
     The logits are not kept."""
-    import torch
-
     dev = _device()
-    rows, hidden = _dims("x", x, 2)
-    vocab = _dims("weight", weight, 2)[0]
-    dtype, per_row = x.dtype, (rows,)
-    px = _tensor("x", x, (rows, hidden), dtype, dev)
-    pw = _tensor("weight", weight, (vocab, hidden), dtype, dev)
-    pt = _tensor("target", target, per_row, torch.int32, dev)
-    ploss = _tensor("loss", loss, per_row, torch.float32, dev)
-    plse = _optional("lse", lse, per_row, torch.float32, dev)
+    px, (rows, hidden) = _shaped("x", x, 2, None, dev)
+    pw, (vocab, wide) = _shaped("weight", weight, 2, x.dtype, dev)
+    if wide != hidden:
+        _tensor("weight", weight, (vocab, hidden), x.dtype, dev)
+    per_row = (rows,)
+    pt = _tensor("target", target, per_row, _int32, dev)
+    ploss = _tensor("loss", loss, per_row, _float32, dev)
+    plse = _optional("lse", lse, per_row, _float32, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_linear_cross_entropy_fwd(
         _storage_code(x), ploss, plse, px, pw, pt, rows, hidden, vocab, label_smoothing,
@@ -225,24 +238,22 @@ def ls_linear_cross_entropy_bwd(dx, dweight, x, weight, target, lse, dloss=None,
                                 workspace=None, stream=None):
     """Gradients of x and weight (either may be None).  A dweight in the
     storage dtype is written; a float32 dweight is added to."""
-    import torch
-
     dev = _device()
-    rows, hidden = _dims("x", x, 2)
-    vocab = _dims("weight", weight, 2)[0]
+    px, (rows, hidden) = _shaped("x", x, 2, None, dev)
+    pw, (vocab, wide) = _shaped("weight", weight, 2, x.dtype, dev)
+    if wide != hidden:
+        _tensor("weight", weight, (vocab, hidden), x.dtype, dev)
     dtype, per_row = x.dtype, (rows,)
-    px = _tensor("x", x, (rows, hidden), dtype, dev)
-    pw = _tensor("weight", weight, (vocab, hidden), dtype, dev)
-    pt = _tensor("target", target, per_row, torch.int32, dev)
-    plse = _tensor("lse", lse, per_row, torch.float32, dev)
-    pg = _optional("dloss", dloss, per_row, torch.float32, dev)
+    pt = _tensor("target", target, per_row, _int32, dev)
+    plse = _tensor("lse", lse, per_row, _float32, dev)
+    pg = _optional("dloss", dloss, per_row, _float32, dev)
     pdx = _optional("dx", dx, (rows, hidden), dtype, dev)
     code = wcode = _storage_code(x)
     pdw = None
     if dweight is not None:
-        wcode = _storage_code(dweight)
-        pdw = _tensor("dweight", dweight, (vocab, hidden),
-                      torch.float32 if wcode == LS_F32 else dtype, dev)
+        if getattr(dweight, "dtype", None) is _float32:
+            wcode, dtype = LS_F32, _float32
+        pdw = _tensor("dweight", dweight, (vocab, hidden), dtype, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_linear_cross_entropy_bwd(
         code, pdx, pdw, wcode, px, pw, pt, plse, pg, rows, hidden, vocab, label_smoothing,
@@ -250,15 +261,13 @@ def ls_linear_cross_entropy_bwd(dx, dweight, x, weight, target, lse, dloss=None,
 
 
 def _distill_inputs(logits, teacher_index, teacher_logits, teacher_lse, dev):
-    import torch
-
-    rows, vocab = _dims("logits", logits, 2)
-    k = _dims("teacher_index", teacher_index, 2)[1]
-    dtype = logits.dtype
-    return (rows, vocab, k, _tensor("logits", logits, (rows, vocab), dtype, dev),
-            _tensor("teacher_index", teacher_index, (rows, k), torch.int32, dev),
-            _tensor("teacher_logits", teacher_logits, (rows, k), dtype, dev),
-            _optional("teacher_lse", teacher_lse, (rows,), torch.float32, dev))
+    pz, (rows, vocab) = _shaped("logits", logits, 2, None, dev)
+    pi, (irows, k) = _shaped("teacher_index", teacher_index, 2, _int32, dev)
+    if irows != rows:
+        _tensor("teacher_index", teacher_index, (rows, k), _int32, dev)
+    return (rows, vocab, k, pz, pi,
+            _tensor("teacher_logits", teacher_logits, (rows, k), logits.dtype, dev),
+            _optional("teacher_lse", teacher_lse, (rows,), _float32, dev))
 
 
 def ls_distill_topk_fwd(loss, lse, logits, teacher_index, teacher_logits, teacher_lse=None,
@@ -266,13 +275,11 @@ def ls_distill_topk_fwd(loss, lse, logits, teacher_index, teacher_logits, teache
     """Per-row distillation loss (FP32 [rows]) of the student's logits
     [rows, vocab] from the teacher's k entries of each row, and the student's
     lse at that temperature (FP32 [rows] or None)."""
-    import torch
-
     dev = _device()
     rows, vocab, k, pz, pi, pt, ptl = _distill_inputs(logits, teacher_index, teacher_logits,
                                                       teacher_lse, dev)
-    ploss = _tensor("loss", loss, (rows,), torch.float32, dev)
-    plse = _optional("lse", lse, (rows,), torch.float32, dev)
+    ploss = _tensor("loss", loss, (rows,), _float32, dev)
+    plse = _optional("lse", lse, (rows,), _float32, dev)
     _check(load().ls_distill_topk_fwd(_storage_code(logits), ploss, plse, pz, pi, pt, ptl, rows,
                                       vocab, k, temperature, _stream_of(stream, dev)))
 
@@ -280,27 +287,21 @@ def ls_distill_topk_fwd(loss, lse, logits, teacher_index, teacher_logits, teache
 def ls_distill_topk_bwd(dlogits, logits, teacher_index, teacher_logits, lse, teacher_lse=None,
                         dloss=None, temperature: float = 1.0, stream=None):
     """Gradient of the student's logits (dlogits may be logits)."""
-    import torch
-
     dev = _device()
     rows, vocab, k, pz, pi, pt, ptl = _distill_inputs(logits, teacher_index, teacher_logits,
                                                       teacher_lse, dev)
     pdz = _tensor("dlogits", dlogits, (rows, vocab), logits.dtype, dev)
-    plse = _tensor("lse", lse, (rows,), torch.float32, dev)
-    pg = _optional("dloss", dloss, (rows,), torch.float32, dev)
+    plse = _tensor("lse", lse, (rows,), _float32, dev)
+    pg = _optional("dloss", dloss, (rows,), _float32, dev)
     _check(load().ls_distill_topk_bwd(_storage_code(logits), pdz, pz, pi, pt, plse, ptl, pg, rows,
                                       vocab, k, temperature, _stream_of(stream, dev)))
 
 
 def ls_embedding_lookup_fwd(y, tokens, table, scale: float = 1.0, stream=None):
     """y [tokens, hidden] = scale * table[tokens] for int32 tokens [tokens]."""
-    import torch
-
     dev = _device()
-    vocab, hidden = _dims("table", table, 2)
-    (n,) = _dims("tokens", tokens, 1)
-    pt = _tensor("tokens", tokens, (n,), torch.int32, dev)
-    pe = _tensor("table", table, (vocab, hidden), table.dtype, dev)
+    pe, (vocab, hidden) = _shaped("table", table, 2, None, dev)
+    pt, (n,) = _shaped("tokens", tokens, 1, _int32, dev)
     py = _tensor("y", y, (n, hidden), table.dtype, dev)
     _check(load().ls_embedding_lookup_fwd(_storage_code(table), py, pt, pe, n, hidden, vocab, scale,
                                           _stream_of(stream, dev)))
@@ -310,15 +311,12 @@ def ls_embedding_lookup_bwd(d_table, dy, tokens, scale: float = 1.0, padding_id:
                             accumulate: bool = False, workspace=None, stream=None):
     """The table's gradient (FP32 [vocab, hidden]) of dy [tokens, hidden]:
     written whole, or added to d_table with accumulate."""
-    import torch
-
     dev = _device()
-    vocab, hidden = _dims("d_table", d_table, 2)
-    (n,) = _dims("tokens", tokens, 1)
-    _dims("dy", dy, 2)
-    pd = _tensor("d_table", d_table, (vocab, hidden), torch.float32, dev)
-    pdy = _tensor("dy", dy, (n, hidden), dy.dtype, dev)
-    pt = _tensor("tokens", tokens, (n,), torch.int32, dev)
+    pd, (vocab, hidden) = _shaped("d_table", d_table, 2, _float32, dev)
+    pt, (n,) = _shaped("tokens", tokens, 1, _int32, dev)
+    pdy, size = _shaped("dy", dy, 2, None, dev)
+    if size != (n, hidden):
+        _tensor("dy", dy, (n, hidden), dy.dtype, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_embedding_lookup_bwd(_storage_code(dy), pd, pdy, pt, n, hidden, vocab, scale,
                                           padding_id, int(bool(accumulate)), ws, ws_bytes,
