@@ -578,14 +578,18 @@ __device__ __forceinline__ void merge_stats(float& m, float& l, float m2, float 
 }
 
 // Statistics of a single row (scoring one token): bound by reading W once.
-// Each warp goes through an equal run of W's rows, four at a time, 16 bytes a
-// lane, against x in shared memory; FP32 products and sums.  Measured at
-// 50257 x 1280 BF16: 26 us (a 256-row tile 28), at 128000 x 4096 152 (172,
-// 6.9 TB/s); two rows are no faster this way than in a tile.
+// Each warp goes through an equal run of W's rows, two at a time, 16 bytes a
+// lane, against x in shared memory; FP32 products and sums.  The loads run
+// ahead over the rows' ends, so that they never wait for a row's reduction.
+// Measured with the merging at 50257 x 1280 BF16: 24 us (a 256-row tile 28),
+// at 128000 x 4096 150 (172; 7.0 TB/s), at 30522 x 768 12.8; four rows and two
+// columns in flight are as fast, 12 or 16 vectors in flight slower.  Two rows
+// of x are no faster this way than in a tile.
 constexpr int kOneThreads = 256;
 constexpr int kOneWarps = kOneThreads / 32;
 constexpr int kOneCtas = 456;               // three on each SM
-constexpr int64_t kOneHidden = (48 << 9) - 128;  // x in the 48 KB that every launch may have, less the warps' sums
+constexpr int kOneRows = 2, kOneSlots = 4;  // a lane's loads in flight: vectors of so many rows of W, so often
+constexpr int64_t kOneHidden = (48 << 9) - 256;  // x in the 48 KB that every launch may have, less the warps' sums
 
 template <typename T>
 __global__ void __launch_bounds__(kOneThreads, 3)
@@ -596,48 +600,63 @@ one_row_kernel(const T* __restrict__ x, const T* __restrict__ w, const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int vecs = a.hidden / kVec;
     pdl_enter();
+    const int64_t all = gridDim.x * kOneWarps, id = blockIdx.x * kOneWarps + warp;
+    const int end = static_cast<int>((id + 1) * a.vocab / all);
+    int j0 = static_cast<int>(id * a.vocab / all);
+    const int columns = (vecs + 31) / 32;  // vectors of a row for a lane
+    // The columns of the groups of rows, one after the other: each is loaded into the place of the one that
+    // has just been used, kOneSlots columns ahead, the next group's too.
+    Raw8<T> r[kOneSlots][kOneRows];
+    int load_j = j0, load_v = lane;
+    auto load = [&](int slot) {
+#pragma unroll
+        for (int q = 0; q < kOneRows; ++q)
+            r[slot][q] = load_j < end && load_v < vecs
+                             ? load8<T>(w + static_cast<int64_t>(min(load_j + q, end - 1)) * a.hidden + load_v * kVec)
+                             : zero8<T>();
+        load_v += 32;
+        if (load_v - lane >= columns * 32) {
+            load_v = lane;
+            load_j += kOneRows;
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < kOneSlots; ++u) load(u);
     for (int v = threadIdx.x; v < vecs; v += kOneThreads) store8<T>(xs + v * kVec, load8<T>(x + v * kVec));
+    for (int v = vecs + threadIdx.x; v < columns * 32; v += kOneThreads) store8<T>(xs + v * kVec, zero8<T>());
     __syncthreads();
     const int32_t y = a.target[0];
     const bool used = used_target(y, a);
     float m = -INFINITY, l = 0.f, s = 0.f;
-    const int64_t all = gridDim.x * kOneWarps, id = blockIdx.x * kOneWarps + warp;
-    const int end = static_cast<int>((id + 1) * a.vocab / all);
-    for (int j0 = static_cast<int>(id * a.vocab / all); j0 < end; j0 += 4) {
-        float z[4] = {0.f, 0.f, 0.f, 0.f};
-        const T* wq[4];
+    float z[kOneRows] = {};
+    for (int v = 0; j0 < end;) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) wq[q] = w + static_cast<int64_t>(min(j0 + q, end - 1)) * a.hidden;
-        for (int v0 = lane; v0 < vecs; v0 += 64) {
-            Raw8<T> f[2][4];
+        for (int u = 0; u < kOneSlots; ++u) {
+            float h[kVec];
+            unpack(load8<T>(xs + (v * 32 + lane) * kVec), h);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int q = 0; q < kOneRows; ++q) {
+                float g[kVec];
+                unpack(r[u][q], g);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    f[u][q] = v0 + u * 32 < vecs ? load8<T>(wq[q] + (v0 + u * 32) * kVec) : zero8<T>();
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (v0 + u * 32 >= vecs) break;
-                float h[kVec];
-                unpack(load8<T>(xs + (v0 + u * 32) * kVec), h);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float g[kVec];
-                    unpack(f[u][q], g);
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) z[q] = fmaf(g[j], h[j], z[q]);
-                }
+                for (int j = 0; j < kVec; ++j) z[q] = fmaf(g[j], h[j], z[q]);
             }
-        }
+            load(u);
+            if (++v < columns) continue;
+            v = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) z[q] = group_sum<32>(z[q]);
+            for (int q = 0; q < kOneRows; ++q) z[q] = group_sum<32>(z[q]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (j0 + q >= end) break;
-            if (used && y == j0 + q && lane == 0) a.zy[0] = z[q];
-            merge_stats(m, l, z[q], 1.f);
-            if (z[q] != z[q]) l = z[q];  // a NaN, which no maximum shows
-            s += z[q];
+            for (int q = 0; q < kOneRows; ++q) {
+                if (j0 + q >= end) break;
+                if (used && y == j0 + q && lane == 0) a.zy[0] = z[q];
+                merge_stats(m, l, z[q], 1.f);
+                if (z[q] != z[q]) l = z[q];  // a NaN, which no maximum shows
+                s += z[q];
+            }
+            j0 += kOneRows;
+#pragma unroll
+            for (int q = 0; q < kOneRows; ++q) z[q] = 0.f;
         }
     }
     if (lane == 0) {
@@ -665,11 +684,27 @@ merge_stats_kernel(float* __restrict__ loss, float* __restrict__ lse_out, const 
     const float2* part = a.part + static_cast<int64_t>(row) * a.parts;
     const float* part_sum = a.part_sum + static_cast<int64_t>(row) * a.parts;
     float m = -INFINITY, l = 0.f, s = 0.f;
-#pragma unroll 4
-    for (int t = lane; t < a.parts; t += 32) {
-        const float2 p = part[t];
-        merge_stats(m, l, p.x, p.y);
-        if (a.eps > 0.f) s += part_sum[t];
+    constexpr int U = 16;  // loads in flight
+    for (int t0 = lane; t0 < a.parts; t0 += 32 * U) {
+        float2 p[U];
+        float q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool there = t0 + 32 * u < a.parts;
+            p[u] = there ? part[t0 + 32 * u] : make_float2(-INFINITY, 0.f);
+            q[u] = there && a.eps > 0.f ? part_sum[t0 + 32 * u] : 0.f;
+        }
+        float mm = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) mm = fmaxf(mm, p[u].x);
+        const float mc = mm == -INFINITY ? 0.f : mm;  // nothing but -inf (or NaN sums) so far
+        l *= exp2_approx((m - mc) * kLog2e);
+        m = mm;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            l += p[u].y * exp2_approx((p[u].x - mc) * kLog2e);
+            s += q[u];
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -755,9 +790,10 @@ struct HeadPlan {
     bool partial_dx;
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
         n_tiles = ceil_div(vocab, kTileN);
+        const size_t parts = static_cast<size_t>(rows == 1 ? std::max<int64_t>(2 * n_tiles, kOneCtas) : rows * 2 * n_tiles);
         part = 0;
-        part_sum = round256(static_cast<size_t>(rows * n_tiles) * 16);
-        zy = part_sum + round256(static_cast<size_t>(rows * n_tiles) * 8);
+        part_sum = round256(parts * 8);
+        zy = part_sum + round256(parts * 4);
         const size_t fwd = zy + static_cast<size_t>(rows) * 4;
 
         // The number of pieces, and of slices that cut dx's long K (the vocabulary) into units about
@@ -881,9 +917,9 @@ cudaError_t fwd(float* loss, float* lse, const void* x, const void* w, const int
     a.part_sum = reinterpret_cast<float*>(ws + p.part_sum);
     a.zy = reinterpret_cast<float*>(ws + p.zy);
     if (sh.rows == 1 && sh.hidden <= kOneHidden) {
-        a.parts = std::min(kOneCtas, 2 * a.n_tiles);
+        a.parts = static_cast<int>(std::min<int64_t>(kOneCtas, ceil_div(sh.vocab, kOneWarps)));
         LS_CUDA(launch_pdl(one_row_kernel<T>, dim3(static_cast<unsigned>(a.parts)), dim3(kOneThreads),
-                           static_cast<size_t>(sh.hidden) * 2, s, static_cast<const T*>(x),
+                           static_cast<size_t>(ceil_div(sh.hidden, 32 * kVec)) * 32 * kVec * 2, s, static_cast<const T*>(x),
                            static_cast<const T*>(w), a));
         return launch_pdl(merge_stats_kernel, dim3(1), dim3(256), 0, s, loss, lse, a);
     }
