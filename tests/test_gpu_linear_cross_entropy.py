@@ -253,3 +253,14 @@ def test_vocabulary_entries_of_minus_infinity(rows):
     w[300] = float("nan")
     ls_vocab.ls_linear_cross_entropy_fwd(loss, lse, x, w, t, workspace=ws)
     assert torch.isnan(loss).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("rows,hidden,vocab", [(16385, 72, 9001), (5000, 520, 14001), (1030, 264, 33000)])
+def test_orders_of_the_output_tiles(rows, hidden, vocab):
+    """Many rows (dweight's tiles are the long ones), few, and a piece that leaves L2."""
+    require_gpu()
+    x, w, t, d = inputs(rows, hidden, vocab, BF16, 19)
+    both = run(x, w, t, d, 0.1)
+    compare(both, x, w, t, d, 0.1, f"{rows}x{hidden}x{vocab}")
+    assert torch.equal(run(x, w, t, d, 0.1, want_dw=False)[2], both[2])
+    assert torch.equal(run(x, w, t, d, 0.1, want_dx=False)[3], both[3])

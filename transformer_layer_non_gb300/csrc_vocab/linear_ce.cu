@@ -72,7 +72,7 @@ struct HeadArgs {
     int units;             // in all
     int x_m_tiles, h_tiles;
     int x_k_blocks, slice_blocks, w_k_blocks;
-    bool x_partial, x_add, w_f32;
+    bool by_slice, w_first, x_partial, x_add, w_f32;
     // kStats
     int parts;             // partial statistics of a row: two for each tile, or one for each CTA
     float2* part;          // [rows][parts]: maximum, sum of exponentials
@@ -132,19 +132,30 @@ template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const HeadArg
         t.m0 = (first + r % gm) * kTileM;
         t.kbs = a.k_blocks;
     } else {
-        // One slice of g after the other, for dx and then for dweight, so that the second reading finds
-        // it in L2; the last slice, which may be narrower, first: it was written last.
-        const int first = a.units - (a.slices - 1) * (a.x_units + a.w_units);
-        int r = u, q = 0;
-        if (u >= first) {
-            q = (u - first) / (a.x_units + a.w_units);
-            r = u - first - q * (a.x_units + a.w_units);
-            ++q;
+        int r = u;
+        if (!a.by_slice) {  // all of one, then all of the other
+            const int x_all = a.slices * a.x_units, first = a.w_first ? a.units - x_all : x_all;
+            t.weight = (r >= first) != a.w_first;
+            if (r >= first) r -= first;
+            if (!t.weight) {
+                t.slice = r / a.x_units;
+                r -= t.slice * a.x_units;
+            }
+        } else {
+            // One slice of g after the other, for dx and then for dweight, so that the second reading
+            // finds it in L2; the last slice, which may be narrower, first: it was written last.
+            const int first = a.units - (a.slices - 1) * (a.x_units + a.w_units);
+            int q = 0;
+            if (u >= first) {
+                q = (u - first) / (a.x_units + a.w_units);
+                r = u - first - q * (a.x_units + a.w_units);
+                ++q;
+            }
+            t.slice = a.slices - 1 - q;
+            t.weight = r >= a.x_units;
+            if (t.weight) r -= a.x_units;
         }
-        t.slice = a.slices - 1 - q;
         t.kb0 = t.slice * a.slice_blocks;
-        t.weight = r >= a.x_units;
-        if (t.weight) r -= a.x_units;
         t.n0 = (r % a.h_tiles) * kTileN;
         t.m0 = (r / a.h_tiles) * kTileM;
         if (t.weight) {
@@ -776,6 +787,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // (never fewer than 2048 entries).
 constexpr int64_t kPieceBytes = int64_t{128} << 20;
 constexpr int64_t kMaxSlices = 16;
+constexpr int64_t kSliceBytes = int64_t{64} << 20;
 // The plan below counts time in K blocks of a pair's tile (256 x 256 x 64
 // products, about 0.25 us).  A launch costs about kLaunchBlocks of them until
 // its tiles run and until the last is written, a unit about one.
@@ -788,6 +800,7 @@ struct HeadPlan {
     int64_t slices, slice_blocks;          // dx: K blocks of a piece per slice
     size_t part, part_sum, zy, scale, g, used_x, partial, bytes;
     bool partial_dx;
+    bool by_slice, w_first;                // the order of kOut's units
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
         n_tiles = ceil_div(vocab, kTileN);
         const size_t parts = static_cast<size_t>(rows == 1 ? std::max<int64_t>(2 * n_tiles, kOneCtas) : rows * 2 * n_tiles);
@@ -807,6 +820,9 @@ struct HeadPlan {
             const int64_t c = ceil_div(ceil_div(vocab, n), kTileN) * kTileN;
             const int64_t np = ceil_div(vocab, c), kb = ceil_div(std::min(c, vocab), kBlockK);
             const int64_t grad = ceil_div(m_tiles * (c / kTileN), kPairs) * (h_blocks + 1);
+            // Where g has left L2 before it is read again, at about 1.1 TB/s of what the products hide.
+            const int64_t g_bytes = rows * std::min(c, vocab) * 2;
+            const int64_t reread = g_bytes > kSliceBytes ? g_bytes >> 22 : 0;
             for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
                 const int64_t len = ceil_div(ceil_div(kb, s), kTileM / kBlockK) * (kTileM / kBlockK);
                 if (ceil_div(kb, len) != s) continue;
@@ -814,8 +830,20 @@ struct HeadPlan {
                 const int64_t x_units = s * m_tiles * h_tiles, w_units = (c / kTileM) * h_tiles;
                 const int64_t x_len = std::min(len, kb) + 1 + (s > 1 || np > 1), w_len = row_blocks + 1;
                 const int64_t units = x_units + w_units;
-                const int64_t out = ceil_div(units, kPairs) * (x_units * x_len + w_units * w_len) / units +
-                                    std::max(x_len, w_len) - std::min(x_len, w_len);
+                // The longer ones first: what the pair with the most of it gets.
+                const bool longer_w = w_len > x_len;
+                const int64_t n_first = longer_w ? w_units : x_units;
+                int64_t out = 0;
+                for (const int64_t p : {int64_t{0}, n_first % kPairs, units % kPairs}) {
+                    const int64_t n = n_first / kPairs + (p < n_first % kPairs);
+                    const int64_t rest = units / kPairs + (p < units % kPairs) - n;
+                    out = std::max(out, n * std::max(x_len, w_len) + rest * std::min(x_len, w_len));
+                }
+                out += reread;
+                // Or slice by slice: no more than this.
+                const int64_t sliced = ceil_div(units, kPairs) * std::max(x_len, w_len);
+                const bool interleaved = s > 1 && reread > 0 && sliced < out;
+                if (interleaved) out = sliced;
                 // joining the slices: their bytes at about 1.7 MB for a K block's time
                 const int64_t join = s > 1 || np > 1 ? 12 + s * rows * hidden * 4 / 1700000 : 0;
                 const int64_t t = np * (grad + out + 2 * kLaunchBlocks) + join;
@@ -825,6 +853,8 @@ struct HeadPlan {
                     pieces = np;
                     slices = s;
                     slice_blocks = len;
+                    by_slice = interleaved;
+                    w_first = longer_w;
                 }
             }
         }
@@ -958,6 +988,8 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     a.w_k_blocks = static_cast<int>(ceil_div(sh.rows, kBlockK));
     a.x_partial = p.partial_dx;
     a.w_f32 = f32_dweight;
+    a.by_slice = p.by_slice;
+    a.w_first = p.w_first;
     HeadMaps mz = {}, mo = {};
     LS_CUDA(make_map<T>(&mz.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
     LS_CUDA(make_map<T>(&mz.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
