@@ -399,14 +399,18 @@ DistillArgs make_args(const DistillShape& sh, int parts) {
     return a;
 }
 
-// One warp for slices below 8K values: rows that short spend their time on the
-// entries' latencies, and an SM then has 32 of them at once (8192 x 4096 FP16,
-// k = 32: step 62 us with 128 threads, 38 with 32; 8192 x 1000: 54 and 23).
-constexpr int kShortSlice = 1024;
+// One warp for slices below 8K values where there are many: they spend their time on the entries'
+// latencies, and an SM then has 32 of them at once (8192 x 4096 FP16, k = 32: step 62 us with 128
+// threads, 38 with 32; 8192 x 1000: 54 and 23; 100 x 50264 FP32 in slices, backward: 10.6 and 8.4).
+// Few slices have the SMs to themselves (5 x 50264 FP32, forward: 4.9 us with 128 threads, 6.4 with 32).
+constexpr int kShortSlice = 1024, kManySlices = 608;
 
 // Threads of a CTA otherwise: 128, and 256 for slices of 64K values or more (measured at
 // 4096 x 30528 FP16: forward 47 us with 128, 51 with 256; 2047 x 131072 BF16: 104 and 92).
-int threads_of(const DistillArgs& a) { return a.slice >= 8192 ? 256 : a.slice >= kShortSlice ? 128 : 32; }
+int threads_of(const DistillArgs& a, int64_t slices) {
+    if (a.slice < kShortSlice && slices >= kManySlices) return 32;
+    return a.slice >= 8192 ? 256 : 128;
+}
 
 // Slices of a row, for about `ctas` CTAs in all; none below two vectors for a thread.
 int parts_of(const DistillShape& sh, int ctas, int most) {
@@ -424,7 +428,7 @@ cudaError_t fwd(float* loss, float* lse, const void* logits, const int32_t* inde
     // A grid's x extent ends at 2^31 - 1 CTAs.
     const int cluster = sh.rows > (1 << 20) ? 1 : parts_of(sh, 608, 8);
     const DistillArgs a = make_args(sh, cluster);
-    const int threads = threads_of(a);
+    const int threads = threads_of(a, sh.rows * cluster);
     return launch_cluster(threads == 32    ? distill_fwd_kernel<T, 32>
                           : threads == 128 ? distill_fwd_kernel<T, 128>
                                            : distill_fwd_kernel<T, 256>,
@@ -441,7 +445,7 @@ cudaError_t bwd(void* dlogits, const void* logits, const int32_t* index, const v
     // 40 in four slices; FP16 rows, half as long, gain nothing.)
     const int parts = parts_of(sh, sizeof(T) == 4 ? 3648 : 1216, 64);
     const DistillArgs a = make_args(sh, parts);
-    const int threads = threads_of(a);
+    const int threads = threads_of(a, sh.rows * parts);
     return launch_pdl(threads == 32    ? distill_bwd_kernel<T, 32>
                       : threads == 128 ? distill_bwd_kernel<T, 128>
                                        : distill_bwd_kernel<T, 256>,
