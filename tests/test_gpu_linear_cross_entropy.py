@@ -264,3 +264,21 @@ def test_orders_of_the_output_tiles(rows, hidden, vocab):
     compare(both, x, w, t, d, 0.1, f"{rows}x{hidden}x{vocab}")
     assert torch.equal(run(x, w, t, d, 0.1, want_dw=False)[2], both[2])
     assert torch.equal(run(x, w, t, d, 0.1, want_dx=False)[3], both[3])
+
+
+@pytest.mark.parametrize("rows,hidden,vocab", [(3, 136, v) for v in (64 * 76, 64 * 76 + 1, 96 * 76, 128 * 76 - 1,
+                                                                  160 * 76 + 5, 192 * 76, 224 * 76 - 3, 224 * 152)]
+                         + [(300, 72, 224 * 38), (512, 72, 9001), (513, 72, 9001)])
+def test_widths_of_the_forward_tiles(rows, hidden, vocab):
+    """The last column, and the columns at the borders of tiles of any width, as targets."""
+    require_gpu()
+    x, w, t, _ = inputs(rows, hidden, vocab, F16, 20)
+    ws = ls_vocab.new_workspace(ls_vocab.linear_cross_entropy_workspace_bytes(rows, hidden, vocab))
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    for width in (32, 64, 96, 128, 160, 192, 224, 256):
+        border = width * (1 + torch.arange(rows, device="cuda", dtype=torch.int32) // 2)
+        t.copy_((border - torch.arange(rows, device="cuda", dtype=torch.int32) % 2) % vocab)
+        ls_vocab.ls_linear_cross_entropy_fwd(loss, lse, x, w, t, 0.1, workspace=ws)
+        ref, bound = vocab_ref.linear_cross_entropy(x, w, t, 0.1)
+        vocab_ref.check(loss, ref[0], bound[0], f"{rows}x{vocab} loss at {width}")
+        vocab_ref.check(lse, ref[1], bound[1], f"{rows}x{vocab} lse at {width}")

@@ -9,7 +9,7 @@
 // storage type in the workspace, then dx += g W_piece and dW_piece = g^T x.
 //
 // All three products run in one kernel (head_kernel) on tcgen05: persistent
-// pairs of CTAs, each pair a 256 x 256 tile with FP32 accumulators in tensor
+// pairs of CTAs, each pair a tile of 256 x 256 (z also narrower) with FP32 accumulators in tensor
 // memory (two of them, so that one is read while the other is filled), operands
 // brought by TMA through a ring of 64-wide K blocks.  Warp 0 issues the copies,
 // warp 1 of the pair's first CTA the products, the other warps take the accumulators
@@ -46,7 +46,6 @@ constexpr int kBlockK = 64;   // 128 bytes: the swizzle's row
 constexpr int kStages = 5;
 constexpr int kEpilogueWarps = 8;  // two for each quarter of the tensor memory's lanes, half the columns each
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kWarpColumns = kTileN / 2;
 constexpr int kWarpBoxes = 2;      // a warp's store boxes: one is filled while the other is on its way
 constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;          // one operand of one CTA and stage
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
@@ -62,6 +61,8 @@ struct HeadArgs {
     int rows, vocab, hidden;
     int col0, cols;        // this piece of the vocabulary
     int m_tiles, n_tiles;  // kStats, kGrad: rows x piece
+    int tile_n;            // kStats, kGrad: columns of a tile, a multiple of 32 (kStats), 128 or 256 (kGrad)
+    int warp_columns;      // and of the first of its two warps in a quarter of the lanes, a multiple of 32
     int row_box;           // rows of the copies of x and g with rows as M: 128, or all where there are fewer
     int k_blocks;
     float eps;
@@ -128,7 +129,7 @@ template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const HeadArg
         const int first = g * kGroupM;
         const int gm = min(kGroupM, a.m_tiles - first);
         const int r = u - first * a.n_tiles;
-        t.n0 = (r / gm) * kTileN;
+        t.n0 = (r / gm) * a.tile_n;
         t.m0 = (first + r % gm) * kTileM;
         t.kbs = a.k_blocks;
     } else {
@@ -310,14 +311,15 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
         uint32_t it = 0;
         for (int u = pair; u < units; u += pairs) {
             const Unit t = unit_of<MODE>(u, a);
-            const int m = t.m0 + static_cast<int>(rank) * 128, n = t.n0 + static_cast<int>(rank) * 128;
+            const int b_rows = MODE == kOut ? 128 : a.tile_n / 2;
+            const int m = t.m0 + static_cast<int>(rank) * 128, n = t.n0 + static_cast<int>(rank) * b_rows;
             // Rows behind the last one are not copied (filling them with zeros costs a copy of 1 row
             // 10 us in 40): what the shared memory holds there reaches rows of the accumulator that
             // nothing reads.
             auto a_bytes = [&](int first) -> uint32_t {
                 return t.weight ? kOperandBytes : first < a.rows ? static_cast<uint32_t>(a.row_box) * 128 : 0;
             };
-            const uint32_t bytes = 2 * kOperandBytes + a_bytes(t.m0) + a_bytes(t.m0 + 128);  // of both CTAs
+            const uint32_t bytes = 2 * b_rows * 128 + a_bytes(t.m0) + a_bytes(t.m0 + 128);  // of both CTAs
             const bool has_a = a_bytes(m) > 0;
             for (int kb = 0; kb < t.kbs; ++kb, ++it) {
                 const uint32_t s = it % kStages;
@@ -366,7 +368,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 tc_fence_after();
                 // Which operands have M or N as their contiguous axis.
                 const bool a_mn = MODE == kOut && t.weight, b_mn = MODE == kOut;
-                const uint32_t idesc = instr_desc(kBf16, false, false, kTileM, kTileN) |
+                const uint32_t idesc = instr_desc(kBf16, false, false, kTileM, MODE == kOut ? kTileN : a.tile_n) |
                                        (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
                 const uint64_t da = desc_at(a_mn ? mnmajor : kmajor, smem_u32(smem));
                 const uint64_t db = desc_at(b_mn ? mnmajor : kmajor, smem_u32(smem) + kOperandBytes);
@@ -414,7 +416,9 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
         unsigned char* const boxes = smem + kStages * kStageBytes + (warp - 2) * kWarpBoxes * kStoreBytes;
         unsigned char* box = boxes;
         uint32_t opened = 0;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kWarpColumns;
+        const int warp_n0 = part * (MODE == kOut ? kTileN / 2 : a.warp_columns);  // this warp's first column
+        const int warp_n = MODE == kOut ? kTileN / 2 : part ? a.tile_n - a.warp_columns : a.warp_columns;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + warp_n0;
         uint32_t tile = 0;
         float2 scale = make_float2(1.f, 1.f);
         if constexpr (MODE == kGrad) {
@@ -446,7 +450,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
             const uint32_t acc = tile & 1;
             const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
             const int row = row0 + lane;
-            const int n0 = t.n0 + part * kWarpColumns;                         // and column
+            const int n0 = t.n0 + warp_n0;                                     // and column
             // The row's values, on their way while the products end.
             const bool there = row < a.rows;
             int32_t y = -1;
@@ -481,8 +485,8 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 }
             };
             if constexpr (MODE == kStats) {
-                const int n = a.cols - n0;  // columns that exist
-                const int at = used_target(y, a) ? y - n0 : -1;
+                const int n = min(a.cols - n0, warp_n);  // columns that exist
+                const int at = used_target(y, a) && y - n0 < n ? y - n0 : -1;
                 float m = -INFINITY;
                 float2 l = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
                 sweep(cols, release, [&](int c, float (&z)[32]) {
@@ -499,12 +503,12 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         add_stats<true, SUM>(z, n - c * 32, m, l, s);
                 });
                 if (row < a.rows) {
-                    const int64_t o = static_cast<int64_t>(row) * a.parts + n0 / kWarpColumns;
+                    const int64_t o = static_cast<int64_t>(row) * a.parts + t.n0 / a.tile_n * 2 + part;
                     a.part[o] = make_float2(m, l.x + l.y);
                     if constexpr (SUM) a.part_sum[o] = s.x + s.y;
                 }
             } else if constexpr (MODE == kGrad) {
-                const int n = a.cols - n0;
+                const int n = min(a.cols - n0, warp_n);
                 const bool used = there && used_target(y, a);
                 const int at = used ? y - a.col0 - n0 : -1;
                 const float d = used ? row_dloss * scale.x : 0.f;
@@ -793,16 +797,41 @@ constexpr int64_t kSliceBytes = int64_t{64} << 20;
 // its tiles run and until the last is written, a unit about one.
 constexpr int64_t kLaunchBlocks = 24;
 
+// Columns of the forward's tiles.  One or two tiles of rows get fewer than 256 where the busiest pair has
+// less to do that way: a K block's time goes with the columns down to 128, and a unit costs about one K block
+// more (8 x 1280 of 50257: three rounds of 256 columns 27.5 us, of 224 26.7; 130 x 264 of 4099: 17 tiles 7.9,
+// 65 of 64 columns 7.4).  More rows lose more by reading x for each tile (1024 x 768 of 30522: 30 -> 34).
+int stats_columns(int64_t rows, int64_t hidden, int64_t vocab) {
+    if (rows > 2 * kTileM) return kTileN;
+    const int64_t m_tiles = ceil_div(rows, kTileM), k_blocks = ceil_div(hidden, kBlockK);
+    int best_n = kTileN;
+    int64_t best = INT64_MAX;
+    for (int n = kTileN; n >= 64; n -= 32) {
+        const int64_t t = ceil_div(m_tiles * ceil_div(vocab, n), kPairs) * ((std::max(n, 128) + 8) * k_blocks + n + 256);
+        if (t < best) {
+            best = t;
+            best_n = n;
+        }
+    }
+    return best_n;
+}
+// Columns of the tiles of g: 128 where that takes no pair a second one (130 x 264 of 4099, both gradients:
+// 17.5 -> 16.1 us; 333 x 512 of 32000, seven rounds for four: 46 -> 50).
+int grad_columns(int64_t rows, int64_t cols) {
+    return ceil_div(rows, kTileM) * ceil_div(cols, kTileN / 2) <= kPairs ? kTileN / 2 : kTileN;
+}
+
 // Sizes and workspace layout; they depend on the shapes alone.
 struct HeadPlan {
-    int64_t n_tiles;                       // of the whole vocabulary
+    int stats_n;                           // columns of the forward's tiles
     int64_t cols, pieces;                  // columns of a piece (the last may have fewer)
     int64_t slices, slice_blocks;          // dx: K blocks of a piece per slice
     size_t part, part_sum, zy, scale, g, used_x, partial, bytes;
     bool partial_dx;
     bool by_slice, w_first;                // the order of kOut's units
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
-        n_tiles = ceil_div(vocab, kTileN);
+        stats_n = stats_columns(rows, hidden, vocab);
+        const int64_t n_tiles = ceil_div(vocab, stats_n);
         const size_t parts = static_cast<size_t>(rows == 1 ? std::max<int64_t>(2 * n_tiles, kOneCtas) : rows * 2 * n_tiles);
         part = 0;
         part_sum = round256(parts * 8);
@@ -922,13 +951,19 @@ HeadArgs make_args(const HeadShape& sh, const int32_t* target) {
     a.hidden = static_cast<int>(sh.hidden);
     a.cols = a.vocab;
     a.m_tiles = static_cast<int>(ceil_div(sh.rows, kTileM));
-    a.n_tiles = static_cast<int>(ceil_div(sh.vocab, kTileN));
     a.k_blocks = static_cast<int>(ceil_div(sh.hidden, kBlockK));
     a.row_box = static_cast<int>(std::min<int64_t>(sh.rows, 128));
     a.eps = sh.eps;
     a.ignore_index = sh.ignore_index;
     a.target = target;
     return a;
+}
+
+// Tiles of z with n columns, over the piece.
+void set_tiles(HeadArgs& a, int n) {
+    a.tile_n = n;
+    a.warp_columns = (n / 2 + 31) / 32 * 32;
+    a.n_tiles = static_cast<int>(ceil_div(a.cols, n));
 }
 
 #define LS_CUDA(expr)                        \
@@ -953,10 +988,11 @@ cudaError_t fwd(float* loss, float* lse, const void* x, const void* w, const int
                            static_cast<const T*>(w), a));
         return launch_pdl(merge_stats_kernel, dim3(1), dim3(256), 0, s, loss, lse, a);
     }
+    set_tiles(a, p.stats_n);
     a.parts = 2 * a.n_tiles;
     HeadMaps maps = {};
     LS_CUDA(make_map<T>(&maps.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
-    LS_CUDA(make_map<T>(&maps.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
+    LS_CUDA(make_map<T>(&maps.b, w, sh.hidden, sh.vocab, sh.hidden, a.tile_n / 2));
     const int64_t units = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
     if (sh.eps > 0.f)
         LS_CUDA((launch_head<T, kStats, true>(maps, a, units, s)));
@@ -992,7 +1028,8 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     a.w_first = p.w_first;
     HeadMaps mz = {}, mo = {};
     LS_CUDA(make_map<T>(&mz.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
-    LS_CUDA(make_map<T>(&mz.b, w, sh.hidden, sh.vocab, sh.hidden, 128));
+    const int grad_n = grad_columns(sh.rows, std::min(p.cols, sh.vocab));
+    LS_CUDA(make_map<T>(&mz.b, w, sh.hidden, sh.vocab, sh.hidden, grad_n / 2));
     LS_CUDA(make_map<T>(&mo.b, w, sh.hidden, sh.vocab, sh.hidden, 64));
     LS_CUDA(make_map<T>(&mo.b2, ws + p.used_x, sh.hidden, sh.rows, sh.hidden, 64));
     if (dx && p.partial_dx)
@@ -1007,7 +1044,7 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
         const int64_t cols = std::min(p.cols, sh.vocab - c);
         a.col0 = static_cast<int>(c);
         a.cols = static_cast<int>(cols);
-        a.n_tiles = static_cast<int>(ceil_div(cols, kTileN));
+        set_tiles(a, grad_n);
         a.x = x;
         a.used_x = dweight && c == 0 ? ws + p.used_x : nullptr;
         LS_CUDA(make_map<T>(&mz.out, g, cols, sh.rows, p.cols, 32));
