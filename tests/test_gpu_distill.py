@@ -189,3 +189,10 @@ def test_nan_among_masked_logits(dtype):
     assert torch.isfinite(loss[4]) and torch.isfinite(lse[4])
     assert torch.isnan(loss[5:7]).all() and torch.isnan(lse[5:7]).all()
     assert torch.isnan(dz[6]).all()
+
+
+@pytest.mark.parametrize("rows,vocab,k", [(3, 8, 1024), (1300, 8, 9), (2, 1073741824 // 512, 3)])
+def test_more_entries_than_vocabulary_and_long_rows(rows, vocab, k):
+    require_gpu()
+    args = inputs(rows, vocab, k, F16, False, 2.0, 8)
+    compare(run(*args, 2.0), args, 2.0, f"{rows}x{vocab} k={k}")

@@ -171,3 +171,17 @@ def test_repeats_bit_for_bit_and_in_a_graph_on_another_stream():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(first[0], y) and torch.equal(first[1], d)
+
+
+def test_widest_hidden():
+    require_gpu()
+    table = torch.randn(7, 65536, device="cuda").half()
+    tok = torch.tensor([3, 3, 6, -1, 0, 3, 6] * 6, device="cuda", dtype=torch.int32)
+    dy = torch.randn(tok.numel(), 65536, device="cuda").half()
+    y, d = torch.empty_like(dy), torch.full((7, 65536), 9.0, device="cuda")
+    ws = ls_vocab.new_workspace(ls_vocab.embedding_lookup_workspace_bytes(tok.numel(), 65536, 7))
+    ls_vocab.ls_embedding_lookup_fwd(y, tok, table, 3.0)
+    ls_vocab.ls_embedding_lookup_bwd(d, dy, tok, 3.0, 6, workspace=ws)
+    ref, bound = vocab_ref.embedding_lookup(table, tok, 3.0, dy, 6)
+    vocab_ref.check(y, ref[0], bound[0], "y")
+    vocab_ref.check(d, ref[1], bound[1], "d_table")

@@ -282,3 +282,10 @@ def test_widths_of_the_forward_tiles(rows, hidden, vocab):
         ref, bound = vocab_ref.linear_cross_entropy(x, w, t, 0.1)
         vocab_ref.check(loss, ref[0], bound[0], f"{rows}x{vocab} loss at {width}")
         vocab_ref.check(lse, ref[1], bound[1], f"{rows}x{vocab} lse at {width}")
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_widest_hidden(rows):
+    require_gpu()
+    x, w, t, d = inputs(rows, 65536, 40, BF16, 21)
+    compare(run(x, w, t, d, 0.1), x, w, t, d, 0.1, "hidden 65536")
