@@ -196,3 +196,22 @@ def test_more_entries_than_vocabulary_and_long_rows(rows, vocab, k):
     require_gpu()
     args = inputs(rows, vocab, k, F16, False, 2.0, 8)
     compare(run(*args, 2.0), args, 2.0, f"{rows}x{vocab} k={k}")
+
+
+@pytest.mark.parametrize("rows,vocab,k", [(1300, 1000, 40), (700, 4096, 256), (3, 131072, 1000), (30, 50264, 600),
+                                          (5, 131072, 1024), (650, 131072, 1024)])
+def test_repeated_entries(rows, vocab, k):
+    """Rows of which every index comes two to five times, in many slices and in one."""
+    require_gpu()
+    z, ix, t, tl, d = inputs(rows, vocab, k, BF16, False, 1.0, 9)
+    some = torch.randint(0, vocab, (rows, k // 3 + 1), device="cuda", dtype=torch.int32)
+    ix = some.gather(1, torch.randint(0, k // 3 + 1, (rows, k), device="cuda")).contiguous()
+    args = (z, ix, t, tl, d)
+    got = run(*args, 1.0)
+    compare(got, args, 1.0, f"{rows}x{vocab} k={k}")
+    for a, b in zip(got, run(*args, 1.0)):
+        assert torch.equal(a, b)
+    if rows < 100:
+        z2 = z.clone()
+        ls_vocab.ls_distill_topk_bwd(z2, z2, ix, t, got[1], tl, d, 1.0)
+        assert torch.equal(z2, got[2])
