@@ -241,8 +241,8 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
 // other way, has left the last ones in L2.
 // Indexes that a row holds twice are found by a hash table, or where the slice is short against k by a bit
 // for each column (8192 x 4096 BF16, k = 256: 68 us with the table, 45 with the bits;
-// 8192 x 1000: 38 and 24).
-// Dynamic shared memory: q, z, ix [k]; then slot [k], hash table, twice [table]; or seen, twice [words].
+// 8192 x 1000: 38 and 23, and 38 where a row has about 30 indexes twice).
+// Dynamic shared memory: q, z, ix, slot [k]; then hash table, twice [table]; or seen, twice [words].
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ index,
@@ -252,14 +252,14 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
     constexpr int U = unroll_bwd<T>();
     extern __shared__ float sm_k[];
     __shared__ float sm_sum;
-    __shared__ int sm_any_twice;
+    __shared__ int sm_repeated;
     float* sm_q = sm_k;
     float* sm_z = sm_k + a.k;
     int* sm_ix = reinterpret_cast<int*>(sm_k + 2 * a.k);
     int* sm_slot = sm_ix + a.k;
     int* sm_table = sm_slot + a.k;
     int* sm_twice = sm_table + a.table;  // [table]: the slot's index came more than once
-    uint32_t* sm_seen = reinterpret_cast<uint32_t*>(sm_slot);
+    uint32_t* sm_seen = reinterpret_cast<uint32_t*>(sm_table);
     uint32_t* sm_more = sm_seen + a.words;  // columns that came more than once
     pdl_enter();
     const int64_t row = gridDim.x - 1 - blockIdx.x;
@@ -309,8 +309,26 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
                 sm_slot[e] = h;
             }
         }
-        any_twice = __any_sync(0xffffffffu, any_twice);
-        if (threadIdx.x == 0) sm_any_twice = any_twice;
+        // The entries whose index came more than once: in order into a list, over the slots that are no
+        // longer needed, and marked by -2 - index.
+        int n = 0;
+        __syncwarp();
+        if (__any_sync(0xffffffffu, any_twice))
+            for (int e0 = 0; e0 < a.k; e0 += 32) {
+                const int e = e0 + threadIdx.x;
+                const int j = e < a.k ? sm_ix[e] : -1;
+                const int c = j - lo * kVec;
+                const bool more =
+                    j >= 0 && (a.table == 0 ? sm_more[c >> 5] >> (c & 31) & 1 : sm_twice[sm_slot[e]]);
+                const unsigned all = __ballot_sync(0xffffffffu, more);
+                if (more) {
+                    sm_ix[e] = -2 - j;
+                    sm_slot[n + __popc(all & ((1u << threadIdx.x) - 1u))] = e;
+                }
+                n += __popc(all);
+                __syncwarp();
+            }
+        if (threadIdx.x == 0) sm_repeated = n;
     };
     const bool in_place = dlogits == logits;
     if (threadIdx.x < 32) {
@@ -375,37 +393,31 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
     }
     if (!some) return;
     __syncthreads();
-    // The entries' columns again, from the FP32 values.  Where a row holds an
-    // index more than once, its first entry writes the sum of their q, added in
-    // entry order by the whole warp.
-    const int lane = threadIdx.x & 31;
-    for (int e0 = threadIdx.x - lane; e0 < a.k; e0 += THREADS) {
-        const int e = e0 + lane;
-        const int j = e < a.k ? sm_ix[e] : -1;
-        bool mine = j >= 0;
-        float q = mine ? sm_q[e] : 0.f;
-        bool more = false;
-        if (sm_any_twice && mine) {
-            const int c = j - lo * kVec;
-            more = a.table == 0 ? sm_more[c >> 5] >> (c & 31) & 1 : sm_twice[sm_slot[e]];
-        }
-        unsigned twice = __ballot_sync(0xffffffffu, more);
-        for (; twice; twice &= twice - 1) {
-            const int l = __ffs(twice) - 1;
-            const int jl = __shfl_sync(0xffffffffu, j, l);
-            float sum = 0.f;
-            bool first = true;
-            for (int f0 = 0; f0 < a.k && first; f0 += 32) {
-                unsigned same = __ballot_sync(0xffffffffu, f0 + lane < a.k && sm_ix[f0 + lane] == jl);
-                if (same && f0 + __ffs(same) - 1 < e0 + l) first = false;
-                for (; same && first; same &= same - 1) sum += sm_q[f0 + __ffs(same) - 1];
-            }
-            if (lane == l) {
-                q = sum;
-                mine = first;
+    // The entries' columns again, from the FP32 values.
+    for (int e = threadIdx.x; e < a.k; e += THREADS) {
+        const int j = sm_ix[e];
+        if (j >= 0) dz[j] = from_f32<T>(g * (Q * prob(sm_z[e]) - sm_q[e]));
+    }
+    // Where a row holds an index more than once, its first entry writes the sum of their q, in entry order.
+    const int n = sm_repeated;
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const int e = sm_slot[i], mark = sm_ix[e];
+        float q = 0.f;
+        bool first = true;
+        for (int m0 = 0; m0 < n && first; m0 += kBatch) {
+            int e2[kBatch], mark2[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) e2[u] = sm_slot[min(m0 + u, n - 1)];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) mark2[u] = sm_ix[e2[u]];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (m0 + u >= n || mark2[u] != mark) continue;
+                first = first && m0 + u >= i;
+                q += sm_q[e2[u]];
             }
         }
-        if (mine) dz[j] = from_f32<T>(g * (Q * prob(sm_z[e]) - q));
+        if (first) dz[-2 - mark] = from_f32<T>(g * (Q * prob(sm_z[e]) - q));
     }
 }
 
@@ -419,7 +431,7 @@ DistillArgs make_args(const DistillShape& sh, int parts) {
     a.table = 2;
     while (a.table < 2 * sh.k) a.table *= 2;
     a.words = (a.slice * kVec + 31) / 32;
-    if (a.words <= std::min(sh.k + 2 * a.table, 4096))  // 45 KB in all at the most
+    if (a.words <= std::min(2 * a.table, 3584))  // 44 KB in all at the most
         a.table = 0;
     else
         a.words = 0;
@@ -475,7 +487,7 @@ cudaError_t bwd(void* dlogits, const void* logits, const int32_t* index, const v
     const int parts = parts_of(sh, sizeof(T) == 4 ? 3648 : 1216, 64);
     const DistillArgs a = make_args(sh, parts);
     const int threads = threads_of(a, sh.rows * parts);
-    const size_t smem = static_cast<size_t>(3 * sh.k + (a.table ? sh.k + 2 * a.table : 2 * a.words)) * 4;
+    const size_t smem = static_cast<size_t>(4 * sh.k + 2 * (a.table ? a.table : a.words)) * 4;
     return launch_pdl(threads == 32    ? distill_bwd_kernel<T, 32>
                       : threads == 128 ? distill_bwd_kernel<T, 128>
                                        : distill_bwd_kernel<T, 256>,
