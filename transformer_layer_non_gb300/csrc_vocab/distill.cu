@@ -236,7 +236,7 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
     }
 }
 
-// CTA (row, slice): the slice's vectors of the row, then the entries that fall
+// A CTA for each slice of each row, a row's side by side: the slice's vectors, then the entries that fall
 // into it.  Rows run from the last to the first: the forward, which runs the
 // other way, has left the last ones in L2.
 // Indexes that a row holds twice are found by a hash table, or where the slice is short against k by a bit
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ index,
                    const T* __restrict__ teacher, const float* __restrict__ lse,
                    const float* __restrict__ teacher_lse, const float* __restrict__ dloss,
-                   const __grid_constant__ DistillArgs a) {
+                   const __grid_constant__ DistillArgs a, int parts) {
     constexpr int U = unroll_bwd<T>();
     extern __shared__ float sm_k[];
     __shared__ float sm_sum;
@@ -262,10 +262,10 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
     uint32_t* sm_seen = reinterpret_cast<uint32_t*>(sm_table);
     uint32_t* sm_more = sm_seen + a.words;  // columns that came more than once
     pdl_enter();
-    const int64_t row = gridDim.x - 1 - blockIdx.x;
+    const int64_t unit = gridDim.x - 1 - blockIdx.x, row = unit / parts;
     const T* z = logits + row * a.vocab;
     T* dz = dlogits + row * a.vocab;
-    const int lo = blockIdx.y * a.slice, hi = min(a.nvec, lo + a.slice);
+    const int lo = static_cast<int>(unit - row * parts) * a.slice, hi = min(a.nvec, lo + a.slice);
     Raw8<T> r[U];
     int v0 = lo + threadIdx.x;
     load_batch<T, U, THREADS>(r, z, v0, hi);
@@ -484,17 +484,22 @@ cudaError_t bwd(void* dlogits, const void* logits, const int32_t* index, const v
                 const DistillShape& sh, cudaStream_t s) {
     // Each slice reads and writes its own columns alone, in place too.  (777 x 32000 FP32: 49 us whole,
     // 40 in four slices; FP16 rows, half as long, gain nothing.)
-    const int parts = parts_of(sh, sizeof(T) == 4 ? 3648 : 1216, 64);
+    int parts = parts_of(sh, sizeof(T) == 4 ? 3648 : 1216, 64);
+    // And none above 32 KB (64 with many entries, which each slice looks through): whole rows in flight on
+    // all SMs spread over so much memory that some placements of the two buffers take 195 us instead of 78
+    // (4096 x 30528 FP16; 76.5 in two slices wherever they lie; 2047 x 131072 BF16: 166 whole, 157 in eight).
+    const int64_t most = (sh.k > 128 ? 65536 : 32768) / (kVec * static_cast<int64_t>(sizeof(T)));
+    while (sh.vocab / kVec > parts * most) parts *= 2;
     const DistillArgs a = make_args(sh, parts);
     const int threads = threads_of(a, sh.rows * parts);
     const size_t smem = static_cast<size_t>(4 * sh.k + 2 * (a.table ? a.table : a.words)) * 4;
     return launch_pdl(threads == 32    ? distill_bwd_kernel<T, 32>
                       : threads == 128 ? distill_bwd_kernel<T, 128>
                                        : distill_bwd_kernel<T, 256>,
-                      dim3(static_cast<unsigned>(sh.rows), static_cast<unsigned>(parts)),
+                      dim3(static_cast<unsigned>(sh.rows * parts)),
                       dim3(threads), smem, s,
                       static_cast<T*>(dlogits), static_cast<const T*>(logits), index,
-                      static_cast<const T*>(teacher), lse, teacher_lse, dloss, a);
+                      static_cast<const T*>(teacher), lse, teacher_lse, dloss, a, parts);
 }
 
 }  // namespace
