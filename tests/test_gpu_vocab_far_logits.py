@@ -1,0 +1,71 @@
+"""The vocabulary operators on logits far from zero: large finite values as masks in a part of a
+row and in the whole of it, in every storage type, and temperatures that bring ordinary logits there;
+against the 64-bit implementation of tests/vocab_ref.py or, where an FP32 lse cannot hold more
+than the row's maximum, against what follows from that."""
+import pytest
+
+torch = pytest.importorskip("torch")
+from tests import vocab_ref  # noqa: E402
+from tests.gpu_util import require_gpu  # noqa: E402
+from tests.test_gpu_distill import compare, inputs, run  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+MASKS = [(F16, -65504.0), (F16, -32752.0)] + [
+    (t, m) for t in (BF16, F32) for m in (-1e6, -1e10, -1e20, -1e30, torch.finfo(t).min / 2)]
+
+
+def masked(rows, vocab, live, k, dtype, tau, seed):
+    """Inputs whose entries all lie in the first `live` columns (or outside the row)."""
+    z, ix, t, tl, d = inputs(rows, vocab, k, dtype, False, tau, seed)
+    ix = torch.where((ix >= 0) & (ix < vocab), ix % live, ix)
+    return z, ix, t, tl, d
+
+
+@pytest.mark.parametrize("dtype,mask", MASKS)
+@pytest.mark.parametrize("tau", [0.25, 0.5, 1.0, 4.0])
+@pytest.mark.parametrize("rows,vocab,live", [(8, 50264, 4096), (700, 2056, 64), (5, 1000, 8)])
+def test_distill_rows_with_a_finite_mask(dtype, mask, tau, rows, vocab, live):
+    """Threads that see masked values alone add nothing to the row, and spoil nothing in it."""
+    require_gpu()
+    z, ix, t, tl, d = masked(rows, vocab, live, 5, dtype, tau, 1)
+    z[:, live:] = mask
+    z[4, live // 2:] = mask
+    ix[4] %= live // 2
+    args = (z, ix, t, tl, d)
+    got = run(*args, tau)
+    compare(got, args, tau, f"{dtype} mask {mask} tau {tau}")
+    assert (got[2][:, live:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,mask", [m for m in MASKS if m[1] <= -1e10])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 4.0])
+@pytest.mark.parametrize("rows,vocab", [(8, 50264), (700, 2056)])
+def test_lse_of_rows_of_one_finite_mask(dtype, mask, tau, rows, vocab):
+    """z / tau is exact here, and log(vocab) < 11 is below half of its last place (512 at the least): the
+    FP32 lse of such a row is z / tau itself."""
+    require_gpu()
+    z, ix, t, tl, d = masked(rows, vocab, vocab, 5, dtype, tau, 2)
+    z[4:6] = mask
+    _, lse, _ = run(z, ix, t, tl, d, tau)
+    assert torch.equal(lse[4:6], z[4:6, 0].float() / tau)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("tau", [2.0 ** -60, 2.0 ** -40, 2.0 ** -30, 2.0 ** -20])
+@pytest.mark.parametrize("rows,vocab", [(4, 50264), (700, 264)])
+def test_distill_forward_at_small_temperatures(dtype, tau, rows, vocab):
+    """Both distributions are all on their largest logit: the log-sum-exp is z_max / tau and the loss
+    tau (z_max - z[the teacher's first choice]), each with an FP32 product or two of rounding."""
+    require_gpu()
+    z, ix, t, tl, d = inputs(rows, vocab, 5, dtype, False, 1.0, 3)
+    z.clamp_(-20.0, 20.0)
+    z[:, 17] = 30.0
+    ix = torch.randint(0, vocab, ix.shape, device="cuda", dtype=torch.int32)
+    t = torch.randn(t.shape, device="cuda").to(dtype).clamp_(-8.0, 8.0)
+    t[:, 1] = 10.0
+    loss, lse, _ = run(z, ix, t, tl, d, tau)
+    assert torch.equal(lse, torch.full_like(lse, 30.0 / tau))
+    want = tau * (30.0 - z.gather(1, ix[:, 1:2].long())[:, 0].double())
+    # loss = tau^2 (q (log q - z / tau) + lse), the terms of up to 30 / tau each
+    vocab_ref.check(loss, want, tau * 50.0 * 4 * 2.0 ** -24, "loss")

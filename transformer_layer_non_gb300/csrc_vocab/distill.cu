@@ -29,6 +29,11 @@ namespace ls {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// exp((z - m) / tau) = 2^(z c - m c), c = log2(e) / tau, by one FMA as long as the rounding of m c, at most
+// 2^-24 of it, is harmless: below 2^17 (FP16's lowest value at tau = 1) it is at most 2^-8, less than the
+// rounding of the row's FP32 lse.  At 1e10 it is hundreds, and the exponential of the maximum itself, which is
+// 1, would be infinite or 0.
+constexpr float kMostFma = 131072.f;
 // Vectors per thread in flight.
 template <typename T> constexpr int unroll_fwd() { return sizeof(T) == 2 ? 6 : 3; }
 template <typename T> constexpr int unroll_bwd() { return sizeof(T) == 2 ? 8 : 4; }
@@ -175,7 +180,7 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
             m = bm;
         }
         const float mc = m * a.c;
-        const bool tame = fabsf(mc) < INFINITY;
+        const bool tame = fabsf(mc) < kMostFma;
         const float2 mm = make_float2(-mc, -mc);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -190,7 +195,7 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
                     const float2 t = fma2(make_float2(f[j], f[j + 1]), cc, mm);
                     l2 = add2(l2, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
                 }
-            } else {  // m c is infinite (FP32's lowest values as a mask), or m is: -inf adds nothing, a NaN stays
+            } else {  // large finite values as a mask (m c may overflow), or m is infinite: -inf adds nothing, a NaN stays
                 for (int j = 0; j < kVec; ++j)
                     if (f[j] != -INFINITY) l2.x += exp2_approx((f[j] - m) * a.c);
             }
