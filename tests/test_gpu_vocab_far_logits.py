@@ -8,6 +8,7 @@ torch = pytest.importorskip("torch")
 from tests import vocab_ref  # noqa: E402
 from tests.gpu_util import require_gpu  # noqa: E402
 from tests.test_gpu_distill import compare, inputs, run  # noqa: E402
+from transformer_layer_non_gb300 import ls_vocab  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
@@ -69,3 +70,50 @@ def test_distill_forward_at_small_temperatures(dtype, tau, rows, vocab):
     want = tau * (30.0 - z.gather(1, ix[:, 1:2].long())[:, 0].double())
     # loss = tau^2 (q (log q - z / tau) + lse), the terms of up to 30 / tau each
     vocab_ref.check(loss, want, tau * 50.0 * 4 * 2.0 ** -24, "loss")
+
+
+def all_on_the_maximum(z, ix, t, d, tau):
+    """dlogits and their bound where p is 1 at each of the row's maxima and 0 elsewhere, which is what an
+    lse equal to z_max / tau says."""
+    p = (z == z.amax(1, keepdim=True)).double()
+    q = torch.softmax(t.double() / tau, 1)
+    dense = torch.zeros_like(p).scatter_add_(1, ix.long(), q)
+    c = (tau * d.double())[:, None]
+    want = c * (p - dense)
+    # q from FP32 exponentials (arguments of up to 2^7 to 2^-17) and sums of 5
+    bound = c * (p + dense) * 2.0 ** -16 + vocab_ref.half_step(z.dtype) * want.abs() + vocab_ref.TINY[z.dtype]
+    return want, bound
+
+
+@pytest.mark.parametrize("dtype,mask", [m for m in MASKS if m[1] <= -1e10])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 4.0])
+@pytest.mark.parametrize("rows,vocab", [(8, 50264), (700, 2056)])
+def test_gradient_of_rows_of_one_finite_mask(dtype, mask, tau, rows, vocab):
+    """The FP32 lse of such a row is z / tau, so that its backward's probabilities are 1."""
+    require_gpu()
+    z, ix, t, tl, d = masked(rows, vocab, vocab, 5, dtype, tau, 2)
+    z[4:6] = mask
+    _, lse, dz = run(z, ix, t, tl, d, tau)
+    assert torch.equal(lse[4:6], z[4:6, 0].float() / tau)
+    want, bound = all_on_the_maximum(z[4:6], ix[4:6], t[4:6], d[4:6], tau)
+    vocab_ref.check(dz[4:6], want, bound, f"{dtype} {mask}")
+    assert torch.isfinite(dz).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tau", [2.0 ** -60, 2.0 ** -40, 2.0 ** -30, 2.0 ** -20])
+@pytest.mark.parametrize("rows,vocab", [(4, 50264), (700, 264)])
+def test_distill_gradient_at_small_temperatures(dtype, tau, rows, vocab):
+    require_gpu()
+    z, ix, t, tl, d = inputs(rows, vocab, 5, dtype, False, 1.0, 4)
+    z.clamp_(-20.0, 20.0)
+    z[:, 17] = 30.0
+    ix = torch.randint(0, vocab, ix.shape, device="cuda", dtype=torch.int32)
+    ix[0, 1] = 17
+    t = torch.randn(t.shape, device="cuda").to(dtype).clamp_(-8.0, 8.0)
+    t[:, 1] = 10.0
+    _, lse, dz = run(z, ix, t, tl, d, tau)
+    vocab_ref.check(dz, *all_on_the_maximum(z, ix, t, d, tau), "dlogits")
+    z2 = z.clone()
+    ls_vocab.ls_distill_topk_bwd(z2, z2, ix, t, lse, tl, d, tau)
+    assert torch.equal(z2, dz)

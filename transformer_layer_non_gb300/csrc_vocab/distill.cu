@@ -360,10 +360,10 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
     const float Q = sm_sum;
     const float gq = g * Q;
     const bool some = Q != 0.f;
-    // exp(z / tau - lse) by one FMA, unless the FMA's terms overflow (FP32's
-    // lowest values in a whole row).
+    // exp(z / tau - lse) by one FMA, unless lse is too far from zero for that (large finite values in a
+    // whole row); the difference is then at most 0, because the forward's lse is no less than z / tau.
     const float ll = row_lse * kLog2e;
-    const bool tame = fabsf(ll) < INFINITY;
+    const bool tame = fabsf(ll) < kMostFma;
     auto prob = [&](float f) {
         return exp2_approx(tame ? fmaf(f, a.c, -ll) : (f / a.tau - row_lse) * kLog2e);
     };
