@@ -117,3 +117,36 @@ def test_distill_gradient_at_small_temperatures(dtype, tau, rows, vocab):
     z2 = z.clone()
     ls_vocab.ls_distill_topk_bwd(z2, z2, ix, t, lse, tl, d, tau)
     assert torch.equal(z2, dz)
+
+
+@pytest.mark.parametrize("dtype,mask", [m for m in MASKS if m[1] <= -1e10])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 4.0])
+@pytest.mark.parametrize("rows,vocab", [(8, 50264), (700, 2056)])
+def test_loss_of_rows_of_one_finite_mask(dtype, mask, tau, rows, vocab):
+    """lse is z / tau, so that log p is 0 and the loss tau^2 sum q log q."""
+    require_gpu()
+    z, ix, t, tl, d = masked(rows, vocab, vocab, 5, dtype, tau, 2)
+    z[4:6] = mask
+    loss, _, _ = run(z, ix, t, tl, d, tau)
+    q = torch.softmax(t[4:6].double() / tau, 1)
+    want = tau * tau * (q * q.log()).sum(1)
+    vocab_ref.check(loss[4:6], want, tau * tau * 2.0 ** -16, f"{dtype} {mask}")
+    assert torch.isfinite(loss).all()
+
+
+@pytest.mark.parametrize("dtype,offset", [(F16, 2000.0), (F32, 2000.0), (F32, 20000.0), (F32, -20000.0)])
+@pytest.mark.parametrize("tau", [1.0, 2.0])
+@pytest.mark.parametrize("k", [3, 32, 200, 1024])
+def test_loss_of_rows_with_an_offset(dtype, offset, tau, k):
+    """An offset of all logits costs the loss the rounding of lse, half a step of |offset / tau|, and
+    not one of a sum over the entries besides."""
+    require_gpu()
+    z, ix, t, tl, d = inputs(40, 2056, k, dtype, False, tau, 5)
+    z += offset
+    loss, _, _ = run(z, ix, t, tl, d, tau)
+    (want, _, _), (bound, _, _) = vocab_ref.distill(z.double() - offset, ix, t, tl, tau)
+    # lse in FP32: its own rounding, that of z_max / tau is exact here, and l's from a product of
+    # |offset| log2(e) / tau, rounded to half a step
+    lse = 3 * abs(offset) / tau * 2.0 ** -24
+    some = (ix >= 0).any(1)
+    vocab_ref.check(loss, want, bound + tau * tau * lse * some, f"{dtype} offset {offset}")

@@ -15,9 +15,12 @@
 // forward, any number of slices in the backward, which needs no merging.
 //
 // The k entries are a few hundred bytes.  Warp 0 works them out by shuffles
-// while the row's first vectors are on their way to all warps; with
-//   A = sum_e q_e (log q_e - z_index(e) / tau)   the forward's   loss = tau^2 (A + Q lse)
-// needs one barrier, the merging of the warps' sums.
+// while the row's first vectors are on their way to all warps:
+//   E = sum_e q_e log q_e,   and q_e and z_index(e) / tau for the end, where
+//   loss = tau^2 (E + sum_e q_e (lse - z_index(e) / tau))
+// needs one barrier, the merging of the warps' sums.  (With the sum of
+// q_e z_index(e) / tau taken beforehand the loss would be a difference of two
+// numbers of lse's size: 1e23 instead of 2 in a row of logits near -1e30.)
 #include <math.h>
 
 #include <algorithm>
@@ -128,7 +131,7 @@ __device__ __forceinline__ void load_batch(Raw8<T> (&r)[U], const T* z, int v0, 
     }
 }
 
-// Dynamic shared memory: logq [k], ix [k].
+// Dynamic shared memory: sm_q [k], sm_ix [k].
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
@@ -147,22 +150,29 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
     Raw8<T> r[U];
     int v0 = lo + threadIdx.x;
     load_batch<T, U, THREADS>(r, z, v0, hi);
-    float A = 0.f, Q = 0.f;
+    float E = 0.f, Q = 0.f;
+    float* sm_q = sm_k;                              // log q, then q
+    int* sm_ix = reinterpret_cast<int*>(sm_k + a.k);  // the index, then the bits of the student's z / tau there
     if (rank == 0 && threadIdx.x < 32) {
-        float* logq = sm_k;
-        int* ix = reinterpret_cast<int*>(sm_k + a.k);
-        load_entries(logq, ix, index, teacher, teacher_lse, row, a);
+        load_entries(sm_q, sm_ix, index, teacher, teacher_lse, row, a);
         __syncwarp();
-        for (int e0 = threadIdx.x; e0 < a.k; e0 += 32 * kBatch) {
+        for (int b = 0; b < a.k; b += 32 * kBatch) {
+            const int e0 = b + threadIdx.x;
             float f[kBatch];
-            gather(f, z, ix, e0, a.k);
+            gather(f, z, sm_ix, e0, a.k);
+            __syncwarp();  // it reads the last index for entries behind it, too
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int e = e0 + 32 * u;
-                if (e >= a.k || ix[e] < 0) continue;
-                const float q = expf(logq[e]);
-                Q += q;
-                A += q * (logq[e] - f[u] / a.tau);
+                if (e >= a.k) continue;
+                float q = 0.f;
+                if (sm_ix[e] >= 0) {
+                    q = expf(sm_q[e]);
+                    Q += q;
+                    E += q * sm_q[e];
+                }
+                sm_q[e] = q;
+                sm_ix[e] = __float_as_int(f[u] / a.tau);
             }
         }
     }
@@ -232,11 +242,13 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
         cluster_sync();  // a CTA's shared memory lives until the first one has read it
         if (rank != 0 || threadIdx.x >= 32) return;
     }
-    A = group_sum<32>(A);
+    const float lse = m / a.tau + logf(l);
+    for (int e = threadIdx.x; e < a.k; e += 32)  // its own entries
+        if (sm_q[e] != 0.f) E += sm_q[e] * (lse - __int_as_float(sm_ix[e]));
+    E = group_sum<32>(E);
     Q = group_sum<32>(Q);
     if (threadIdx.x == 0) {
-        const float lse = m / a.tau + logf(l);
-        loss[row] = Q == 0.f ? 0.f : a.tau * a.tau * (A + Q * lse);
+        loss[row] = Q == 0.f ? 0.f : a.tau * a.tau * E;
         if (lse_out) lse_out[row] = lse;
     }
 }
