@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 from tests import vocab_ref  # noqa: E402
 from tests.gpu_util import require_gpu  # noqa: E402
+from tests import test_gpu_linear_cross_entropy as head  # noqa: E402
 from tests.test_gpu_distill import compare, inputs, run  # noqa: E402
 from transformer_layer_non_gb300 import ls_vocab  # noqa: E402
 
@@ -150,3 +151,60 @@ def test_loss_of_rows_with_an_offset(dtype, offset, tau, k):
     lse = 3 * abs(offset) / tau * 2.0 ** -24
     some = (ix >= 0).any(1)
     vocab_ref.check(loss, want, bound + tau * tau * lse * some, f"{dtype} offset {offset}")
+
+
+def head_inputs(rows, hidden, vocab, dtype, seed):
+    """Positive hidden states, so that one entry's weight of a large constant is one large logit of its sign."""
+    x, w, t, d = head.inputs(rows, hidden, vocab, dtype, seed)
+    return (x.abs() + 0.125).to(dtype), w, t, d
+
+
+@pytest.mark.parametrize("dtype,mask", [(F16, -65504.0), (F16, -30000.0), (BF16, -1e5), (BF16, -1e10), (BF16, -1e30),
+                                        (BF16, -1e36)])
+@pytest.mark.parametrize("rows", [1, 5, 130, 300])
+def test_vocabulary_entries_of_large_negative_logits(dtype, mask, rows):
+    """Padded entries of a vocabulary: whole groups of columns, at its end and inside, have the probability 0."""
+    require_gpu()
+    x, w, t, d = head_inputs(rows, 64, 1000, dtype, 6)
+    w[256:600] = mask
+    w[961:] = mask
+    t = torch.where((t >= 256) & (t < 1000), t % 256, t)
+    got = head.run(x, w, t, d)
+    head.compare(got, x, w, t, d, 0.0, f"{dtype} {mask} {rows}")
+    assert (got[3][256:600] == 0).all() and (got[3][961:] == 0).all()
+    # the other entries' values are those of a vocabulary without these
+    keep = torch.cat([w[:256], w[600:961]])
+    t2 = torch.where((t >= 600) & (t < 1000), t - 344, torch.where(t >= 1000, -100, t))
+    ref, bound = vocab_ref.linear_cross_entropy(x, keep, t2, 0.0, -100, d)
+    for g, r, b in zip(got[:3], ref, bound):
+        vocab_ref.check(g, r, b, f"{dtype} {mask} {rows}")
+
+
+@pytest.mark.parametrize("value", [-1e10, -1e30, 1e10, 1e30])
+@pytest.mark.parametrize("rows", [1, 5, 130])
+def test_all_logits_far_from_zero(value, rows):
+    """Rows of one large finite logit have finite outputs: lse is that logit, and p at most 1."""
+    require_gpu()
+    x, w, t, d = head_inputs(rows, 64, 1000, BF16, 7)
+    w[:] = value
+    loss, lse, dx, dw = head.run(x, w, t, d)
+    z = x.double().sum(1) * w[0, 0].double()
+    assert ((lse - z).abs() <= 64 * 2.0 ** -23 * z.abs()).all()
+    # the target's logit and lse: the same sum of the same products
+    assert (loss == 0).all()
+    assert torch.isfinite(dw).all()
+    # |g| <= dloss for each entry, and the row's sum of them times the value
+    assert (dx.double().abs() <= (d.double() * 1000 * abs(w[0, 0].double()) * 1.01)[:, None]).all()
+
+
+@pytest.mark.parametrize("rows", [2, 130])
+def test_one_logit_far_above(rows):
+    require_gpu()
+    x, w, t, d = head_inputs(rows, 64, 1000, BF16, 8)
+    w[7] = 1e10
+    t[0] = 7
+    loss, lse, dx, dw = head.run(x, w, t, d)
+    z = x.double().sum(1) * w[7, 0].double()
+    assert ((lse - z).abs() <= 64 * 2.0 ** -23 * z.abs()).all()
+    assert loss[0] == 0 and (dx[0] == 0).all()
+    assert all(torch.isfinite(a).all() for a in (loss, dx, dw))

@@ -39,6 +39,10 @@ namespace ls {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// exp(z - m) = 2^(z log2(e) - m log2(e)) by one FMA as long as the rounding of m log2(e), at most 2^-24 of it,
+// is harmless: below 2^17 it is at most 2^-8, less than the rounding of the row's FP32 lse.  At 1e10 it is
+// hundreds, and the exponential of the maximum itself, which is 1, would be infinite or 0.
+constexpr float kMostFma = 131072.f;
 
 constexpr int kTileM = 256;   // of a pair; 128 rows for each CTA
 constexpr int kTileN = 256;
@@ -212,7 +216,12 @@ __device__ __forceinline__ void add_stats(float (&z)[32], int n, float& m, float
         l = mul2(l, make_float2(f, f));
         m = cm;
     }
-    const float mc = m == -INFINITY ? 0.f : -m * kLog2e;  // nothing but -inf (or NaN) so far
+    float mc = m == -INFINITY ? 0.f : -m * kLog2e;  // nothing but -inf (or NaN) so far
+    if (fabsf(mc) > kMostFma) {  // the difference first
+        mc = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] -= m;
+    }
     const float2 cc = make_float2(kLog2e, kLog2e), mm = make_float2(mc, mc);
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
@@ -223,7 +232,13 @@ __device__ __forceinline__ void add_stats(float (&z)[32], int n, float& m, float
 
 // 32 values of a row of g: d (exp(z - lse) - q0 - [j == at] (1 - eps)).
 template <bool HIT>
-__device__ __forceinline__ void grads_of(float (&z)[32], float d, float ml, float q0, float qy, int at) {
+__device__ __forceinline__ void grads_of(float (&z)[32], float d, float lse, float q0, float qy, int at) {
+    float ml = -lse * kLog2e;
+    if (fabsf(ml) > kMostFma) {  // the difference first; it is at most 0 but for the rounding of z and lse
+        ml = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = z[j] > lse ? 0.f : z[j] - lse;
+    }
     const float2 cc = make_float2(kLog2e, kLog2e), mm = make_float2(ml, ml);
     const float2 dd = make_float2(d, d), dq = make_float2(-d * q0, -d * q0);
 #pragma unroll
@@ -512,16 +527,15 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 const bool used = there && used_target(y, a);
                 const int at = used ? y - a.col0 - n0 : -1;
                 const float d = used ? row_dloss * scale.x : 0.f;
-                const float ml = -row_lse * kLog2e;
                 const float q0 = a.eps / static_cast<float>(a.vocab), qy = 1.f - a.eps;
                 sweep(cols, release, [&](int c, float (&z)[32]) {
                     if (c * 32 >= n) return;
                     if ((c & 1) == 0) open_box();
                     const int rel = at - c * 32;
                     if (__any_sync(0xffffffffu, rel >= 0 && rel < 32))
-                        grads_of<true>(z, d, ml, q0, qy, rel);
+                        grads_of<true>(z, d, row_lse, q0, qy, rel);
                     else
-                        grads_of<false>(z, d, ml, q0, qy, rel);
+                        grads_of<false>(z, d, row_lse, q0, qy, rel);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint4 v = pack8<T>(z, 8 * j, 1.f);
