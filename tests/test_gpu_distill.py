@@ -215,3 +215,21 @@ def test_repeated_entries(rows, vocab, k):
         z2 = z.clone()
         ls_vocab.ls_distill_topk_bwd(z2, z2, ix, t, got[1], tl, d, 1.0)
         assert torch.equal(z2, got[2])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,vocab,k", [(1, 131072, 1024), (7, 524288, 300), (300, 50264, 64)])
+def test_in_place_in_many_slices(dtype, rows, vocab, k):
+    """Entries in every slice of a row, at the slices' borders among them: in place the same bits as beside it."""
+    require_gpu()
+    z, ix, t, tl, d = inputs(rows, vocab, k, dtype, True, 2.0, 10)
+    step = vocab // 64
+    ix[0, :63] = torch.arange(1, 64, device="cuda", dtype=torch.int32) * step - (
+        torch.arange(1, 64, device="cuda", dtype=torch.int32) % 2)
+    args = (z, ix, t, tl, d)
+    got = run(*args, 2.0)
+    compare(got, args, 2.0, f"{rows}x{vocab} k={k}")
+    for _ in range(5):
+        z2 = z.clone()
+        ls_vocab.ls_distill_topk_bwd(z2, z2, ix, t, got[1], tl, d, 2.0)
+        assert torch.equal(z2, got[2])

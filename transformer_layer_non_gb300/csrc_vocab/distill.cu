@@ -64,12 +64,15 @@ __device__ __forceinline__ void merge(float& m, float& l, float m2, float l2, fl
 
 constexpr int kBatch = 4;  // entries per lane whose loads are in flight together
 
-// The student's logits at a lane's entries e0, e0 + 32, ... (0 where ix is -1 or the entry does not exist).
+// The student's logits at a lane's entries e0, e0 + 32, ..., 0 where the index is not in [lo, hi) (or -1).
 template <typename T>
-__device__ __forceinline__ void gather(float (&f)[kBatch], const T* z, const int* ix, int e0, int k) {
+__device__ __forceinline__ void gather(float (&f)[kBatch], const T* z, const int* ix, int e0, int k, int lo, int hi) {
     T w[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) w[u] = z[max(0, ix[min(e0 + 32 * u, k - 1)])];
+    for (int u = 0; u < kBatch; ++u) {
+        const int j = ix[min(e0 + 32 * u, k - 1)];
+        w[u] = j >= lo && j < hi ? z[j] : from_f32<T>(0.f);
+    }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) f[u] = to_f32(w[u]);
 }
@@ -159,7 +162,7 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
         for (int b = 0; b < a.k; b += 32 * kBatch) {
             const int e0 = b + threadIdx.x;
             float f[kBatch];
-            gather(f, z, sm_ix, e0, a.k);
+            gather(f, z, sm_ix, e0, a.k, 0, static_cast<int>(a.vocab));
             __syncwarp();  // it reads the last index for entries behind it, too
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
@@ -288,12 +291,13 @@ distill_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ inde
     load_batch<T, U, THREADS>(r, z, v0, hi);
     const float row_lse = lse[row];
     const float g = a.tau * (dloss ? dloss[row] : 1.f);
-    // Warp 0: the slice's entries' logits, and the hash table of their indexes.
+    // Warp 0: the slice's entries' logits, and the hash table of their indexes.  Logits of other slices are
+    // not read: in place, their CTAs may have written gradients over them.
     auto place_entries = [&]() {
         bool any_twice = false;
         for (int e0 = threadIdx.x; e0 < a.k; e0 += 32 * kBatch) {
             float f[kBatch];
-            gather(f, z, sm_ix, e0, a.k);
+            gather(f, z, sm_ix, e0, a.k, lo * kVec, hi * kVec);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int e = e0 + 32 * u;
