@@ -15,7 +15,7 @@
  * `stream`, argument errors returned before anything is enqueued), and:
  *  - Storage may also be BF16 (LS_BF16).
  *  - int32 arrays (targets, tokens, teacher indices) and FP32 per-row arrays
- *    need 4-byte alignment only.
+ *    need 4-byte alignment only, teacher logits that of their element.
  *  - No output may overlap an input, another output or the workspace, except
  *    where an entry point says so.
  *  - A workspace is scratch: it needs no initialisation and holds nothing

@@ -233,3 +233,15 @@ def test_in_place_in_many_slices(dtype, rows, vocab, k):
         z2 = z.clone()
         ls_vocab.ls_distill_topk_bwd(z2, z2, ix, t, got[1], tl, d, 2.0)
         assert torch.equal(z2, got[2])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_teacher_rows_of_an_odd_k(dtype):
+    """A view of the teacher's entries that starts at an odd row is aligned to its elements alone."""
+    require_gpu()
+    z, ix, t, tl, d = inputs(10, 1000, 3, dtype, True, 2.0, 11)
+    whole = run(z, ix, t, tl, d, 2.0)
+    for first in (1, 5):
+        part = run(z[first:], ix[first:], t[first:], tl[first:], d[first:], 2.0)
+        for a, b in zip(whole, part):
+            assert torch.equal(a[first:], b)

@@ -130,6 +130,16 @@ def test_distill_refusals_of_one_direction():
     assert distill_fwd(rows=0, loss=None) == distill_bwd(rows=0, dz=None) == ls_ops.LS_OK
 
 
+def test_distill_teacher_logits_need_their_elements_alignment():
+    """A 16-bit view may start at any row of an odd k.  (The next pointer's refusal shows that they passed.)"""
+    for call_ in (distill_fwd, distill_bwd):
+        for dt, step in ((F16, 2), (BF16, 2), (F32, 4)):
+            assert call_(dt=dt, t=P[4] + step, tl=P[5] + 1) == MISALIGNED
+            assert "teacher_lse" in ls_vocab.last_error()
+            assert call_(dt=dt, t=P[4] + step // 2) == MISALIGNED
+            assert "teacher_logits" in ls_vocab.last_error()
+
+
 def lookup_fwd(dt=F16, y=P[0], tok=P[1], e=P[2], n=16, hidden=64, vocab=100, scale=1.0):
     return call("ls_embedding_lookup_fwd", dt, y, tok, e, n, hidden, vocab, scale, None)
 

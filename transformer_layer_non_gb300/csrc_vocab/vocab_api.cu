@@ -18,14 +18,18 @@ ls_status check_storage(const char* fn, ls_dtype dt, bool f32_too) {
                 static_cast<int>(dt));
 }
 
-ls_status check_ptr4(const void* p, const char* name, bool required) {
+ls_status check_ptr_n(const void* p, const char* name, bool required, size_t bytes) {
     if (!p) {
         if (required) return fail(LS_ERR_INVALID_ARGUMENT, "%s is NULL", name);
         return LS_OK;
     }
-    if (reinterpret_cast<uintptr_t>(p) & 3u)
-        return fail(LS_ERR_MISALIGNED, "%s is not 4-byte aligned", name);
+    if (reinterpret_cast<uintptr_t>(p) & (bytes - 1))
+        return fail(LS_ERR_MISALIGNED, "%s is not %zu-byte aligned", name, bytes);
     return LS_OK;
+}
+
+ls_status check_ptr4(const void* p, const char* name, bool required) {
+    return check_ptr_n(p, name, required, 4);
 }
 
 // A size in [lo, hi].
@@ -207,7 +211,7 @@ ls_status ls_distill_topk_fwd(ls_dtype dtype, float* loss, float* lse, const voi
     LS_TRY(check_ptr4(lse, "lse", false));
     LS_TRY(check_ptr(logits, "logits", true));
     LS_TRY(check_ptr4(teacher_index, "teacher_index", true));
-    LS_TRY(check_ptr4(teacher_logits, "teacher_logits", true));
+    LS_TRY(check_ptr_n(teacher_logits, "teacher_logits", true, elem_size(dtype)));
     LS_TRY(check_ptr4(teacher_lse, "teacher_lse", false));
     const size_t rb = static_cast<size_t>(rows) * 4, es = elem_size(dtype);
     const Span outs[] = {{"loss", loss, rb}, {"lse", lse, rb}};
@@ -233,7 +237,7 @@ ls_status ls_distill_topk_bwd(ls_dtype dtype, void* dlogits, const void* logits,
     LS_TRY(check_ptr(dlogits, "dlogits", true));
     LS_TRY(check_ptr(logits, "logits", true));
     LS_TRY(check_ptr4(teacher_index, "teacher_index", true));
-    LS_TRY(check_ptr4(teacher_logits, "teacher_logits", true));
+    LS_TRY(check_ptr_n(teacher_logits, "teacher_logits", true, elem_size(dtype)));
     LS_TRY(check_ptr4(lse, "lse", true));
     LS_TRY(check_ptr4(teacher_lse, "teacher_lse", false));
     LS_TRY(check_ptr4(dloss, "dloss", false));
