@@ -76,8 +76,11 @@ struct HeadArgs {
     int x_units, w_units;  // units of dx and of dweight in a slice
     int units;             // in all
     int x_m_tiles, h_tiles;
-    int x_k_blocks, slice_blocks, w_k_blocks;
+    int x_k_blocks, slice_blocks;
+    int w_kb0, w_k_blocks;  // the rows that dweight's sums run over in this launch
+    int w_row;              // row of `out2` that the piece's first entry has
     bool by_slice, w_first, x_partial, x_add, w_f32;
+    bool w_partial, w_add;  // dweight's sums go to FP32 scratch, without the scale; they are added to what is there
     // kStats
     int parts;             // partial statistics of a row: two for each tile, or one for each CTA
     float2* part;          // [rows][parts]: maximum, sum of exponentials
@@ -165,7 +168,7 @@ template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const HeadArg
         t.m0 = (r / a.h_tiles) * kTileM;
         if (t.weight) {
             t.m0 += t.kb0 * kBlockK;
-            t.kb0 = 0;
+            t.kb0 = a.w_kb0;
             t.kbs = a.w_k_blocks;
         } else {
             t.kbs = min(a.slice_blocks, a.x_k_blocks - t.kb0);
@@ -547,8 +550,8 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         });
                 });
             } else {
-                const bool f32 = t.weight ? a.w_f32 : a.x_partial;
-                const float sc = t.weight || !a.x_partial ? scale.y : 1.f;
+                const bool f32 = t.weight ? a.w_f32 || a.w_partial : a.x_partial;
+                const float sc = (t.weight ? a.w_partial : a.x_partial) ? 1.f : scale.y;
                 const int n = a.hidden - n0;
                 const bool stores = row0 < (t.weight ? a.cols : a.rows);
                 if (f32)
@@ -561,8 +564,10 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                                   f2u4(make_float4(z[4 * j] * sc, z[4 * j + 1] * sc, z[4 * j + 2] * sc,
                                                    z[4 * j + 3] * sc)));
                         close_box([&] {
-                            if (stores && t.weight)
-                                tma_add_2d(&maps.out2, n0 + c * 32, a.col0 + row0, box);
+                            if (stores && t.weight && a.w_add)
+                                tma_add_2d(&maps.out2, n0 + c * 32, a.w_row + row0, box);
+                            else if (stores && t.weight)
+                                tma_store_2d(&maps.out2, n0 + c * 32, a.w_row + row0, box);
                             else if (stores && a.x_add)
                                 tma_add_3d(&maps.out, n0 + c * 32, row0, t.slice, box);
                             else if (stores)
@@ -578,7 +583,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         if ((c & 1) == 1 || c * 32 + 32 >= n)
                             close_box([&] {
                                 if (stores && t.weight)
-                                    tma_store_2d(&maps.out2, n0 + (c & ~1) * 32, a.col0 + row0, box);
+                                    tma_store_2d(&maps.out2, n0 + (c & ~1) * 32, a.w_row + row0, box);
                                 else if (stores)
                                     tma_store_2d(&maps.out, n0 + (c & ~1) * 32, row0, box);
                             });
@@ -775,7 +780,7 @@ __global__ void __launch_bounds__(1024) grad_scale_kernel(const __grid_constant_
     }
 }
 
-// dx = scale * sum over the slices' partial sums, in slice order.
+// dx (or a piece of dweight) = scale * sum over the slices' partial sums, in slice order.
 template <typename T>
 __global__ void __launch_bounds__(256)
 join_slices_kernel(T* __restrict__ dx, const float* __restrict__ part, int slices, int64_t nvec,
@@ -806,6 +811,12 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr int64_t kPieceBytes = int64_t{128} << 20;
 constexpr int64_t kMaxSlices = 16;
 constexpr int64_t kSliceBytes = int64_t{64} << 20;
+// Tensor cores drop low bits as they accumulate: a sum of terms of one sign loses about 5.6e-9 of itself for
+// each of them (measured: 2^17 rows 5.7e-4, 2^20 6.5e-3, 2^24 0.10).  No accumulator adds up more than these;
+// what it has then is added, rounded, in FP32.  16384 rows lose 9e-5, 32768 columns 1.8e-4, an FP16 half step
+// being 4.9e-4.
+constexpr int64_t kMostRows = 16384;
+constexpr int64_t kMostColumns = 32768;
 // The plan below counts time in K blocks of a pair's tile (256 x 256 x 64
 // products, about 0.25 us).  A launch costs about kLaunchBlocks of them until
 // its tiles run and until the last is written, a unit about one.
@@ -840,7 +851,7 @@ struct HeadPlan {
     int stats_n;                           // columns of the forward's tiles
     int64_t cols, pieces;                  // columns of a piece (the last may have fewer)
     int64_t slices, slice_blocks;          // dx: K blocks of a piece per slice
-    size_t part, part_sum, zy, scale, g, used_x, partial, bytes;
+    size_t part, part_sum, zy, scale, g, used_x, partial, w_partial, bytes;
     bool partial_dx;
     bool by_slice, w_first;                // the order of kOut's units
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
@@ -854,7 +865,8 @@ struct HeadPlan {
 
         // The number of pieces, and of slices that cut dx's long K (the vocabulary) into units about
         // as long as dweight's (K is the rows): those whose tiles deal out evenly to the pairs.
-        const int64_t most = std::max<int64_t>(2048, kPieceBytes / 2 / rows / kTileN * kTileN);
+        const int64_t most =
+            std::min(kMaxSlices * kMostColumns, std::max<int64_t>(2048, kPieceBytes / 2 / rows / kTileN * kTileN));
         const int64_t fewest = ceil_div(vocab, most);
         const int64_t m_tiles = ceil_div(rows, kTileM), h_tiles = ceil_div(hidden, kTileN);
         const int64_t row_blocks = ceil_div(rows, kBlockK), h_blocks = ceil_div(hidden, kBlockK);
@@ -868,7 +880,7 @@ struct HeadPlan {
             const int64_t reread = g_bytes > kSliceBytes ? g_bytes >> 22 : 0;
             for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
                 const int64_t len = ceil_div(ceil_div(kb, s), kTileM / kBlockK) * (kTileM / kBlockK);
-                if (ceil_div(kb, len) != s) continue;
+                if (ceil_div(kb, len) != s || len * kBlockK > kMostColumns) continue;
                 // Units of dx (a slice's K blocks long) and of dweight (the rows'), dealt to the pairs in turn.
                 const int64_t x_units = s * m_tiles * h_tiles, w_units = (c / kTileM) * h_tiles;
                 const int64_t x_len = std::min(len, kb) + 1 + (s > 1 || np > 1), w_len = row_blocks + 1;
@@ -906,7 +918,8 @@ struct HeadPlan {
         g = 256;
         used_x = g + round256(static_cast<size_t>(rows * cols) * 2);
         partial = used_x + round256(static_cast<size_t>(rows * hidden) * 2);
-        const size_t bwd = partial + (partial_dx ? static_cast<size_t>(slices * rows * hidden) * 4 : 0);
+        w_partial = partial + (partial_dx ? static_cast<size_t>(slices * rows * hidden) * 4 : 0);
+        const size_t bwd = w_partial + (rows > kMostRows ? static_cast<size_t>(cols * hidden) * 4 : 0);
         bytes = std::max(fwd, bwd);
     }
 };
@@ -1035,10 +1048,8 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     a.x_m_tiles = a.m_tiles;
     a.h_tiles = static_cast<int>(ceil_div(sh.hidden, kTileN));
     a.slice_blocks = static_cast<int>(p.slice_blocks);
-    a.w_k_blocks = static_cast<int>(ceil_div(sh.rows, kBlockK));
     a.x_partial = p.partial_dx;
     a.w_f32 = f32_dweight;
-    a.by_slice = p.by_slice;
     a.w_first = p.w_first;
     HeadMaps mz = {}, mo = {};
     LS_CUDA(make_map<T>(&mz.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
@@ -1050,7 +1061,13 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
         LS_CUDA(make_map<float>(&mo.out, partial, sh.hidden, sh.rows, sh.hidden, 32, p.slices));
     else if (dx)
         LS_CUDA(make_map<T>(&mo.out, dx, sh.hidden, sh.rows, sh.hidden, 32));
-    if (dweight && f32_dweight)
+    // dweight's sums over the rows, kMostRows of them at a time: added to an FP32 dweight, or to scratch.
+    const int64_t row_blocks = ceil_div(sh.rows, kBlockK);
+    a.w_partial = dweight && !f32_dweight && sh.rows > kMostRows;
+    float* w_partial = reinterpret_cast<float*>(ws + p.w_partial);
+    if (a.w_partial)
+        LS_CUDA(make_map<float>(&mo.out2, w_partial, sh.hidden, p.cols, sh.hidden, 32));
+    else if (dweight && f32_dweight)
         LS_CUDA(make_map<float>(&mo.out2, dweight, sh.hidden, sh.vocab, sh.hidden, 32));
     else if (dweight)
         LS_CUDA(make_map<T>(&mo.out2, dweight, sh.hidden, sh.vocab, sh.hidden, 32));
@@ -1070,8 +1087,25 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
         a.slices = static_cast<int>(ceil_div(a.x_k_blocks, a.slice_blocks));
         a.x_units = dx ? a.x_m_tiles * a.h_tiles : 0;
         a.w_units = dweight ? a.slice_blocks / (kTileM / kBlockK) * a.h_tiles : 0;
-        a.units = a.slices * a.x_units + (dweight ? static_cast<int>(ceil_div(cols, kTileM)) * a.h_tiles : 0);
-        LS_CUDA((launch_head<T, kOut, false>(mo, a, a.units, s)));
+        const int all_w_units = dweight ? static_cast<int>(ceil_div(cols, kTileM)) * a.h_tiles : 0;
+        a.units = a.slices * a.x_units + all_w_units;
+        a.by_slice = p.by_slice;
+        a.w_row = a.w_partial ? 0 : a.col0;
+        a.w_add = f32_dweight;
+        for (int64_t kb = 0; kb < (dweight ? row_blocks : 1); kb += kMostRows / kBlockK) {
+            a.w_kb0 = static_cast<int>(kb);
+            a.w_k_blocks = static_cast<int>(std::min(kMostRows / kBlockK, row_blocks - kb));
+            LS_CUDA((launch_head<T, kOut, false>(mo, a, a.units, s)));
+            a.x_units = 0;
+            a.units = all_w_units;
+            a.by_slice = false;
+            a.w_add = true;
+        }
+        if (a.w_partial) {
+            const int64_t nvec = cols * sh.hidden / kVec;
+            LS_CUDA(launch_pdl(join_slices_kernel<T>, dim3(static_cast<unsigned>(ceil_div(nvec, 256))), dim3(256), 0, s,
+                               static_cast<T*>(dweight) + c * sh.hidden, static_cast<const float*>(w_partial), 1, nvec, a));
+        }
     }
     if (!dx || !p.partial_dx) return cudaSuccess;
     const int64_t nvec = sh.rows * sh.hidden / kVec;
