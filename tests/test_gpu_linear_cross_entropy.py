@@ -289,3 +289,16 @@ def test_widest_hidden(rows):
     require_gpu()
     x, w, t, d = inputs(rows, 65536, 40, BF16, 21)
     compare(run(x, w, t, d, 0.1), x, w, t, d, 0.1, "hidden 65536")
+
+
+@pytest.mark.parametrize("rows", [9000, 16384, 16385])
+def test_scale_of_many_pieces(rows):
+    """The largest dloss, found with the first piece of the vocabulary, holds for the others: FP16 gradients
+    near the top of their range, one row's dloss 2^12 times the others'."""
+    require_gpu()
+    x, w, t, d = inputs(rows, 64, 20011, F16, 22)
+    t[rows - 2] = 20000
+    d = d * 2.0 ** 14
+    d[rows - 2] = 2.0 ** 12 * d.max()
+    compare(run(x, w, t, d, 0.1, torch.float32, torch.zeros(20011, 64, device="cuda")), x, w, t, d, 0.1,
+            f"{rows} rows", torch.float32)

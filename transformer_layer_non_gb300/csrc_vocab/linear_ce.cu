@@ -91,7 +91,7 @@ struct HeadArgs {
     const float* dloss;
     float* scale;          // [2] in the workspace: g's factor and its inverse, if dloss is given
     float2 fixed_scale;    // the same if not
-    bool find_scale;       // kGrad: from dloss, by every CTA (and left in `scale`)
+    bool find_scale;       // kGrad: from dloss, by every CTA (and left in `scale`), while the first tile's products run
     const void* x;         // kGrad: copied to used_x, if that is given, with zeros for the rows that are
     void* used_x;          //        not used: what they hold (a NaN, say) stays out of g^T x
 };
@@ -1041,9 +1041,10 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
     a.dloss = dloss;
     a.scale = reinterpret_cast<float*>(ws + p.scale);
     a.fixed_scale = scale_for<T>(1.f, sh.eps);
-    // A CTA goes through this many rows in less time than its first tile takes.
-    a.find_scale = dloss && sh.rows <= 16384;
-    if (dloss && !a.find_scale)
+    // Up to this many rows each CTA of the first piece looks for the scale itself, before it reads its first
+    // accumulator (16384 rows: 6 us, a launch for it 4 to 6; 4096: 1); the other pieces find it in `scale`.
+    const bool find_scale = dloss && sh.rows <= 16384;
+    if (dloss && !find_scale)
         LS_CUDA(launch_pdl(grad_scale_kernel<T>, dim3(1), dim3(1024), 0, s, a));
     a.x_m_tiles = a.m_tiles;
     a.h_tiles = static_cast<int>(ceil_div(sh.hidden, kTileN));
@@ -1076,6 +1077,7 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
         a.col0 = static_cast<int>(c);
         a.cols = static_cast<int>(cols);
         set_tiles(a, grad_n);
+        a.find_scale = find_scale && c == 0;
         a.x = x;
         a.used_x = dweight && c == 0 ? ws + p.used_x : nullptr;
         LS_CUDA(make_map<T>(&mz.out, g, cols, sh.rows, p.cols, 32));
