@@ -47,6 +47,12 @@ const char* ls_vocab_last_error(void);
  * clears them. */
 ls_status ls_vocab_check_device_errors(uint32_t* flags);
 
+/* Self-test of that failure path, as ls_selftest_wait_timeout: enqueues two
+ * warps that wait on a barrier which nothing completes, for `polls` polls
+ * (1 .. 2^19, each up to about 2 us); LS_DEVERR_WAIT_TIMEOUT is recorded and
+ * they exit. */
+ls_status ls_vocab_selftest_wait_timeout(uint32_t polls, void* stream);
+
 /* Linear cross entropy.  x: [rows, hidden], weight: [vocab, hidden], both in
  * the storage dtype (LS_F16 or LS_BF16), target: int32 [rows].  With
  *   z[i,j]  = sum_c x[i,c] * weight[j,c]          (products and sums in FP32, never rounded to 16 bits)

@@ -87,6 +87,12 @@ def test_workspace_queries():
     assert e(1 << 20, 64, 100) >= 4 * 4 * (1 << 20)
 
 
+def test_selftest_argument_errors():
+    assert call("ls_vocab_selftest_wait_timeout", 0, None) == INVALID
+    assert call("ls_vocab_selftest_wait_timeout", (1 << 19) + 1, None) == INVALID
+    assert "polls" in ls_vocab.last_error()
+
+
 def distill_fwd(dt=F16, loss=P[0], lse=P[1], z=P[2], ix=P[3], t=P[4], tl=P[5], rows=16, vocab=64,
                 k=4, tau=2.0):
     return call("ls_distill_topk_fwd", dt, loss, lse, z, ix, t, tl, rows, vocab, k, tau, None)

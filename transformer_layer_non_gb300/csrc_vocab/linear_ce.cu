@@ -182,8 +182,9 @@ template <int MODE> __device__ __forceinline__ int units_of(const HeadArgs& a) {
 
 // Bounded wait of a converged warp; false (and the failure flagged for the CTA
 // and the host) when it runs out.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead) {
-    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead,
+                                         uint32_t polls = kWaitPolls) {
+    for (uint32_t i = 0; i < polls; ++i) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if ((i & 63) == 63 && __any_sync(0xffffffffu, *dead)) return false;
     }
@@ -598,6 +599,20 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
     cluster_sync();
     tc_fence_after();
     if (warp == 1) tmem_free(tmem, kTmemColumns);
+}
+
+// Self-test of the waits' failure path: two warps wait, as those of head_kernel do, on a barrier that expects
+// an arrival nobody makes; the first whose polls run out flags the failure, the other one sees it.
+__global__ void __launch_bounds__(64) wait_selftest_kernel(uint32_t polls) {
+    __shared__ uint64_t bar;
+    __shared__ volatile int dead;
+    if (threadIdx.x == 0) {
+        dead = 0;
+        mbar_init(&bar, 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    wait_bar(&bar, 0, &dead, polls);
 }
 
 // (m, l) <- the maximum and the sum of exponentials of two sets of logits.
@@ -1136,6 +1151,11 @@ cudaError_t launch_linear_ce_bwd(ls_dtype dt, void* dx, void* dweight, bool f32_
         return bwd<__half>(dx, dweight, f32_dweight, x, weight, target, lse, dloss, sh, workspace,
                            s);
     return bwd<bf16>(dx, dweight, f32_dweight, x, weight, target, lse, dloss, sh, workspace, s);
+}
+
+cudaError_t launch_vocab_wait_selftest(uint32_t polls, cudaStream_t s) {
+    wait_selftest_kernel<<<1, 64, 0, s>>>(polls);
+    return cudaGetLastError();
 }
 
 cudaError_t linear_ce_take_device_error(unsigned int* flags) {

@@ -123,6 +123,13 @@ ls_status ls_vocab_check_device_errors(uint32_t* flags) {
     return ok();
 }
 
+ls_status ls_vocab_selftest_wait_timeout(uint32_t polls, void* stream) {
+    if (polls == 0 || polls > (1u << 19))
+        return fail(LS_ERR_INVALID_ARGUMENT, "polls = %u is not in [1, 2^19]", polls);
+    return from_cuda(ls::launch_vocab_wait_selftest(polls, as_stream(stream)),
+                     "ls_vocab_selftest_wait_timeout");
+}
+
 size_t ls_linear_cross_entropy_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab) {
     if (rows <= 0 || rows > ls::kMaxHeadRows || hidden <= 0 || hidden > ls::kMaxHeadHidden ||
         hidden % 8 != 0 || vocab <= 0 || vocab > ls::kMaxVocab)

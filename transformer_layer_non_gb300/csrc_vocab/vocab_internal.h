@@ -31,6 +31,7 @@ cudaError_t launch_linear_ce_bwd(ls_dtype dt, void* dx, void* dweight, bool f32_
                                  const void* x, const void* weight, const int32_t* target,
                                  const float* lse, const float* dloss, const HeadShape& sh,
                                  void* workspace, cudaStream_t s);
+cudaError_t launch_vocab_wait_selftest(uint32_t polls, cudaStream_t s);
 cudaError_t linear_ce_take_device_error(unsigned int* flags);
 
 struct DistillShape {

@@ -22,7 +22,7 @@ LS_BF16 = 2
 
 # Every entry point declared in include/ls_vocab.h.
 EXPORTS = (
-    "ls_vocab_last_error", "ls_vocab_check_device_errors",
+    "ls_vocab_last_error", "ls_vocab_check_device_errors", "ls_vocab_selftest_wait_timeout",
     "ls_linear_cross_entropy_fwd", "ls_linear_cross_entropy_bwd",
     "ls_linear_cross_entropy_workspace_bytes",
     "ls_distill_topk_fwd", "ls_distill_topk_bwd",
@@ -41,6 +41,7 @@ _SZ = ctypes.c_size_t
 _SIGNATURES = {
     "ls_vocab_last_error": (ctypes.c_char_p, []),
     "ls_vocab_check_device_errors": (_INT, [ctypes.POINTER(ctypes.c_uint32)]),
+    "ls_vocab_selftest_wait_timeout": (_INT, [ctypes.c_uint32, _P]),
     "ls_linear_cross_entropy_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "ls_linear_cross_entropy_fwd": (_INT, [_INT, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F32, _I32,
                                            _P, _SZ, _P]),
@@ -87,6 +88,11 @@ def check_device_errors() -> int:
     v = ctypes.c_uint32(0)
     _check(load().ls_vocab_check_device_errors(ctypes.byref(v)))
     return int(v.value)
+
+
+def selftest_wait_timeout(polls: int = 1024, stream=None):
+    """Enqueue the bounded-wait failure self-test (see include/ls_vocab.h)."""
+    _check(load().ls_vocab_selftest_wait_timeout(polls, _stream(stream)))
 
 
 def linear_cross_entropy_workspace_bytes(rows: int, hidden: int, vocab: int) -> int:
