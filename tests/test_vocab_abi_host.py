@@ -198,3 +198,19 @@ def test_binding_checks_tensors_on_the_host():
         ls_vocab.ls_linear_cross_entropy_fwd(out, None, x[0], w, t)
     with pytest.raises(TypeError, match="must be a tensor"):
         ls_vocab.ls_distill_topk_fwd(out, None, None, t, t)
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 3, -2 ** 31 - 1])
+def test_binding_refuses_ids_that_are_no_int32(value):
+    """2^32 + 3 would reach the library as 3, an id of the table."""
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros(4, 16).half(), torch.zeros(9, 16).half()
+    t, out = torch.zeros(4, dtype=torch.int32), torch.zeros(4)
+    for call_ in (lambda: ls_vocab.ls_linear_cross_entropy_fwd(out, None, x, w, t, ignore_index=value),
+                  lambda: ls_vocab.ls_linear_cross_entropy_bwd(x, w, x, w, t, out, ignore_index=value),
+                  lambda: ls_vocab.ls_embedding_lookup_bwd(w.float(), x, t, padding_id=value)):
+        with pytest.raises(ValueError, match="int32"):
+            call_()
+    for ok in (2 ** 31 - 1, -2 ** 31):
+        with pytest.raises(ValueError, match="CUDA"):
+            ls_vocab.ls_linear_cross_entropy_fwd(out, None, x, w, t, ignore_index=ok)

@@ -202,6 +202,13 @@ def _workspace(t, device: int):
     return _tensor("workspace", t, shape, dtype, device), t.nbytes
 
 
+def _id(name: str, v) -> int:
+    """An int32 argument: ctypes would keep the lower 32 bits of anything larger."""
+    if -2 ** 31 <= v < 2 ** 31:
+        return v
+    raise ValueError(f"{name} = {v} is not an int32")
+
+
 _raw_stream = None
 
 
@@ -224,7 +231,7 @@ def ls_linear_cross_entropy_fwd(loss, lse, x, weight, target, label_smoothing: f
     """Per-row loss (FP32 [rows]) and lse (FP32 [rows] or None) of the logits
     x weight^T against int32 targets: x [rows, hidden], weight [vocab, hidden].
     The logits are not kept."""
-    dev = _device()
+    ignore, dev = _id("ignore_index", ignore_index), _device()
     px, (rows, hidden) = _shaped("x", x, 2, None, dev)
     pw, (vocab, wide) = _shaped("weight", weight, 2, x.dtype, dev)
     if wide != hidden:
@@ -236,7 +243,7 @@ def ls_linear_cross_entropy_fwd(loss, lse, x, weight, target, label_smoothing: f
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_linear_cross_entropy_fwd(
         _storage_code(x), ploss, plse, px, pw, pt, rows, hidden, vocab, label_smoothing,
-        ignore_index, ws, ws_bytes, _stream_of(stream, dev)))
+        ignore, ws, ws_bytes, _stream_of(stream, dev)))
 
 
 def ls_linear_cross_entropy_bwd(dx, dweight, x, weight, target, lse, dloss=None,
@@ -244,7 +251,7 @@ def ls_linear_cross_entropy_bwd(dx, dweight, x, weight, target, lse, dloss=None,
                                 workspace=None, stream=None):
     """Gradients of x and weight (either may be None).  A dweight in the
     storage dtype is written; a float32 dweight is added to."""
-    dev = _device()
+    ignore, dev = _id("ignore_index", ignore_index), _device()
     px, (rows, hidden) = _shaped("x", x, 2, None, dev)
     pw, (vocab, wide) = _shaped("weight", weight, 2, x.dtype, dev)
     if wide != hidden:
@@ -263,7 +270,7 @@ def ls_linear_cross_entropy_bwd(dx, dweight, x, weight, target, lse, dloss=None,
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_linear_cross_entropy_bwd(
         code, pdx, pdw, wcode, px, pw, pt, plse, pg, rows, hidden, vocab, label_smoothing,
-        ignore_index, ws, ws_bytes, _stream_of(stream, dev)))
+        ignore, ws, ws_bytes, _stream_of(stream, dev)))
 
 
 def _distill_inputs(logits, teacher_index, teacher_logits, teacher_lse, dev):
@@ -317,7 +324,7 @@ def ls_embedding_lookup_bwd(d_table, dy, tokens, scale: float = 1.0, padding_id:
                             accumulate: bool = False, workspace=None, stream=None):
     """The table's gradient (FP32 [vocab, hidden]) of dy [tokens, hidden]:
     written whole, or added to d_table with accumulate."""
-    dev = _device()
+    padding, dev = _id("padding_id", padding_id), _device()
     pd, (vocab, hidden) = _shaped("d_table", d_table, 2, _float32, dev)
     pt, (n,) = _shaped("tokens", tokens, 1, _int32, dev)
     pdy, size = _shaped("dy", dy, 2, None, dev)
@@ -325,5 +332,5 @@ def ls_embedding_lookup_bwd(d_table, dy, tokens, scale: float = 1.0, padding_id:
         _tensor("dy", dy, (n, hidden), dy.dtype, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().ls_embedding_lookup_bwd(_storage_code(dy), pd, pdy, pt, n, hidden, vocab, scale,
-                                          padding_id, int(bool(accumulate)), ws, ws_bytes,
+                                          padding, int(bool(accumulate)), ws, ws_bytes,
                                           _stream_of(stream, dev)))
