@@ -62,7 +62,7 @@ ls_status ls_vocab_selftest_wait_timeout(uint32_t polls, void* stream);
  * multiple of 8 and at most 65536; any vocab from 1 to 2^30, any rows up to
  * 2^24.  A target equal to ignore_index, or outside [0, vocab), gives loss 0;
  * its lse is still written.  loss and lse: FP32 [rows]; lse may be NULL.
- * workspace: at least ls_linear_cross_entropy_workspace_bytes bytes. */
+ * workspace: at least ls_linear_cross_entropy_fwd_workspace_bytes bytes. */
 ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, const void* x,
                                       const void* weight, const int32_t* target, int64_t rows,
                                       int64_t hidden, int64_t vocab, float label_smoothing,
@@ -84,7 +84,8 @@ ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, c
  * written; with dweight_dtype == LS_F32 the gradient is ADDED to it, as
  * ls_embedding_bwd and ls_embedding_lookup_bwd add to theirs, so that tied
  * embeddings share one gradient.  rows == 0 writes zeros to a dweight in the
- * storage dtype. */
+ * storage dtype.
+ * workspace: at least ls_linear_cross_entropy_workspace_bytes bytes. */
 ls_status ls_linear_cross_entropy_bwd(ls_dtype dtype, void* dx, void* dweight,
                                       ls_dtype dweight_dtype, const void* x, const void* weight,
                                       const int32_t* target, const float* lse, const float* dloss,
@@ -92,9 +93,15 @@ ls_status ls_linear_cross_entropy_bwd(ls_dtype dtype, void* dx, void* dweight,
                                       float label_smoothing, int32_t ignore_index,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes that both calls above need for these sizes: a piece of the
- * vocabulary's gradients and FP32 partial sums.  0 for invalid sizes. */
+/* Workspace bytes that either call above can do with for these sizes: for the
+ * backward, a piece of the vocabulary's gradients (128 MB or 2048 columns of
+ * them at the most), a copy of x, up to 16 FP32 copies of dx and, beyond 16384
+ * rows, a piece of dweight in FP32.  0 for invalid sizes. */
 size_t ls_linear_cross_entropy_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab);
+
+/* What the forward alone needs, as a program that only scores does: 24 bytes
+ * for each row and 256 (or fewer) columns. */
+size_t ls_linear_cross_entropy_fwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab);
 
 /* Distillation from a teacher's top logits.  logits: [rows, vocab] of the
  * student (LS_F32, LS_F16 or LS_BF16; vocab a multiple of 8), teacher_index:

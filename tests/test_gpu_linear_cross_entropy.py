@@ -302,3 +302,18 @@ def test_scale_of_many_pieces(rows):
     d[rows - 2] = 2.0 ** 12 * d.max()
     compare(run(x, w, t, d, 0.1, torch.float32, torch.zeros(20011, 64, device="cuda")), x, w, t, d, 0.1,
             f"{rows} rows", torch.float32)
+
+
+@pytest.mark.parametrize("rows,hidden,vocab", [(1, 1280, 50257), (1, 24584, 300), (3, 136, 9001), (333, 512, 32000),
+                                               (1030, 264, 33000)])
+def test_scoring_with_the_forwards_workspace(rows, hidden, vocab):
+    require_gpu()
+    x, w, t, d = inputs(rows, hidden, vocab, BF16, 23)
+    both = run(x, w, t, d, 0.1)
+    nbytes = ls_vocab.linear_cross_entropy_workspace_bytes(rows, hidden, vocab, backward=False)
+    ws = Guarded((nbytes // 4,), torch.float32)
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ls_vocab.ls_linear_cross_entropy_fwd(loss, lse, x, w, t, 0.1, workspace=ws.t)
+    torch.cuda.synchronize()
+    ws.check()
+    assert torch.equal(loss, both[0]) and torch.equal(lse, both[1])

@@ -87,6 +87,23 @@ def test_workspace_queries():
     assert e(1 << 20, 64, 100) >= 4 * 4 * (1 << 20)
 
 
+def test_workspace_of_the_forward_alone():
+    q = ls_vocab.linear_cross_entropy_workspace_bytes
+    assert q(0, 64, 100, backward=False) == q(4, 60, 100, backward=False) == q(4, 64, 0, False) == 0
+    for shape in ((1, 1280, 50257), (333, 512, 32000), (4096, 768, 30522), (16384, 4096, 128000)):
+        both, fwd = q(*shape), q(*shape, backward=False)
+        assert 0 < fwd <= both
+        # a maximum, a sum of exponentials and a sum for each row and half tile
+        assert shape[0] == 1 or fwd <= shape[0] * (shape[2] / 32 + 2) * 12 + 4 * shape[0] + 512
+        # (a refusal that follows shows that the workspace passed)
+        rows, hidden, vocab = shape
+        assert head_fwd(rows=rows, hidden=hidden, vocab=vocab, wsb=fwd - 1) == SMALL
+        assert head_fwd(rows=rows, hidden=hidden, vocab=vocab, wsb=fwd, lse=P[0]) == INVALID
+        assert "overlap" in ls_vocab.last_error()
+        assert head_bwd(rows=rows, hidden=hidden, vocab=vocab, wsb=both - 1) == SMALL
+    assert q(4096, 768, 30522, backward=False) < q(4096, 768, 30522) // 10
+
+
 def test_selftest_argument_errors():
     assert call("ls_vocab_selftest_wait_timeout", 0, None) == INVALID
     assert call("ls_vocab_selftest_wait_timeout", (1 << 19) + 1, None) == INVALID

@@ -866,7 +866,7 @@ struct HeadPlan {
     int stats_n;                           // columns of the forward's tiles
     int64_t cols, pieces;                  // columns of a piece (the last may have fewer)
     int64_t slices, slice_blocks;          // dx: K blocks of a piece per slice
-    size_t part, part_sum, zy, scale, g, used_x, partial, w_partial, bytes;
+    size_t part, part_sum, zy, scale, g, used_x, partial, w_partial, fwd_bytes, bytes;
     bool partial_dx;
     bool by_slice, w_first;                // the order of kOut's units
     HeadPlan(int64_t rows, int64_t hidden, int64_t vocab) {
@@ -876,7 +876,7 @@ struct HeadPlan {
         part = 0;
         part_sum = round256(parts * 8);
         zy = part_sum + round256(parts * 4);
-        const size_t fwd = zy + static_cast<size_t>(rows) * 4;
+        fwd_bytes = zy + static_cast<size_t>(rows) * 4;
 
         // The number of pieces, and of slices that cut dx's long K (the vocabulary) into units about
         // as long as dweight's (K is the rows): those whose tiles deal out evenly to the pairs.
@@ -935,7 +935,7 @@ struct HeadPlan {
         partial = used_x + round256(static_cast<size_t>(rows * hidden) * 2);
         w_partial = partial + (partial_dx ? static_cast<size_t>(slices * rows * hidden) * 4 : 0);
         const size_t bwd = w_partial + (rows > kMostRows ? static_cast<size_t>(cols * hidden) * 4 : 0);
-        bytes = std::max(fwd, bwd);
+        bytes = std::max(fwd_bytes, bwd);
     }
 };
 
@@ -1134,6 +1134,10 @@ cudaError_t bwd(void* dx, void* dweight, bool f32_dweight, const void* x, const 
 
 size_t linear_ce_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab) {
     return HeadPlan(rows, hidden, vocab).bytes;
+}
+
+size_t linear_ce_fwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab) {
+    return HeadPlan(rows, hidden, vocab).fwd_bytes;
 }
 
 cudaError_t launch_linear_ce_fwd(ls_dtype dt, float* loss, float* lse, const void* x,

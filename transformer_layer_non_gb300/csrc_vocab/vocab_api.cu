@@ -130,11 +130,18 @@ ls_status ls_vocab_selftest_wait_timeout(uint32_t polls, void* stream) {
                      "ls_vocab_selftest_wait_timeout");
 }
 
+static bool head_sizes(int64_t rows, int64_t hidden, int64_t vocab) {
+    return rows > 0 && rows <= ls::kMaxHeadRows && hidden > 0 && hidden <= ls::kMaxHeadHidden &&
+           hidden % 8 == 0 && vocab > 0 && vocab <= ls::kMaxVocab;
+}
+
 size_t ls_linear_cross_entropy_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab) {
-    if (rows <= 0 || rows > ls::kMaxHeadRows || hidden <= 0 || hidden > ls::kMaxHeadHidden ||
-        hidden % 8 != 0 || vocab <= 0 || vocab > ls::kMaxVocab)
-        return 0;
-    return ls::linear_ce_workspace_bytes(rows, hidden, vocab);
+    return head_sizes(rows, hidden, vocab) ? ls::linear_ce_workspace_bytes(rows, hidden, vocab) : 0;
+}
+
+size_t ls_linear_cross_entropy_fwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab) {
+    return head_sizes(rows, hidden, vocab) ? ls::linear_ce_fwd_workspace_bytes(rows, hidden, vocab)
+                                           : 0;
 }
 
 ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, const void* x,
@@ -150,7 +157,7 @@ ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, c
     LS_TRY(check_ptr(x, "x", true));
     LS_TRY(check_ptr(weight, "weight", true));
     LS_TRY(check_ptr4(target, "target", true));
-    const size_t need = ls::linear_ce_workspace_bytes(rows, hidden, vocab);
+    const size_t need = ls::linear_ce_fwd_workspace_bytes(rows, hidden, vocab);
     LS_TRY(check_workspace(fn, workspace, workspace_bytes, need));
     const size_t rb = static_cast<size_t>(rows) * 4;
     const Span outs[] = {{"loss", loss, rb}, {"lse", lse, rb}, {"workspace", workspace, need}};

@@ -23,6 +23,7 @@ struct HeadShape {
     int32_t ignore_index;
 };
 size_t linear_ce_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab);
+size_t linear_ce_fwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab);
 cudaError_t launch_linear_ce_fwd(ls_dtype dt, float* loss, float* lse, const void* x,
                                  const void* weight, const int32_t* target, const HeadShape& sh,
                                  void* workspace, cudaStream_t s);

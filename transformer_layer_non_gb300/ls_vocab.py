@@ -24,7 +24,7 @@ LS_BF16 = 2
 EXPORTS = (
     "ls_vocab_last_error", "ls_vocab_check_device_errors", "ls_vocab_selftest_wait_timeout",
     "ls_linear_cross_entropy_fwd", "ls_linear_cross_entropy_bwd",
-    "ls_linear_cross_entropy_workspace_bytes",
+    "ls_linear_cross_entropy_workspace_bytes", "ls_linear_cross_entropy_fwd_workspace_bytes",
     "ls_distill_topk_fwd", "ls_distill_topk_bwd",
     "ls_embedding_lookup_fwd", "ls_embedding_lookup_bwd",
     "ls_embedding_lookup_workspace_bytes",
@@ -43,6 +43,7 @@ _SIGNATURES = {
     "ls_vocab_check_device_errors": (_INT, [ctypes.POINTER(ctypes.c_uint32)]),
     "ls_vocab_selftest_wait_timeout": (_INT, [ctypes.c_uint32, _P]),
     "ls_linear_cross_entropy_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "ls_linear_cross_entropy_fwd_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "ls_linear_cross_entropy_fwd": (_INT, [_INT, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F32, _I32,
                                            _P, _SZ, _P]),
     "ls_linear_cross_entropy_bwd": (_INT, [_INT, _P, _P, _INT, _P, _P, _P, _P, _P, _I64, _I64,
@@ -95,7 +96,11 @@ def selftest_wait_timeout(polls: int = 1024, stream=None):
     _check(load().ls_vocab_selftest_wait_timeout(polls, _stream(stream)))
 
 
-def linear_cross_entropy_workspace_bytes(rows: int, hidden: int, vocab: int) -> int:
+def linear_cross_entropy_workspace_bytes(rows: int, hidden: int, vocab: int,
+                                         backward: bool = True) -> int:
+    """For both directions, or for the forward alone."""
+    if not backward:
+        return int(load().ls_linear_cross_entropy_fwd_workspace_bytes(rows, hidden, vocab))
     return int(load().ls_linear_cross_entropy_workspace_bytes(rows, hidden, vocab))
 
 
