@@ -16,11 +16,12 @@
 //
 // The k entries are a few hundred bytes.  Warp 0 works them out by shuffles
 // while the row's first vectors are on their way to all warps:
-//   E = sum_e q_e log q_e,   and q_e and z_index(e) / tau for the end, where
-//   loss = tau^2 (E + sum_e q_e (lse - z_index(e) / tau))
-// needs one barrier, the merging of the warps' sums.  (With the sum of
-// q_e z_index(e) / tau taken beforehand the loss would be a difference of two
+// each lane, of its entries,
+//   r = max_e z_index(e) / tau,   E = sum_e q_e (log q_e + r - z_index(e) / tau),   Q = sum_e q_e,
+// and   loss = tau^2 sum_lanes (E + Q (lse - r))   then needs one barrier, the
+// merging of the warps' sums.  (Without r the loss would be a difference of two
 // numbers of lse's size: 1e23 instead of 2 in a row of logits near -1e30.)
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -134,7 +135,7 @@ __device__ __forceinline__ void load_batch(Raw8<T> (&r)[U], const T* z, int v0, 
     }
 }
 
-// Dynamic shared memory: sm_q [k], sm_ix [k].
+// Dynamic shared memory: logq [k], ix [k].
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
@@ -153,29 +154,26 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
     Raw8<T> r[U];
     int v0 = lo + threadIdx.x;
     load_batch<T, U, THREADS>(r, z, v0, hi);
-    float E = 0.f, Q = 0.f;
-    float* sm_q = sm_k;                              // log q, then q
-    int* sm_ix = reinterpret_cast<int*>(sm_k + a.k);  // the index, then the bits of the student's z / tau there
+    float E = 0.f, Q = 0.f, ref = -FLT_MAX;
     if (rank == 0 && threadIdx.x < 32) {
-        load_entries(sm_q, sm_ix, index, teacher, teacher_lse, row, a);
+        float* logq = sm_k;
+        int* ix = reinterpret_cast<int*>(sm_k + a.k);
+        load_entries(logq, ix, index, teacher, teacher_lse, row, a);
         __syncwarp();
-        for (int b = 0; b < a.k; b += 32 * kBatch) {
-            const int e0 = b + threadIdx.x;
+        for (int e0 = threadIdx.x; e0 < a.k; e0 += 32 * kBatch) {
             float f[kBatch];
-            gather(f, z, sm_ix, e0, a.k, 0, static_cast<int>(a.vocab));
-            __syncwarp();  // it reads the last index for entries behind it, too
+            gather(f, z, ix, e0, a.k, 0, static_cast<int>(a.vocab));
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int e = e0 + 32 * u;
-                if (e >= a.k) continue;
-                float q = 0.f;
-                if (sm_ix[e] >= 0) {
-                    q = expf(sm_q[e]);
-                    Q += q;
-                    E += q * sm_q[e];
+                if (e >= a.k || ix[e] < 0) continue;
+                const float q = expf(logq[e]), zu = f[u] / a.tau;
+                if (zu > ref) {
+                    if (Q != 0.f) E += Q * (zu - ref);
+                    ref = zu;
                 }
-                sm_q[e] = q;
-                sm_ix[e] = __float_as_int(f[u] / a.tau);
+                E += q * (logq[e] + (ref - zu));
+                Q += q;
             }
         }
     }
@@ -246,8 +244,7 @@ distill_fwd_kernel(float* __restrict__ loss, float* __restrict__ lse_out,
         if (rank != 0 || threadIdx.x >= 32) return;
     }
     const float lse = m / a.tau + logf(l);
-    for (int e = threadIdx.x; e < a.k; e += 32)  // its own entries
-        if (sm_q[e] != 0.f) E += sm_q[e] * (lse - __int_as_float(sm_ix[e]));
+    if (Q != 0.f) E += Q * (lse - ref);
     E = group_sum<32>(E);
     Q = group_sum<32>(Q);
     if (threadIdx.x == 0) {
