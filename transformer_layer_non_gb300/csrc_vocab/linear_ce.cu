@@ -234,14 +234,16 @@ __device__ __forceinline__ void add_stats(float (&z)[32], int n, float& m, float
     }
 }
 
-// 32 values of a row of g: d (exp(z - lse) - q0 - [j == at] (1 - eps)).
-template <bool HIT>
-__device__ __forceinline__ void grads_of(float (&z)[32], float d, float lse, float q0, float qy, int at) {
-    float ml = -lse * kLog2e;
-    if (fabsf(ml) > kMostFma) {  // the difference first; it is at most 0 but for the rounding of z and lse
-        ml = 0.f;
+// 32 values of a row of g: d (exp(z - lse) - q0 - [j == at] (1 - eps)).  FAR: some row of the warp has an lse
+// too far from zero for one FMA (ml = -lse log2(e)).
+template <bool HIT, bool FAR>
+__device__ __forceinline__ void grads_of(float (&z)[32], float d, float lse, float ml, float q0, float qy, int at) {
+    if constexpr (FAR) {
+        if (fabsf(ml) > kMostFma) {  // the difference first; it is at most 0 but for the rounding of z and lse
+            ml = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) z[j] = z[j] > lse ? 0.f : z[j] - lse;
+            for (int j = 0; j < 32; ++j) z[j] = z[j] > lse ? 0.f : z[j] - lse;
+        }
     }
     const float2 cc = make_float2(kLog2e, kLog2e), mm = make_float2(ml, ml);
     const float2 dd = make_float2(d, d), dq = make_float2(-d * q0, -d * q0);
@@ -531,15 +533,17 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 const bool used = there && used_target(y, a);
                 const int at = used ? y - a.col0 - n0 : -1;
                 const float d = used ? row_dloss * scale.x : 0.f;
+                const float ml = -row_lse * kLog2e;
                 const float q0 = a.eps / static_cast<float>(a.vocab), qy = 1.f - a.eps;
-                sweep(cols, release, [&](int c, float (&z)[32]) {
+                auto columns = [&](int c, float (&z)[32], auto far) {
+                    constexpr bool kFar = decltype(far)::value;
                     if (c * 32 >= n) return;
                     if ((c & 1) == 0) open_box();
                     const int rel = at - c * 32;
-                    if (__any_sync(0xffffffffu, rel >= 0 && rel < 32))
-                        grads_of<true>(z, d, row_lse, q0, qy, rel);
+                    if (kFar || __any_sync(0xffffffffu, rel >= 0 && rel < 32))
+                        grads_of<true, kFar>(z, d, row_lse, ml, q0, qy, rel);
                     else
-                        grads_of<false>(z, d, row_lse, q0, qy, rel);
+                        grads_of<false, kFar>(z, d, row_lse, ml, q0, qy, rel);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint4 v = pack8<T>(z, 8 * j, 1.f);
@@ -549,7 +553,12 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                         close_box([&] {
                             if (row0 < a.rows) tma_store_2d(&maps.out, n0 + (c & ~1) * 32, row0, box);
                         });
-                });
+                };
+                // Code of its own for rows far from zero, so that it is not fetched with the others'.
+                if (__any_sync(0xffffffffu, fabsf(ml) > kMostFma))
+                    sweep(cols, release, [&](int c, float (&z)[32]) { columns(c, z, std::true_type{}); });
+                else
+                    sweep(cols, release, [&](int c, float (&z)[32]) { columns(c, z, std::false_type{}); });
             } else {
                 const bool f32 = t.weight ? a.w_f32 || a.w_partial : a.x_partial;
                 const float sc = (t.weight ? a.w_partial : a.x_partial) ? 1.f : scale.y;
