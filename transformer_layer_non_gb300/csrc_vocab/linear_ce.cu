@@ -389,8 +389,7 @@ head_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadA
                 tc_fence_after();
                 // Which operands have M or N as their contiguous axis.
                 const bool a_mn = MODE == kOut && t.weight, b_mn = MODE == kOut;
-                const uint32_t idesc = instr_desc(kBf16, false, false, kTileM, MODE == kOut ? kTileN : a.tile_n) |
-                                       (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+                const uint32_t idesc = instr_desc(kBf16, a_mn, b_mn, kTileM, MODE == kOut ? kTileN : a.tile_n);
                 const uint64_t da = desc_at(a_mn ? mnmajor : kmajor, smem_u32(smem));
                 const uint64_t db = desc_at(b_mn ? mnmajor : kmajor, smem_u32(smem) + kOperandBytes);
                 // 16 values of K further on, in the descriptors' units of 16 bytes
