@@ -21,7 +21,9 @@
  *  - A workspace is scratch: it needs no initialisation and holds nothing
  *    between calls, so calls ordered on one stream (or graphs whose replays
  *    are ordered) may share one.  Calls that can run at the same time on the
- *    GPU must not.
+ *    GPU must not; nor may a workspace that a reduction of ls_ops.h still
+ *    reads on its second stream (ls_set_reduction_stream) be given to these
+ *    calls before ls_join_reductions: they do not know of it.
  *  - Results do not depend on the run: every sum is added in an order that
  *    the shapes and the ids fix, without floating-point atomics.
  */
@@ -60,7 +62,7 @@ ls_status ls_vocab_selftest_wait_timeout(uint32_t polls, void* stream);
  *   loss[i] = (1 - eps) * (lse[i] - z[i,target]) + eps * (lse[i] - mean_j z[i,j])
  * as ls_cross_entropy_fwd computes them from given logits.  hidden must be a
  * multiple of 8 and at most 65536; any vocab from 1 to 2^30, any rows up to
- * 2^24.  A target equal to ignore_index, or outside [0, vocab), gives loss 0;
+ * 2^24, as long as rows * vocab is at most 2^46 and vocab * hidden 2^40.  A target equal to ignore_index, or outside [0, vocab), gives loss 0;
  * its lse is still written.  loss and lse: FP32 [rows]; lse may be NULL.
  * workspace: at least ls_linear_cross_entropy_fwd_workspace_bytes bytes. */
 ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, const void* x,
@@ -76,7 +78,10 @@ ls_status ls_linear_cross_entropy_fwd(ls_dtype dtype, float* loss, float* lse, c
  *   dweight[j,c] = sum_i g[i,j] * x[i,c]
  * g is rounded once to the storage dtype for the two products, after a
  * division by max|dloss| (1 - eps) which the FP32 sums undo (FP16 keeps
- * values down to 2^-38 of the largest dloss that way).
+ * values down to 2^-38 of the largest dloss that way).  The sums run in the
+ * tensor cores' accumulators, which drop low bits, over at most 16384 rows or
+ * 32768 entries (9e-5 and 2e-4 of a sum of terms of one sign), and in FP32
+ * from there on.
  * dloss: FP32 [rows] or NULL for 1.  Rows with an ignored target contribute
  * nothing and get a zero dx, whatever they and their dloss hold (NaN too).
  * dx: [rows, hidden] in the storage dtype, written, or NULL.
@@ -118,7 +123,9 @@ size_t ls_linear_cross_entropy_fwd_workspace_bytes(int64_t rows, int64_t hidden,
  * an index outside [0, vocab) (such as -1, for a row with fewer entries), has
  * q = 0 and adds nothing; a row without entries has loss 0.  An index that a
  * row holds twice counts twice.  1 <= k <= 1024.  loss and lse: FP32 [rows],
- * lse may be NULL. */
+ * lse may be NULL.  Masks may be -inf or any finite value: a row of nothing
+ * but one has the lse that FP32 can hold, the mask / tau itself where
+ * log(vocab) is below its last place. */
 ls_status ls_distill_topk_fwd(ls_dtype dtype, float* loss, float* lse, const void* logits,
                               const int32_t* teacher_index, const void* teacher_logits,
                               const float* teacher_lse, int64_t rows, int64_t vocab, int64_t k,
@@ -128,7 +135,8 @@ ls_status ls_distill_topk_fwd(ls_dtype dtype, float* loss, float* lse, const voi
  *   dlogits[j] = dloss[row] * tau * (p[j] * sum_e q[e] - sum_{e: index[e] == j} q[e])
  * dloss: FP32 [rows], or NULL for 1.  A row whose q are all 0 gets a zero
  * gradient.  dlogits may be logits (in place).  p carries the rounding of the
- * FP32 lse, |lse| * 2^-24 relative. */
+ * FP32 lse, |lse| * 2^-24 relative; it is at most 1 wherever lse is the
+ * forward's. */
 ls_status ls_distill_topk_bwd(ls_dtype dtype, void* dlogits, const void* logits,
                               const int32_t* teacher_index, const void* teacher_logits,
                               const float* lse, const float* teacher_lse, const float* dloss,
