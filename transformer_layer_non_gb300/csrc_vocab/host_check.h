@@ -1,5 +1,6 @@
-// host_check.h -- host-side argument checks of the vocabulary operators' C
-// ABI: the per-thread error message, pointers, and overlapping buffers.
+// host_check.h -- host-side argument checks of the C ABIs of the vocabulary
+// and the block operators: the per-thread error message, types, sizes, pointers,
+// workspaces, and overlapping buffers.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -76,5 +77,57 @@ ls_status check_ptr(const void* p, const char* name, bool required) {
         ls_status _st = (expr);              \
         if (_st != LS_OK) return _st;        \
     } while (0)
+
+size_t elem_size(ls_dtype dt) { return dt == LS_F32 ? 4 : 2; }
+
+ls_status check_storage(const char* fn, ls_dtype dt, bool f32_too) {
+    if (dt == LS_F16 || dt == LS_BF16 || (dt == LS_F32 && f32_too)) return LS_OK;
+    return fail(LS_ERR_INVALID_ARGUMENT, "%s: unsupported storage dtype %d", fn,
+                static_cast<int>(dt));
+}
+
+ls_status check_ptr_n(const void* p, const char* name, bool required, size_t bytes) {
+    if (!p) {
+        if (required) return fail(LS_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+        return LS_OK;
+    }
+    if (reinterpret_cast<uintptr_t>(p) & (bytes - 1))
+        return fail(LS_ERR_MISALIGNED, "%s is not %zu-byte aligned", name, bytes);
+    return LS_OK;
+}
+
+ls_status check_ptr4(const void* p, const char* name, bool required) {
+    return check_ptr_n(p, name, required, 4);
+}
+
+// A size in [lo, hi].
+ls_status check_size(const char* fn, const char* name, int64_t v, int64_t lo, int64_t hi) {
+    if (v < lo)
+        return fail(LS_ERR_INVALID_ARGUMENT, "%s: %s = %lld < %lld", fn, name, (long long)v,
+                    (long long)lo);
+    if (v > hi)
+        return fail(LS_ERR_UNSUPPORTED_SHAPE, "%s: %s = %lld exceeds %lld", fn, name, (long long)v,
+                    (long long)hi);
+    return LS_OK;
+}
+
+ls_status check_multiple_of_8(const char* fn, const char* name, int64_t v) {
+    if (v % 8 != 0)
+        return fail(LS_ERR_MISALIGNED, "%s: %s = %lld is not a multiple of 8", fn, name,
+                    (long long)v);
+    return LS_OK;
+}
+
+ls_status check_workspace(const char* fn, const void* ws, size_t have, size_t need) {
+    if (need == 0) return LS_OK;
+    if (!ws) return fail(LS_ERR_INVALID_ARGUMENT, "%s: workspace is NULL", fn);
+    if (!aligned16(ws)) return fail(LS_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+    if (have < need)
+        return fail(LS_ERR_WORKSPACE_TOO_SMALL, "%s: workspace has %zu bytes, needs %zu", fn, have,
+                    need);
+    return LS_OK;
+}
+
+cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 }  // namespace

@@ -26,13 +26,12 @@
 // itself (1/rows, say) would be off by the same half step in every row, and
 // with it the whole gradient.  FP16, which has no exponent range for 1/rows
 // times 1/vocab, also gets a factor of 2^14.
-#include <cuda.h>
 #include <math.h>
 
 #include <algorithm>
 #include <type_traits>
 
-#include "tc.cuh"
+#include "tc_tile.cuh"
 #include "vocab_internal.h"
 
 namespace ls {
@@ -180,24 +179,6 @@ template <int MODE> __device__ __forceinline__ int units_of(const HeadArgs& a) {
     return MODE == kOut ? a.units : a.m_tiles * a.n_tiles;
 }
 
-// Bounded wait of a converged warp; false (and the failure flagged for the CTA
-// and the host) when it runs out.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead,
-                                         uint32_t polls = kWaitPolls) {
-    for (uint32_t i = 0; i < polls; ++i) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((i & 63) == 63 && __any_sync(0xffffffffu, *dead)) return false;
-    }
-    flag_device_error(kDevErrWaitTimeout);
-    *dead = 1;
-    return false;
-}
-
-// 16 bytes `c` of a lane's 128-byte row in a swizzled store box.
-__device__ __forceinline__ void put16(unsigned char* box, int lane, int c, uint4 v) {
-    st16(box + lane * 128 + ((c ^ (lane & 7)) << 4), v);
-}
-
 // Statistics of 32 logits of one row: n of them exist (n >= 1).
 template <bool EDGE, bool SUM>
 __device__ __forceinline__ void add_stats(float (&z)[32], int n, float& m, float2& l, float2& s) {
@@ -259,31 +240,6 @@ __device__ __forceinline__ void grads_of(float (&z)[32], float d, float lse, flo
         z[j] = p.x;
         z[j + 1] = p.y;
     }
-}
-
-template <typename T> __device__ __forceinline__ uint4 pack8(const float (&z)[32], int j, float sc) {
-    return make_uint4(pack2<T>(z[j] * sc, z[j + 1] * sc), pack2<T>(z[j + 2] * sc, z[j + 3] * sc),
-                      pack2<T>(z[j + 4] * sc, z[j + 5] * sc), pack2<T>(z[j + 6] * sc, z[j + 7] * sc));
-}
-
-// f(c, z) for the warp's four groups of 32 accumulator columns, the next group
-// on its way while f works; release() once all of them are in registers.
-template <typename R, typename F>
-__device__ __forceinline__ void sweep(uint32_t cols, R&& release, F&& f) {
-    float za[32], zb[32];
-    tmem_ld32(za, cols);
-    tmem_ld_wait(za);
-    tmem_ld32(zb, cols + 32);
-    f(0, za);
-    tmem_ld_wait(zb);
-    tmem_ld32(za, cols + 64);
-    f(1, zb);
-    tmem_ld_wait(za);
-    tmem_ld32(zb, cols + 96);
-    f(2, za);
-    tmem_ld_wait(zb);
-    release();
-    f(3, zb);
 }
 
 // kGrad has two more warps, which write used_x.
@@ -826,9 +782,6 @@ join_slices_kernel(T* __restrict__ dx, const float* __restrict__ part, int slice
 }
 
 // --- host ----------------------------------------------------------------------
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-
 // Pieces: g for `cols` vocabulary entries at a time, at most about 128 MB of it
 // (never fewer than 2048 entries).
 constexpr int64_t kPieceBytes = int64_t{128} << 20;
@@ -947,43 +900,6 @@ struct HeadPlan {
     }
 };
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                                               cudaEnableDefault, &r);
-        return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
-    }();
-    return fn;
-}
-
-// A row-major [depth][outer][inner] tensor in boxes of [1][box_outer][128 bytes].
-template <typename E>
-cudaError_t make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
-                     int64_t depth = 0) {
-    const EncodeFn fn = encode_fn();
-    if (!fn) return cudaErrorNotSupported;
-    const CUtensorMapDataType type = std::is_same<E, float>::value  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                     : std::is_same<E, bf16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const cuuint64_t size = sizeof(E);
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
-                                static_cast<cuuint64_t>(depth)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size,
-                                   static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(outer) * size};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_outer), 1};
-    const cuuint32_t one[3] = {1, 1, 1};
-    const CUresult r = fn(map, type, depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <typename T, int MODE, bool SUM>
 cudaError_t launch_head(const HeadMaps& maps, const HeadArgs& a, int64_t units, cudaStream_t s) {
     static int done[kMaxDevices];
@@ -1015,12 +931,6 @@ void set_tiles(HeadArgs& a, int n) {
     a.warp_columns = (n / 2 + 31) / 32 * 32;
     a.n_tiles = static_cast<int>(ceil_div(a.cols, n));
 }
-
-#define LS_CUDA(expr)                        \
-    do {                                     \
-        const cudaError_t _e = (expr);       \
-        if (_e != cudaSuccess) return _e;    \
-    } while (0)
 
 template <typename T>
 cudaError_t fwd(float* loss, float* lse, const void* x, const void* w, const int32_t* target, const HeadShape& sh,
