@@ -1,6 +1,7 @@
 """Build the C-ABI operator libraries for sm_103a with nvcc: ``libls_ops.so``
-(the layer operators, ``csrc/``) and ``libls_vocab.so`` (the vocabulary
-operators, ``csrc_vocab/``).
+(the layer operators, ``csrc/``), ``libls_vocab.so`` (the vocabulary
+operators, ``csrc_vocab/``) and ``libls_block.so`` (the decoder block's
+operators, ``csrc_block/``).
 
 A library's translation units compile in parallel and link into
 ``transformer_layer_non_gb300/_build/``.  A rebuild happens only when a source
@@ -26,6 +27,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libls_ops.so")
 VOCAB_CSRC = os.path.join(PKG, "csrc_vocab")
 VOCAB_LIB = os.path.join(BUILD, "libls_vocab.so")
+BLOCK_CSRC = os.path.join(PKG, "csrc_block")
+BLOCK_LIB = os.path.join(BUILD, "libls_block.so")
 # The benchmark's reference streaming kernel (not part of the operator library).
 FLOOR_SRC = os.path.join(PKG, "floor", "stream_floor.cu")
 FLOOR_LIB = os.path.join(BUILD, "libls_floor.so")
@@ -50,6 +53,10 @@ def vocab_sources():
     return sorted(glob.glob(os.path.join(VOCAB_CSRC, "*.cu")))
 
 
+def block_sources():
+    return sorted(glob.glob(os.path.join(BLOCK_CSRC, "*.cu")))
+
+
 def _headers():
     return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
         os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
@@ -58,6 +65,11 @@ def _headers():
 def _vocab_headers():
     return _headers() + glob.glob(os.path.join(VOCAB_CSRC, "*.cuh")) + glob.glob(
         os.path.join(VOCAB_CSRC, "*.h"))
+
+
+def _block_headers():
+    return _vocab_headers() + glob.glob(os.path.join(BLOCK_CSRC, "*.cuh")) + glob.glob(
+        os.path.join(BLOCK_CSRC, "*.h"))
 
 
 def _newer_than(lib: str, inputs) -> bool:
@@ -73,6 +85,10 @@ def up_to_date() -> bool:
 
 def vocab_up_to_date() -> bool:
     return _newer_than(VOCAB_LIB, vocab_sources() + _vocab_headers())
+
+
+def block_up_to_date() -> bool:
+    return _newer_than(BLOCK_LIB, block_sources() + _block_headers())
 
 
 def _compile_and_link(lib: str, srcs, obj_dir: str, verbose: bool, ptxas_verbose: bool) -> str:
@@ -118,6 +134,14 @@ def build_vocab(force: bool = False, verbose: bool = False, ptxas_verbose: bool 
                              ptxas_verbose)
 
 
+def build_block(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """Compile and link the decoder block's operators' library; returns its path."""
+    if not force and block_up_to_date():
+        return BLOCK_LIB
+    return _compile_and_link(BLOCK_LIB, block_sources(), os.path.join(BUILD, "block"), verbose,
+                             ptxas_verbose)
+
+
 def build_floor(force: bool = False) -> str:
     """Compile the benchmark's reference streaming kernel into libls_floor.so."""
     if (not force and os.path.exists(FLOOR_LIB)
@@ -142,4 +166,5 @@ if __name__ == "__main__":
     a = ap.parse_args()
     print(build(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
     print(build_vocab(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
+    print(build_block(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
     print(build_floor(force=a.force))

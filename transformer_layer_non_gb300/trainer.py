@@ -16,7 +16,7 @@ from __future__ import annotations
 
 from typing import Iterable, List
 
-from . import ls_ops
+from . import ls_block, ls_ops
 
 ALIGN_BYTES = 16
 
@@ -49,6 +49,8 @@ class LinkedParameters:
         self.exp_avg = torch.zeros(n, dtype=torch.float32, device=device)
         self.exp_avg_sq = torch.zeros(n, dtype=torch.float32, device=device)
         self.step = 0
+        self.grad_norm = None  # of the last step with max_norm: FP32 [1] on the device
+        self._factor = self._norm_ws = self._grad_list = None
         with torch.no_grad():
             for p, off in zip(self.params, self.offsets):
                 k = p.numel()
@@ -62,9 +64,25 @@ class LinkedParameters:
         self.grad_ws.zero_()
 
     def adam_step(self, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-                  weight_decay: float = 0.0, grad_scale: float = 1.0, stream=None):
-        """One fused Adam update of every linked parameter (one launch)."""
+                  weight_decay: float = 0.0, grad_scale: float = 1.0, stream=None,
+                  max_norm: float = None):
+        """One fused Adam update of every linked parameter (one launch).  With
+        max_norm the gradients are clipped to that global norm first, which
+        ``grad_norm`` then holds: two more launches, no copy of the gradients
+        and no synchronisation."""
         self.step += 1
-        ls_ops.ls_adam_update(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq, lr,
-                              beta1, beta2, eps, weight_decay, self.step, grad_scale,
-                              stream=stream)
+        if max_norm is None:
+            ls_ops.ls_adam_update(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq, lr,
+                                  beta1, beta2, eps, weight_decay, self.step, grad_scale,
+                                  stream=stream)
+            return
+        if self.grad_norm is None:
+            self.grad_norm, self._factor = (self.exp_avg.new_empty(1) for _ in range(2))
+            self._norm_ws = ls_block.new_workspace(ls_block.grad_norm_workspace_bytes(),
+                                                   self.grad_ws.device)
+            self._grad_list = ls_block.TensorList([self.grad_ws])
+        ls_block.ls_grad_norm(self.grad_norm, self._factor, self._grad_list, max_norm, grad_scale,
+                              workspace=self._norm_ws, stream=stream)
+        ls_block.ls_adam_update_scaled(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq,
+                                       self._factor, lr, beta1, beta2, eps, weight_decay, self.step,
+                                       stream=stream)
