@@ -200,3 +200,34 @@ def test_gradients_against_differences():
             value = float(got.view(-1)[e])
             # third derivatives of about 10 times step^2, 64-bit sums over step
             assert abs(diff - value) <= float(bound.view(-1)[e]) + float(torch.finfo(c.t).eps) * abs(diff) + 1e-8
+
+
+@pytest.mark.parametrize("sizes", [(16384, 72, 136), (33000, 64, 72), (40, 72, 33000), (3, 8, 65536), (2, 65536, 8)], ids=name)
+def test_long_sums(sizes):
+    """More rows than one accumulator adds up, more columns than one slice of dx holds, the widest sizes."""
+    c = Case("f16", *sizes, seed=6)
+    c.dh *= 0.05
+    h, eh, dx, edx, dw, edw = c.exact()
+    ref.check(c.forward(), h, eh + ref.half_step(c.t, h), "h")
+    gx, gw = c.backward()
+    ref.check(gx, dx, edx + ref.half_step(c.t, dx), "dx")
+    for got, want, bound in zip(gw, dw, edw):
+        ref.check(got, want, bound + ref.half_step(c.t, want), "dweight")
+    into = [torch.ones(t.shape, device="cuda") for t in dw]
+    _, gw = c.backward(into)
+    for got, want, bound in zip(gw, dw, edw):
+        ref.check(got, want + 1, bound + ref.U * 8 * (1 + want.abs()), "added")
+
+
+def test_sums_of_one_sign():
+    """dW as sums of 65536 terms of one sign: accumulators that took them all would lose 3.7e-4."""
+    require_gpu()
+    rows = 65536
+    c = Case("f16", rows, 8, 8, "relu")
+    c.x.fill_(1.0)
+    c.wg.fill_(0.125)
+    c.wu.fill_(0.125)
+    c.dh.fill_(2.0 ** -12)
+    _, gw = c.backward([torch.zeros(8, 8, device="cuda") for _ in range(2)])
+    for got in gw:  # dg = du = 2^-12, exactly
+        assert ((got.double() - 16.0).abs() <= 16.0 * (16384 * LOST + 4 * ref.U)).all()

@@ -1,10 +1,28 @@
 // gated.cu -- the gated feed-forward block: h = act(x Wg^T) * (x Wu^T), and its
-// gradients.
+// gradients, on tcgen05.
 //
-// Simple tiles: 64 x 64 outputs for each CTA, FP32 products of operands staged
-// through shared memory.  The backward computes both sums again, writes dg and
-// du in the storage type, and multiplies them with the weights and with x.
+// Forward: a tile has 256 rows and the same `half` columns of both projections.
+// They are one product whose second operand is Wg's rows in the pair's first CTA
+// and Wu's in its second, so that the accumulator has gate and up side by side
+// and one warp reads both of an element: the activation and the product never
+// leave registers.
+// Backward: the same tiles again, with dh; dg and du are rounded to the storage
+// type in the workspace.  Then dx = [dg du] [Wg; Wu] and dW = [dg du]^T x, in one
+// launch.  Computing g and u again costs 2 of 6 products; keeping them in 16 bits
+// instead would cost two more roundings in dg and du and 4 bytes for each element
+// of the block, in FP32 8.
+//
+// Persistent pairs of CTAs, each pair a tile of up to 256 x 256 with FP32
+// accumulators in tensor memory (two of them, so that one is read while the
+// other is filled), operands brought by TMA through a ring of 64-wide K blocks.
+// Warp 0 issues the copies, warp 1 of the pair's first CTA the products, the
+// other warps take the accumulators to the outputs.  Operands of which M or N is
+// the contiguous axis (the weights in dx; dg, du and x in dW) are read as they
+// lie in memory.
+#include <math.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "../csrc_vocab/tc_tile.cuh"
 #include "block_internal.h"
@@ -12,150 +30,424 @@
 namespace ls {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kTileM = 256;   // of a pair; 128 rows for each CTA
+constexpr int kTileN = 256;
+constexpr int kBlockK = 64;   // 128 bytes: the swizzle's row
+constexpr int kStages = 5;
+constexpr int kEpilogueWarps = 8;  // two for each quarter of the tensor memory's lanes, half the columns each
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kWarpBoxes = 2;      // a warp's store boxes
+constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;  // one operand of one CTA and stage
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr uint32_t kStoreBytes = 32 * 128;             // one warp's store box
+constexpr uint32_t kTmemColumns = 512;
+constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * kWarpBoxes * kStoreBytes;
+constexpr int kGroupM = 16;   // row tiles that share a sweep over the columns
+constexpr int kPairs = 76;    // pairs of SMs; a constant, so that plans depend on the shapes alone
+constexpr int kMostHalf = 128;
 
-struct ActValue {
-    float a, slope;  // act(g), act'(g)
+enum Mode { kFwd = 0, kGrad = 1, kOut = 2 };
+
+struct GatedArgs {
+    int rows, ffn, hidden;
+    int act;
+    int m_tiles, n_tiles;  // kFwd, kGrad: rows x ffn
+    int half;              // columns of h in a tile: 32, 64, 96 or 128
+    int row_box;           // rows of the copies with rows as M: 128, or all where there are fewer
+    int k_blocks;
+    const void* dh;        // kGrad
+    void *out, *out2;      // tiles of fewer than 128 columns: h; dg and du
+    // kOut
+    int slices, slice_blocks;  // of dx's K, dg's columns and then du's
+    int x_units, w_units;      // units of dx in a slice; units of both dW
+    int w_tiles;               // of one dW
+    int h_tiles, f_blocks;
+    int w_kb0, w_k_blocks;     // the rows that dW's sums run over in this launch
+    bool w_first, x_partial, w_f32, w_add;
 };
-__device__ __forceinline__ ActValue act_of(float g, int act) {
-    if (act == LS_ACT_RELU) return {g > 0.f ? g : 0.f, g > 0.f ? 1.f : 0.f};
-    if (act == LS_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-g));
-        return {g * s, s * (1.f + g * (1.f - s))};
-    }
-    if (act == LS_ACT_GELU) {
-        const float phi = 0.5f * erfcf(-g * 0.70710678f);
-        return {g * phi, phi + g * 0.39894228f * expf(-0.5f * g * g)};
-    }
-    const float k = 0.79788456f, t = tanhf(k * (g + 0.044715f * g * g * g));
-    return {0.5f * g * (1.f + t), 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * k * (1.f + 0.134145f * g * g)};
-}
 
-// A matrix of which rows or columns are contiguous.
-template <typename T> struct Matrix {
-    const T* p;
-    int64_t row, col;  // strides
-    int rows, cols;
-    __device__ __forceinline__ float at(int r, int c) const {
-        return r < rows && c < cols ? to_f32(p[r * row + c * col]) : 0.f;
-    }
+struct GatedMaps {
+    CUtensorMap a, b, b2;      // kFwd, kGrad: x, Wg, Wu;  kOut: dg for dx, Wg, Wu
+    CUtensorMap a2;            // kOut: du for dx
+    CUtensorMap wa, wa2, wb;   // kOut: dg, du, x for dW
+    CUtensorMap out, out2, out3;  // h; dg, du; dx, dWg, dWu
 };
 
-// Both products of a 64 x 64 tile: a (M x K) with b[0..N) (N x K), each thread 4 x 4 of it.
-template <typename T>
-__device__ __forceinline__ void multiply(const Matrix<T>& a, const Matrix<T>& b, int m0, int n0, float (&acc)[4][4]) {
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int k0 = 0; k0 < a.cols; k0 += kStep) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int r = i / kStep, k = i % kStep;
-            sa[k][r] = a.at(m0 + r, k0 + k);
-            sb[k][r] = b.at(n0 + r, k0 + k);
+// One unit of work of a pair.
+struct Unit {
+    int m0, n0;   // first row and column of the tile
+    int kb0, kbs;  // K blocks
+    int slice;
+    int weight;   // kOut: 0 a tile of dx, 1 of dWg, 2 of dWu
+};
+
+template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const GatedArgs& a) {
+    Unit t;
+    t.weight = 0;
+    t.slice = 0;
+    t.kb0 = 0;
+    if constexpr (MODE != kOut) {
+        const int g = u / (kGroupM * a.n_tiles);
+        const int first = g * kGroupM;
+        const int gm = min(kGroupM, a.m_tiles - first);
+        const int r = u - first * a.n_tiles;
+        t.n0 = (r / gm) * a.half;
+        t.m0 = (first + r % gm) * kTileM;
+        t.kbs = a.k_blocks;
+    } else {  // all of one kind, then all of the other
+        const int first = a.w_first ? a.w_units : a.slices * a.x_units;
+        int r = u;
+        const bool weight = (r >= first) != a.w_first;
+        if (r >= first) r -= first;
+        if (weight) {
+            t.weight = 1 + r / a.w_tiles;
+            r -= (t.weight - 1) * a.w_tiles;
+            t.kb0 = a.w_kb0;
+            t.kbs = a.w_k_blocks;
+        } else {
+            t.slice = r / a.x_units;
+            r -= t.slice * a.x_units;
+            t.kb0 = t.slice * a.slice_blocks;
+            t.kbs = min(a.slice_blocks, 2 * a.f_blocks - t.kb0);
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
+        t.n0 = (r % a.h_tiles) * kTileN;
+        t.m0 = (r / a.h_tiles) * kTileM;
+    }
+    return t;
+}
+template <int MODE> __device__ __forceinline__ int units_of(const GatedArgs& a) {
+    return MODE == kOut ? a.slices * a.x_units + a.w_units : a.m_tiles * a.n_tiles;
+}
+
+// act(g), and its slope.
+struct ActValue {
+    float a, slope;
+};
+__device__ __forceinline__ float sigmoid(float x) {
+    return __fdividef(1.f, 1.f + exp2_approx(-1.4426950408889634f * x));  // 0 where the exponential is infinite
+}
+template <int ACT> __device__ __forceinline__ ActValue act_of(float g) {
+    if constexpr (ACT == LS_ACT_RELU) {
+        return {g > 0.f ? g : g != g ? g : 0.f, g > 0.f ? 1.f : 0.f};
+    } else if constexpr (ACT == LS_ACT_SILU) {
+        const float s = sigmoid(g);
+        return {g * s, s * (1.f + g * (1.f - s))};
+    } else if constexpr (ACT == LS_ACT_GELU) {
+        const float phi = normcdff(g);
+        return {g * phi, phi + g * 0.3989422804014327f * exp2_approx(-0.7213475204444817f * g * g)};
+    } else {  // 0.5 (1 + tanh y) = sigmoid(2 y)
+        const float k = 1.5957691216057308f, q = g * g;
+        const float s = sigmoid(k * g * fmaf(0.044715f, q, 1.f));
+        const float t = s * (1.f - s);
+        return {g * s, s + (t > 0.f ? g * t * k * fmaf(0.134145f, q, 1.f) : 0.f)};
     }
 }
 
-// h, or with dh its gradients dg and du.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-gated_kernel(T* __restrict__ h, T* __restrict__ dg, T* __restrict__ du, const T* __restrict__ dh, Matrix<T> x, Matrix<T> wg,
-             Matrix<T> wu, int act) {
-    pdl_enter();
-    const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float g[4][4] = {}, u[4][4] = {};
-    multiply(x, wg, m0, n0, g);
-    multiply(x, wu, m0, n0, u);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = m0 + ty + 16 * i, f = n0 + tx + 16 * j;
-            if (r >= x.rows || f >= wg.rows) continue;
-            const int64_t e = static_cast<int64_t>(r) * wg.rows + f;
-            const ActValue v = act_of(g[i][j], act);
-            if (dh) {
-                const float d = to_f32(dh[e]);
-                dg[e] = from_f32<T>(d * u[i][j] * v.slope);
-                du[e] = from_f32<T>(d * v.a);
+// 32 values each of g and u to act(g) u, or with dh to dg and du in their places.
+template <int MODE, int ACT, typename T>
+__device__ __forceinline__ void combine(float (&g)[32], float (&u)[32], const uint4 (&dh)[4]) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        float d[kVec];
+        if constexpr (MODE == kGrad) unpack(Raw8<T>{dh[v]}, d);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const int i = v * kVec + j;
+            const ActValue a = act_of<ACT>(g[i]);
+            if constexpr (MODE == kFwd) {
+                g[i] = a.a * u[i];
             } else {
-                h[e] = from_f32<T>(v.a * u[i][j]);
+                g[i] = d[j] * u[i] * a.slope;
+                u[i] = d[j] * a.a;
             }
         }
-}
-
-// out (+)= a b^T + a2 b2^T
-template <typename T, typename O>
-__global__ void __launch_bounds__(kThreads)
-product_kernel(O* __restrict__ out, Matrix<T> a, Matrix<T> b, Matrix<T> a2, Matrix<T> b2, bool add) {
-    pdl_enter();
-    const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[4][4] = {};
-    multiply(a, b, m0, n0, acc);
-    if (a2.p) multiply(a2, b2, m0, n0, acc);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = m0 + ty + 16 * i, c = n0 + tx + 16 * j;
-            if (r >= a.rows || c >= b.rows) continue;
-            const int64_t e = static_cast<int64_t>(r) * b.rows + c;
-            out[e] = from_f32<O>(add ? to_f32(out[e]) + acc[i][j] : acc[i][j]);
-        }
-}
-
-// rows x cols, row-major, and transposed.
-template <typename T> Matrix<T> mat(const void* p, int64_t rows, int64_t cols) {
-    return Matrix<T>{static_cast<const T*>(p), cols, 1, static_cast<int>(rows), static_cast<int>(cols)};
-}
-template <typename T> Matrix<T> transposed(const void* p, int64_t rows, int64_t cols) {
-    return Matrix<T>{static_cast<const T*>(p), 1, cols, static_cast<int>(cols), static_cast<int>(rows)};
-}
-dim3 tiles(int64_t rows, int64_t cols) {
-    return dim3(static_cast<unsigned>(ceil_div(cols, kTile)), static_cast<unsigned>(ceil_div(rows, kTile)));
-}
-
-template <typename T>
-cudaError_t fwd(void* h, const void* x, const void* wg, const void* wu, const GatedShape& sh, cudaStream_t s) {
-    return launch_pdl(gated_kernel<T>, tiles(sh.rows, sh.ffn), dim3(kThreads), 0, s, static_cast<T*>(h), nullptr, nullptr,
-                      nullptr, mat<T>(x, sh.rows, sh.hidden), mat<T>(wg, sh.ffn, sh.hidden), mat<T>(wu, sh.ffn, sh.hidden),
-                      static_cast<int>(sh.act));
-}
-
-template <typename T, typename O>
-cudaError_t product(O* out, const Matrix<T>& a, const Matrix<T>& b, const Matrix<T>& a2, const Matrix<T>& b2, bool add,
-                    cudaStream_t s) {
-    return launch_pdl(product_kernel<T, O>, tiles(a.rows, b.rows), dim3(kThreads), 0, s, out, a, b, a2, b2, add);
-}
-
-template <typename T>
-cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const void* x, const void* wg, const void* wu,
-                const GatedShape& sh, void* workspace, cudaStream_t s) {
-    T* dg = static_cast<T*>(workspace);
-    T* du = dg + sh.rows * sh.ffn;
-    LS_CUDA(launch_pdl(gated_kernel<T>, tiles(sh.rows, sh.ffn), dim3(kThreads), 0, s, nullptr, dg, du,
-                       static_cast<const T*>(dh), mat<T>(x, sh.rows, sh.hidden), mat<T>(wg, sh.ffn, sh.hidden),
-                       mat<T>(wu, sh.ffn, sh.hidden), static_cast<int>(sh.act)));
-    const Matrix<T> none = {};
-    if (dx)
-        LS_CUDA(product(static_cast<T*>(dx), mat<T>(dg, sh.rows, sh.ffn), transposed<T>(wg, sh.ffn, sh.hidden),
-                        mat<T>(du, sh.rows, sh.ffn), transposed<T>(wu, sh.ffn, sh.hidden), false, s));
-    for (int k = 0; k < 2 && dwg; ++k) {
-        const Matrix<T> a = transposed<T>(k ? du : dg, sh.rows, sh.ffn), b = transposed<T>(x, sh.rows, sh.hidden);
-        void* dw = k ? dwu : dwg;
-        if (f32)
-            LS_CUDA(product(static_cast<float*>(dw), a, b, none, none, true, s));
-        else
-            LS_CUDA(product(static_cast<T*>(dw), a, b, none, none, false, s));
     }
-    return cudaSuccess;
+}
+template <int MODE, typename T>
+__device__ __forceinline__ void combine_act(int act, float (&g)[32], float (&u)[32], const uint4 (&dh)[4]) {
+    if (act == LS_ACT_SILU) combine<MODE, LS_ACT_SILU, T>(g, u, dh);
+    else if (act == LS_ACT_GELU) combine<MODE, LS_ACT_GELU, T>(g, u, dh);
+    else if (act == LS_ACT_GELU_TANH) combine<MODE, LS_ACT_GELU_TANH, T>(g, u, dh);
+    else combine<MODE, LS_ACT_RELU, T>(g, u, dh);
 }
 
-// Self-test of the waits' failure path: two warps wait on a barrier that expects an arrival nobody makes; the
-// first whose polls run out flags the failure, the other one sees it.
+template <typename T, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedArgs a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_at;
+    __shared__ volatile int dead;
+    // The swizzle's pattern repeats every 1024 bytes of the address.
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int units = units_of<MODE>(a);
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        dead = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(&drained, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + s, 1);
+            mbar_init(acc_empty + s, 2 * kEpilogueWarps);
+        }
+        mbar_init_fence();
+        prefetch_map(&maps.a);
+        prefetch_map(MODE == kOut || rank == 0 ? &maps.b : &maps.b2);
+    }
+    if (warp == 1) tmem_alloc(&tmem_at, kTmemColumns);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    pdl_enter();
+
+    // The copying and the multiplying warp stay converged: all lanes wait, one elected lane issues.
+    if (warp == 0) {
+        uint32_t it = 0;
+        for (int u = pair; u < units; u += pairs) {
+            const Unit t = unit_of<MODE>(u, a);
+            const int m = t.m0 + static_cast<int>(rank) * 128;
+            const int n = MODE == kOut ? t.n0 + static_cast<int>(rank) * 128 : t.n0;
+            const int b_rows = MODE == kOut ? 128 : a.half;
+            // Rows behind the last one are not copied: what the shared memory holds there reaches rows of the
+            // accumulator that nothing reads.
+            auto a_bytes = [&](int first) -> uint32_t {
+                return t.weight ? kOperandBytes : first < a.rows ? static_cast<uint32_t>(a.row_box) * 128 : 0;
+            };
+            const uint32_t bytes = 2 * b_rows * 128 + a_bytes(t.m0) + a_bytes(t.m0 + 128);  // of both CTAs
+            const bool has_a = a_bytes(m) > 0;
+            for (int kb = 0; kb < t.kbs; ++kb, ++it) {
+                const uint32_t s = it % kStages;
+                if (!wait_bar(empty + s, ((it / kStages) & 1) ^ 1, &dead)) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+                    const uint32_t bar = map_rank(full + s, 0);
+                    unsigned char* pa = smem + s * kStageBytes;
+                    unsigned char* pb = pa + kOperandBytes;
+                    if constexpr (MODE != kOut) {
+                        const int k = kb * kBlockK;
+                        if (has_a) tma_load_2d(pa, &maps.a, k, m, bar);
+                        tma_load_2d(pb, rank == 0 ? &maps.b : &maps.b2, k, n, bar);
+                    } else if (!t.weight) {
+                        const bool up = t.kb0 + kb >= a.f_blocks;
+                        const int k = (t.kb0 + kb - (up ? a.f_blocks : 0)) * kBlockK;
+                        const CUtensorMap* w = up ? &maps.b2 : &maps.b;
+                        if (has_a) tma_load_2d(pa, up ? &maps.a2 : &maps.a, k, m, bar);
+                        tma_load_2d(pb, w, n, k, bar);
+                        tma_load_2d(pb + kOperandBytes / 2, w, n + 64, k, bar);
+                    } else {
+                        const int k = (t.kb0 + kb) * kBlockK;
+                        const CUtensorMap* d = t.weight == 2 ? &maps.wa2 : &maps.wa;
+                        tma_load_2d(pa, d, m, k, bar);
+                        tma_load_2d(pa + kOperandBytes / 2, d, m + 64, k, bar);
+                        tma_load_2d(pb, &maps.wb, n, k, bar);
+                        tma_load_2d(pb + kOperandBytes / 2, &maps.wb, n + 64, k, bar);
+                    }
+                }
+                __syncwarp();
+            }
+            if (dead) break;
+        }
+        // After a failed wait: the copies in flight land before the CTA ends.
+        if (dead && rank == 0)
+            for (uint32_t s = 0; s < kStages && s < it; ++s) {
+                const uint32_t uses = (it - 1 - s) / kStages;  // its last use, counted from 0
+                for (uint32_t i = 0; i < kWaitPolls; ++i)
+                    if (mbar_try_wait(full + s, uses & 1)) break;
+            }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            constexpr bool kBf16 = std::is_same<T, bf16>::value;
+            const uint64_t kmajor = desc_base(16), mnmajor = desc_base(kOperandBytes / 2);
+            uint32_t it = 0, tile = 0;
+            for (int u = pair; u < units; u += pairs, ++tile) {
+                const Unit t = unit_of<MODE>(u, a);
+                const uint32_t acc = tile & 1;
+                if (!wait_bar(acc_empty + acc, ((tile >> 1) & 1) ^ 1, &dead)) break;
+                tc_fence_after();
+                // Which operands have M or N as their contiguous axis.
+                const bool a_mn = MODE == kOut && t.weight, b_mn = MODE == kOut;
+                const uint32_t idesc = instr_desc(kBf16, a_mn, b_mn, kTileM, MODE == kOut ? kTileN : 2 * a.half);
+                const uint64_t da = desc_at(a_mn ? mnmajor : kmajor, smem_u32(smem));
+                const uint64_t db = desc_at(b_mn ? mnmajor : kmajor, smem_u32(smem) + kOperandBytes);
+                // 16 values of K further on, in the descriptors' units of 16 bytes
+                const uint32_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
+                const uint32_t d = tmem + acc * kTileN;
+                for (int kb = 0; kb < t.kbs; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!wait_bar(full + s, (it / kStages) & 1, &dead)) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = s * (kStageBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < kBlockK / 16; ++k)
+                            tc_mma(d, da + (at + k * step_a), db + (at + k * step_b), idesc, kb + k > 0);
+                        tc_commit(empty + s);
+                    }
+                    __syncwarp();
+                }
+                if (dead) break;
+                if (elect_one()) tc_commit(acc_full + acc);
+                __syncwarp();
+            }
+            if (dead) {  // the products in flight end before their operands' memory is given back
+                if (elect_one()) tc_commit(&drained);
+                __syncwarp();
+                for (uint32_t i = 0; i < kWaitPolls; ++i)
+                    if (mbar_try_wait(&drained, 0)) break;
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3;         // the TMEM lanes this warp may read
+        const int part = (warp - 2) >> 2;  // its part of the tile's columns
+        unsigned char* const boxes = smem + kStages * kStageBytes + (warp - 2) * kWarpBoxes * kStoreBytes;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        uint32_t tile = 0, opened = 0;
+        for (int u = pair; u < units; u += pairs, ++tile) {
+            const Unit t = unit_of<MODE>(u, a);
+            const uint32_t acc = tile & 1;
+            const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
+            const int row = row0 + lane;
+            auto release = [&]() {  // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty + acc, 0));
+            };
+            if constexpr (MODE != kOut) {
+                const int chunks = a.half / 32, per = (chunks + 1) / 2;
+                const int c0 = part * per, cs = min(per, chunks - c0);  // its groups of 32 columns, 0 to 2
+                uint4 dh[2][4];
+                if constexpr (MODE == kGrad) {  // on its way while the products end
+                    const T* p = static_cast<const T*>(a.dh) + static_cast<int64_t>(row) * a.ffn;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const int f = t.n0 + (c0 + c) * 32 + v * kVec;
+                            dh[c][v] = c < cs && row < a.rows && f < a.ffn ? ld16(p + f) : make_uint4(0, 0, 0, 0);
+                        }
+                }
+                if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
+                tc_fence_after();
+                const uint32_t cols = lanes + acc * kTileN;
+                const bool boxed = a.half == kMostHalf;
+                unsigned char* box = boxes;
+                if (boxed) {  // the boxes are free: one of two for h, both for dg and du
+                    if constexpr (MODE == kFwd) box += (opened++ % kWarpBoxes) * kStoreBytes;
+                    if (lane == 0) bulk_wait_read<MODE == kFwd ? 1 : 0>();
+                    __syncwarp();
+                }
+                if (cs <= 0) release();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (c >= cs) break;
+                    float zg[32], zu[32];
+                    tmem_ld32(zg, cols + (c0 + c) * 32);
+                    tmem_ld32(zu, cols + a.half + (c0 + c) * 32);
+                    tmem_ld_wait(zg);
+                    tmem_ld_wait(zu);
+                    if (c + 1 == cs) release();
+                    combine_act<MODE, T>(a.act, zg, zu, dh[c]);
+                    if (boxed) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            put16(box, lane, c * 4 + j, pack8<T>(zg, 8 * j, 1.f));
+                            if constexpr (MODE == kGrad) put16(box + kStoreBytes, lane, c * 4 + j, pack8<T>(zu, 8 * j, 1.f));
+                        }
+                    } else if (row < a.rows) {
+                        const int f = t.n0 + (c0 + c) * 32;
+                        const int64_t e = static_cast<int64_t>(row) * a.ffn + f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (f + 8 * j < a.ffn) {
+                                st16(static_cast<T*>(a.out) + e + 8 * j, pack8<T>(zg, 8 * j, 1.f));
+                                if constexpr (MODE == kGrad)
+                                    st16(static_cast<T*>(a.out2) + e + 8 * j, pack8<T>(zu, 8 * j, 1.f));
+                            }
+                    }
+                }
+                if (boxed) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row0 < a.rows && t.n0 + c0 * 32 < a.ffn) {
+                            tma_store_2d(&maps.out, t.n0 + c0 * 32, row0, box);
+                            if constexpr (MODE == kGrad) tma_store_2d(&maps.out2, t.n0 + c0 * 32, row0, box + kStoreBytes);
+                        }
+                        bulk_commit();
+                    }
+                }
+            } else {
+                if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
+                tc_fence_after();
+                const int n0 = t.n0 + part * (kTileN / 2);
+                const uint32_t cols = lanes + part * (kTileN / 2) + acc * kTileN;
+                const bool f32 = t.weight ? a.w_f32 : a.x_partial;
+                const int n = a.hidden - n0;
+                const bool stores = row0 < (t.weight ? a.ffn : a.rows);
+                const CUtensorMap* w_out = t.weight == 2 ? &maps.out3 : &maps.out2;
+                unsigned char* box = boxes;
+                auto open_box = [&]() {  // the next store box, free to be written
+                    box = boxes + (opened++ % kWarpBoxes) * kStoreBytes;
+                    if (lane == 0) bulk_wait_read<kWarpBoxes - 1>();
+                    __syncwarp();
+                };
+                auto close_box = [&](auto&& store) {  // and on its way to memory
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (stores) store();
+                        bulk_commit();
+                    }
+                };
+                if (f32)
+                    sweep(cols, release, [&](int c, float (&z)[32]) {
+                        if (c * 32 >= n) return;
+                        open_box();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            put16(box, lane, j, f2u4(make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3])));
+                        close_box([&] {
+                            if (!t.weight)
+                                tma_store_3d(&maps.out, n0 + c * 32, row0, t.slice, box);
+                            else if (a.w_add)
+                                tma_add_2d(w_out, n0 + c * 32, row0, box);
+                            else
+                                tma_store_2d(w_out, n0 + c * 32, row0, box);
+                        });
+                    });
+                else
+                    sweep(cols, release, [&](int c, float (&z)[32]) {
+                        if (c * 32 >= n) return;
+                        if ((c & 1) == 0) open_box();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) put16(box, lane, (c & 1) * 4 + j, pack8<T>(z, 8 * j, 1.f));
+                        if ((c & 1) == 1 || c * 32 + 32 >= n)
+                            close_box([&] { tma_store_2d(t.weight ? w_out : &maps.out, n0 + (c & ~1) * 32, row0, box); });
+                    });
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free(tmem, kTmemColumns);
+}
+
+// Self-test of the waits' failure path: two warps wait, as those of gated_kernel do, on a barrier that expects
+// an arrival nobody makes; the first whose polls run out flags the failure, the other one sees it.
 __global__ void __launch_bounds__(64) wait_selftest_kernel(uint32_t polls) {
     __shared__ uint64_t bar;
     __shared__ volatile int dead;
@@ -168,15 +460,201 @@ __global__ void __launch_bounds__(64) wait_selftest_kernel(uint32_t polls) {
     wait_bar(&bar, 0, &dead, polls);
 }
 
+// out = the sum over the slices' FP32 sums, in slice order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+join_kernel(T* __restrict__ out, const float* __restrict__ part, int slices, int64_t nvec) {
+    pdl_enter();
+    const int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (v >= nvec) return;
+    float acc[kVec];
+    load8f<float>(part + v * kVec, acc);
+    for (int s = 1; s < slices; ++s) {
+        float f[kVec];
+        load8f<float>(part + (s * nvec + v) * kVec, f);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) acc[j] += f[j];
+    }
+    store8f<T>(out + v * kVec, acc);
+}
+
+// --- host ----------------------------------------------------------------------
+constexpr int64_t kMaxSlices = 16;
+// Tensor cores drop low bits as they accumulate: a sum of terms of one sign loses about 5.6e-9 of itself for
+// each of them.  No accumulator adds up more than these; what it has then is added in FP32.
+constexpr int64_t kMostRows = 16384;
+constexpr int64_t kMostColumns = 32768;
+
+// Columns of h in a tile: fewer than 128 for one or two tiles of rows where the busiest pair has less to do that
+// way.  A K block's time goes with the columns down to 64 of each projection, and a tile costs about one K block more.
+int half_columns(int64_t rows, int64_t hidden, int64_t ffn) {
+    if (rows > 2 * kTileM) return kMostHalf;
+    const int64_t m_tiles = ceil_div(rows, kTileM), k_blocks = ceil_div(hidden, kBlockK);
+    int best_half = kMostHalf;
+    int64_t best = INT64_MAX;
+    for (int half = kMostHalf; half >= 32; half -= 32) {
+        const int64_t t = ceil_div(m_tiles * ceil_div(ffn, half), kPairs) *
+                          ((std::max(2 * half, 128) + 8) * k_blocks + 2 * half + 256);
+        if (t < best) {
+            best = t;
+            best_half = half;
+        }
+    }
+    return best_half;
+}
+
+// Slices and workspace layout; they depend on the shapes alone.  Time is counted in K blocks of a pair's tile
+// (256 x 256 x 64 products, about 0.25 us).
+struct GatedPlan {
+    int64_t slices, slice_blocks;  // of dx's K
+    bool w_first;
+    size_t du, partial, w_partial, bytes;
+    GatedPlan(int64_t rows, int64_t hidden, int64_t ffn) {
+        const int64_t m_tiles = ceil_div(rows, kTileM), h_tiles = ceil_div(hidden, kTileN);
+        const int64_t kb = 2 * ceil_div(ffn, kBlockK);
+        const int64_t w_units = 2 * ceil_div(ffn, kTileM) * h_tiles, w_len = ceil_div(rows, kBlockK) + 1;
+        int64_t best = INT64_MAX;
+        for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
+            const int64_t len = ceil_div(kb, s);
+            if (ceil_div(kb, len) != s || len * kBlockK > kMostColumns) continue;
+            const int64_t x_units = s * m_tiles * h_tiles, x_len = len + 1 + (s > 1), units = x_units + w_units;
+            // Dealt to the pairs in turn, the longer ones first: what the pair with the most of it gets.
+            const bool longer_w = w_len > x_len;
+            const int64_t n_first = longer_w ? w_units : x_units;
+            int64_t out = 0;
+            for (const int64_t p : {int64_t{0}, n_first % kPairs, units % kPairs}) {
+                const int64_t n = n_first / kPairs + (p < n_first % kPairs);
+                const int64_t rest = units / kPairs + (p < units % kPairs) - n;
+                out = std::max(out, n * std::max(x_len, w_len) + rest * std::min(x_len, w_len));
+            }
+            // joining the slices: their bytes at about 1.7 MB for a K block's time
+            const int64_t t = out + (s > 1 ? 12 + s * rows * hidden * 4 / 1700000 : 0);
+            if (t < best) {
+                best = t;
+                slices = s;
+                slice_blocks = len;
+                w_first = longer_w;
+            }
+        }
+        du = round256(static_cast<size_t>(rows * ffn) * 2);
+        partial = 2 * du;
+        w_partial = partial + (slices > 1 ? round256(static_cast<size_t>(slices * rows * hidden) * 4) : 0);
+        bytes = w_partial + (rows > kMostRows ? 2 * round256(static_cast<size_t>(ffn * hidden) * 4) : 0);
+    }
+};
+
+template <typename T, int MODE>
+cudaError_t launch_gated(const GatedMaps& maps, const GatedArgs& a, int64_t units, cudaStream_t s) {
+    static int done[kMaxDevices];
+    const cudaError_t e = allow_max_dynamic_smem(gated_kernel<T, MODE>, done);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = std::min<int64_t>(units, kPairs);
+    return launch_pdl(gated_kernel<T, MODE>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes, s, maps, a);
+}
+
+// The forward's tiles, or with dh those of dg (out) and du (out2).
+template <typename T, int MODE>
+cudaError_t launch_tiles(void* out, void* out2, const void* dh, const void* x, const void* wg, const void* wu,
+                         const GatedShape& sh, cudaStream_t s) {
+    GatedArgs a = {};
+    a.rows = static_cast<int>(sh.rows);
+    a.hidden = static_cast<int>(sh.hidden);
+    a.ffn = static_cast<int>(sh.ffn);
+    a.act = static_cast<int>(sh.act);
+    a.half = half_columns(sh.rows, sh.hidden, sh.ffn);
+    a.m_tiles = static_cast<int>(ceil_div(sh.rows, kTileM));
+    a.n_tiles = static_cast<int>(ceil_div(sh.ffn, a.half));
+    a.k_blocks = static_cast<int>(ceil_div(sh.hidden, kBlockK));
+    a.row_box = static_cast<int>(std::min<int64_t>(sh.rows, 128));
+    a.dh = dh;
+    a.out = out;
+    a.out2 = out2;
+    GatedMaps maps = {};
+    LS_CUDA(make_map<T>(&maps.a, x, sh.hidden, sh.rows, sh.hidden, a.row_box));
+    LS_CUDA(make_map<T>(&maps.b, wg, sh.hidden, sh.ffn, sh.hidden, a.half));
+    LS_CUDA(make_map<T>(&maps.b2, wu, sh.hidden, sh.ffn, sh.hidden, a.half));
+    LS_CUDA(make_map<T>(&maps.out, out, sh.ffn, sh.rows, sh.ffn, 32));
+    if (MODE == kGrad) LS_CUDA(make_map<T>(&maps.out2, out2, sh.ffn, sh.rows, sh.ffn, 32));
+    return launch_gated<T, MODE>(maps, a, static_cast<int64_t>(a.m_tiles) * a.n_tiles, s);
+}
+
+template <typename T> cudaError_t join(void* out, const float* part, int64_t slices, int64_t n, cudaStream_t s) {
+    return launch_pdl(join_kernel<T>, dim3(static_cast<unsigned>(ceil_div(n / kVec, 256))), dim3(256), 0, s,
+                      static_cast<T*>(out), part, static_cast<int>(slices), n / kVec);
+}
+
+template <typename T>
+cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const void* x, const void* wg, const void* wu,
+                const GatedShape& sh, void* workspace, cudaStream_t s) {
+    const GatedPlan p(sh.rows, sh.hidden, sh.ffn);
+    char* ws = static_cast<char*>(workspace);
+    void *dg = ws, *du = ws + p.du;
+    float* partial = reinterpret_cast<float*>(ws + p.partial);
+    float* w_partial = reinterpret_cast<float*>(ws + p.w_partial);
+    LS_CUDA((launch_tiles<T, kGrad>(dg, du, dh, x, wg, wu, sh, s)));
+    GatedArgs a = {};
+    a.rows = static_cast<int>(sh.rows);
+    a.hidden = static_cast<int>(sh.hidden);
+    a.ffn = static_cast<int>(sh.ffn);
+    a.row_box = static_cast<int>(std::min<int64_t>(sh.rows, 128));
+    a.h_tiles = static_cast<int>(ceil_div(sh.hidden, kTileN));
+    a.f_blocks = static_cast<int>(ceil_div(sh.ffn, kBlockK));
+    a.slices = static_cast<int>(p.slices);
+    a.slice_blocks = static_cast<int>(p.slice_blocks);
+    a.x_units = dx ? static_cast<int>(ceil_div(sh.rows, kTileM)) * a.h_tiles : 0;
+    a.w_tiles = static_cast<int>(ceil_div(sh.ffn, kTileM)) * a.h_tiles;
+    a.w_units = dwg ? 2 * a.w_tiles : 0;
+    a.w_first = p.w_first;
+    a.x_partial = p.slices > 1;
+    GatedMaps m = {};
+    LS_CUDA(make_map<T>(&m.a, dg, sh.ffn, sh.rows, sh.ffn, a.row_box));
+    LS_CUDA(make_map<T>(&m.a2, du, sh.ffn, sh.rows, sh.ffn, a.row_box));
+    LS_CUDA(make_map<T>(&m.b, wg, sh.hidden, sh.ffn, sh.hidden, 64));
+    LS_CUDA(make_map<T>(&m.b2, wu, sh.hidden, sh.ffn, sh.hidden, 64));
+    LS_CUDA(make_map<T>(&m.wa, dg, sh.ffn, sh.rows, sh.ffn, 64));
+    LS_CUDA(make_map<T>(&m.wa2, du, sh.ffn, sh.rows, sh.ffn, 64));
+    LS_CUDA(make_map<T>(&m.wb, x, sh.hidden, sh.rows, sh.hidden, 64));
+    if (dx && a.x_partial)
+        LS_CUDA(make_map<float>(&m.out, partial, sh.hidden, sh.rows, sh.hidden, 32, p.slices));
+    else if (dx)
+        LS_CUDA(make_map<T>(&m.out, dx, sh.hidden, sh.rows, sh.hidden, 32));
+    // dW's sums over the rows, kMostRows of them at a time: added to FP32 gradients, or to scratch.
+    const bool scratch = dwg && !f32 && sh.rows > kMostRows;
+    const int64_t w_elements = sh.ffn * sh.hidden;
+    float* scratch2 = w_partial + round256(static_cast<size_t>(w_elements) * 4) / 4;
+    a.w_f32 = f32 || scratch;
+    if (dwg && a.w_f32) {
+        LS_CUDA(make_map<float>(&m.out2, scratch ? w_partial : dwg, sh.hidden, sh.ffn, sh.hidden, 32));
+        LS_CUDA(make_map<float>(&m.out3, scratch ? scratch2 : dwu, sh.hidden, sh.ffn, sh.hidden, 32));
+    } else if (dwg) {
+        LS_CUDA(make_map<T>(&m.out2, dwg, sh.hidden, sh.ffn, sh.hidden, 32));
+        LS_CUDA(make_map<T>(&m.out3, dwu, sh.hidden, sh.ffn, sh.hidden, 32));
+    }
+    a.w_add = f32;
+    const int64_t row_blocks = ceil_div(sh.rows, kBlockK), most = kMostRows / kBlockK;
+    for (int64_t kb = 0; kb < (dwg ? row_blocks : 1); kb += most) {
+        a.w_kb0 = static_cast<int>(kb);
+        a.w_k_blocks = static_cast<int>(std::min(most, row_blocks - kb));
+        LS_CUDA((launch_gated<T, kOut>(m, a, static_cast<int64_t>(a.slices) * a.x_units + a.w_units, s)));
+        a.x_units = 0;
+        a.w_add = true;
+    }
+    if (scratch) {
+        LS_CUDA(join<T>(dwg, w_partial, 1, w_elements, s));
+        LS_CUDA(join<T>(dwu, scratch2, 1, w_elements, s));
+    }
+    if (dx && a.x_partial) LS_CUDA(join<T>(dx, partial, p.slices, sh.rows * sh.hidden, s));
+    return cudaSuccess;
+}
+
 }  // namespace
 
-size_t gated_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn) {
-    return round256(static_cast<size_t>(rows * ffn) * 4);
-}
+size_t gated_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn) { return GatedPlan(rows, hidden, ffn).bytes; }
 
 cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg, const void* wu,
                              const GatedShape& sh, cudaStream_t s) {
-    return dt == LS_F16 ? fwd<__half>(h, x, wg, wu, sh, s) : fwd<bf16>(h, x, wg, wu, sh, s);
+    if (dt == LS_F16) return launch_tiles<__half, kFwd>(h, nullptr, nullptr, x, wg, wu, sh, s);
+    return launch_tiles<bf16, kFwd>(h, nullptr, nullptr, x, wg, wu, sh, s);
 }
 
 cudaError_t launch_gated_bwd(ls_dtype dt, void* dx, void* dwg, void* dwu, bool f32_dweight,
