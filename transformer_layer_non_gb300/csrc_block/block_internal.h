@@ -28,7 +28,7 @@ struct HeadsCall {
     float eps;
     void* workspace;
 };
-constexpr int kPartialCtas = 304;  // CTAs that hold sums of the weights' gradients: two on each of 152 SMs
+constexpr int kPartialCtas = 608;  // CTAs that hold sums of the weights' gradients: four on each of 152 SMs
 inline size_t heads_workspace_bytes(int64_t dim) { return static_cast<size_t>(kPartialCtas * dim) * sizeof(float); }
 template <typename T> cudaError_t launch_heads(const HeadsCall& c, cudaStream_t s);
 cudaError_t launch_heads_dtype(ls_dtype dt, const HeadsCall& c, cudaStream_t s);
@@ -58,6 +58,10 @@ cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg
 cudaError_t launch_gated_bwd(ls_dtype dt, void* dx, void* dwg, void* dwu, bool f32_dweight,
                              const void* dh, const void* x, const void* wg, const void* wu,
                              const GatedShape& sh, void* workspace, cudaStream_t s);
+// The forward of few rows (gated_few.cu): whether these sizes are its own, and its launch.
+bool gated_few_rows(int64_t rows);
+cudaError_t launch_gated_few(ls_dtype dt, void* h, const void* x, const void* wg, const void* wu,
+                             const GatedShape& sh, cudaStream_t s);
 cudaError_t launch_block_wait_selftest(uint32_t polls, cudaStream_t s);
 cudaError_t gated_take_device_error(unsigned int* flags);
 

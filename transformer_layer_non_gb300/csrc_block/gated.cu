@@ -26,6 +26,7 @@
 
 #include "../csrc_vocab/tc_tile.cuh"
 #include "block_internal.h"
+#include "gated_act.cuh"
 
 namespace ls {
 namespace {
@@ -64,6 +65,7 @@ struct GatedArgs {
     int h_tiles, f_blocks;
     int w_kb0, w_k_blocks;     // the rows that dW's sums run over in this launch
     bool w_first, x_partial, w_f32, w_add;
+    int pairs1, first_short1;  // how the shorter units are dealt, see Deal
 };
 
 struct GatedMaps {
@@ -115,33 +117,40 @@ template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const GatedAr
     }
     return t;
 }
-template <int MODE> __device__ __forceinline__ int units_of(const GatedArgs& a) {
-    return MODE == kOut ? a.slices * a.x_units + a.w_units : a.m_tiles * a.n_tiles;
-}
 
-// act(g), and its slope.
-struct ActValue {
-    float a, slope;
-};
-__device__ __forceinline__ float sigmoid(float x) {
-    return __fdividef(1.f, 1.f + exp2_approx(-1.4426950408889634f * x));  // 0 where the exponential is infinite
-}
-template <int ACT> __device__ __forceinline__ ActValue act_of(float g) {
-    if constexpr (ACT == LS_ACT_RELU) {
-        return {g > 0.f ? g : g != g ? g : 0.f, g > 0.f ? 1.f : 0.f};
-    } else if constexpr (ACT == LS_ACT_SILU) {
-        const float s = sigmoid(g);
-        return {g * s, s * (1.f + g * (1.f - s))};
-    } else if constexpr (ACT == LS_ACT_GELU) {
-        const float phi = normcdff(g);
-        return {g * phi, phi + g * 0.3989422804014327f * exp2_approx(-0.7213475204444817f * g * g)};
-    } else {  // 0.5 (1 + tanh y) = sigmoid(2 y)
-        const float k = 1.5957691216057308f, q = g * g;
-        const float s = sigmoid(k * g * fmaf(0.044715f, q, 1.f));
-        const float t = s * (1.f - s);
-        return {g * s, s + (t > 0.f ? g * t * k * fmaf(0.134145f, q, 1.f) : 0.f)};
+// The units of a pair, one after the other: its number'th in turn of the tiles.  kOut: the longer units in turn,
+// then the shorter ones, of which the pairs that got one more of the longer (the first `pairs1`) have those from
+// number `first_short1` on among themselves, and the others those before it.
+template <int MODE> struct PairUnits {
+    int u, step, end;
+    int next, next_step, next_end;  // the shorter ones
+    __device__ __forceinline__ PairUnits(int pair, int pairs, const GatedArgs& a) {
+        u = pair;
+        step = pairs;
+        end = MODE == kOut ? (a.w_first ? a.w_units : a.slices * a.x_units) : a.m_tiles * a.n_tiles;
+        if constexpr (MODE == kOut) {
+            const int all = a.slices * a.x_units + a.w_units;
+            const bool more = pair < a.pairs1;
+            next = end + (more ? a.first_short1 + pair : pair - a.pairs1);
+            next_step = more ? a.pairs1 : pairs - a.pairs1;
+            next_end = more ? all : end + a.first_short1;
+            settle();
+        }
     }
-}
+    __device__ __forceinline__ void settle() {
+        if (MODE == kOut && u >= end) {
+            u = next;
+            step = next_step;
+            end = next_end;
+            next = next_end;  // none behind these
+        }
+    }
+    __device__ __forceinline__ bool there() const { return u < end; }
+    __device__ __forceinline__ void advance() {
+        u += step;
+        settle();
+    }
+};
 
 // 32 values each of g and u to act(g) u, or with dh to dg and du in their places.
 template <int MODE, int ACT, typename T>
@@ -182,7 +191,6 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int units = units_of<MODE>(a);
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -211,8 +219,8 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     // The copying and the multiplying warp stay converged: all lanes wait, one elected lane issues.
     if (warp == 0) {
         uint32_t it = 0;
-        for (int u = pair; u < units; u += pairs) {
-            const Unit t = unit_of<MODE>(u, a);
+        for (PairUnits<MODE> p(pair, pairs, a); p.there(); p.advance()) {
+            const Unit t = unit_of<MODE>(p.u, a);
             const int m = t.m0 + static_cast<int>(rank) * 128;
             const int n = MODE == kOut ? t.n0 + static_cast<int>(rank) * 128 : t.n0;
             const int b_rows = MODE == kOut ? 128 : a.half;
@@ -268,8 +276,8 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
             constexpr bool kBf16 = std::is_same<T, bf16>::value;
             const uint64_t kmajor = desc_base(16), mnmajor = desc_base(kOperandBytes / 2);
             uint32_t it = 0, tile = 0;
-            for (int u = pair; u < units; u += pairs, ++tile) {
-                const Unit t = unit_of<MODE>(u, a);
+            for (PairUnits<MODE> p(pair, pairs, a); p.there(); p.advance(), ++tile) {
+                const Unit t = unit_of<MODE>(p.u, a);
                 const uint32_t acc = tile & 1;
                 if (!wait_bar(acc_empty + acc, ((tile >> 1) & 1) ^ 1, &dead)) break;
                 tc_fence_after();
@@ -312,8 +320,8 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
         unsigned char* const boxes = smem + kStages * kStageBytes + (warp - 2) * kWarpBoxes * kStoreBytes;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         uint32_t tile = 0, opened = 0;
-        for (int u = pair; u < units; u += pairs, ++tile) {
-            const Unit t = unit_of<MODE>(u, a);
+        for (PairUnits<MODE> p(pair, pairs, a); p.there(); p.advance(), ++tile) {
+            const Unit t = unit_of<MODE>(p.u, a);
             const uint32_t acc = tile & 1;
             const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
             const int row = row0 + lane;
@@ -327,13 +335,13 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                 const int c0 = part * per, cs = min(per, chunks - c0);  // its groups of 32 columns, 0 to 2
                 uint4 dh[2][4];
                 if constexpr (MODE == kGrad) {  // on its way while the products end
-                    const T* p = static_cast<const T*>(a.dh) + static_cast<int64_t>(row) * a.ffn;
+                    const T* d = static_cast<const T*>(a.dh) + static_cast<int64_t>(row) * a.ffn;
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             const int f = t.n0 + (c0 + c) * 32 + v * kVec;
-                            dh[c][v] = c < cs && row < a.rows && f < a.ffn ? ld16(p + f) : make_uint4(0, 0, 0, 0);
+                            dh[c][v] = c < cs && row < a.rows && f < a.ffn ? ld16(d + f) : make_uint4(0, 0, 0, 0);
                         }
                 }
                 if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
@@ -503,6 +511,26 @@ int half_columns(int64_t rows, int64_t hidden, int64_t ffn) {
     return best_half;
 }
 
+// Units of two lengths dealt to the pairs: the longer ones in turn, the shorter ones so that the pair with the
+// most to do has as little as can be: `each1` for each of the first `pairs1` pairs, which have one more of the
+// longer, the rest for the others.
+struct Deal {
+    int64_t pairs1, short1, most;  // short1: shorter units for the first pairs
+    Deal(int64_t n_long, int64_t len_long, int64_t n_short, int64_t len_short) {
+        const int64_t pairs = std::min<int64_t>(kPairs, n_long + n_short), base = n_long / pairs;
+        pairs1 = n_long % pairs;
+        most = INT64_MAX;
+        for (int64_t each1 = 0; each1 <= ceil_div(n_short, pairs); ++each1) {
+            const int64_t s1 = std::min(n_short, pairs1 * each1);
+            const int64_t load1 = pairs1 ? (base + 1) * len_long + ceil_div(s1, pairs1) * len_short : 0;
+            const int64_t load0 = base * len_long + ceil_div(n_short - s1, pairs - pairs1) * len_short;
+            if (std::max(load1, load0) >= most) continue;
+            most = std::max(load1, load0);
+            short1 = s1;
+        }
+    }
+};
+
 // Slices and workspace layout; they depend on the shapes alone.  Time is counted in K blocks of a pair's tile
 // (256 x 256 x 64 products, about 0.25 us).
 struct GatedPlan {
@@ -517,16 +545,9 @@ struct GatedPlan {
         for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
             const int64_t len = ceil_div(kb, s);
             if (ceil_div(kb, len) != s || len * kBlockK > kMostColumns) continue;
-            const int64_t x_units = s * m_tiles * h_tiles, x_len = len + 1 + (s > 1), units = x_units + w_units;
-            // Dealt to the pairs in turn, the longer ones first: what the pair with the most of it gets.
+            const int64_t x_units = s * m_tiles * h_tiles, x_len = len + 1 + (s > 1);
             const bool longer_w = w_len > x_len;
-            const int64_t n_first = longer_w ? w_units : x_units;
-            int64_t out = 0;
-            for (const int64_t p : {int64_t{0}, n_first % kPairs, units % kPairs}) {
-                const int64_t n = n_first / kPairs + (p < n_first % kPairs);
-                const int64_t rest = units / kPairs + (p < units % kPairs) - n;
-                out = std::max(out, n * std::max(x_len, w_len) + rest * std::min(x_len, w_len));
-            }
+            const int64_t out = longer_w ? Deal(w_units, w_len, x_units, x_len).most : Deal(x_units, x_len, w_units, w_len).most;
             // joining the slices: their bytes at about 1.7 MB for a K block's time
             const int64_t t = out + (s > 1 ? 12 + s * rows * hidden * 4 / 1700000 : 0);
             if (t < best) {
@@ -635,7 +656,13 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
     for (int64_t kb = 0; kb < (dwg ? row_blocks : 1); kb += most) {
         a.w_kb0 = static_cast<int>(kb);
         a.w_k_blocks = static_cast<int>(std::min(most, row_blocks - kb));
-        LS_CUDA((launch_gated<T, kOut>(m, a, static_cast<int64_t>(a.slices) * a.x_units + a.w_units, s)));
+        const int64_t x_units = static_cast<int64_t>(a.slices) * a.x_units;
+        const int64_t x_len = a.slice_blocks + 1 + (a.slices > 1), w_len = a.w_k_blocks + 1;
+        const Deal d(a.w_first ? a.w_units : x_units, a.w_first ? w_len : x_len, a.w_first ? x_units : a.w_units,
+                     a.w_first ? x_len : w_len);
+        a.pairs1 = static_cast<int>(d.pairs1);
+        a.first_short1 = static_cast<int>((a.w_first ? x_units : a.w_units) - d.short1);
+        LS_CUDA((launch_gated<T, kOut>(m, a, x_units + a.w_units, s)));
         a.x_units = 0;
         a.w_add = true;
     }
@@ -653,6 +680,7 @@ size_t gated_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn) { return
 
 cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg, const void* wu,
                              const GatedShape& sh, cudaStream_t s) {
+    if (gated_few_rows(sh.rows)) return launch_gated_few(dt, h, x, wg, wu, sh, s);
     if (dt == LS_F16) return launch_tiles<__half, kFwd>(h, nullptr, nullptr, x, wg, wu, sh, s);
     return launch_tiles<bf16, kFwd>(h, nullptr, nullptr, x, wg, wu, sh, s);
 }
