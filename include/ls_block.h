@@ -200,8 +200,8 @@ ls_status ls_gated_linear_bwd(ls_dtype dtype, void* dx, void* dgate_weight, void
                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of ls_gated_linear_bwd: dg and du, up to 16 FP32 copies of
- * dx and, beyond 16384 rows, FP32 sums of the weights' gradients.  0 for
- * invalid sizes.  The forward needs none. */
+ * dx, and FP32 sums of the weights' gradients (one of each beyond 16384 rows, up
+ * to 8 of small weights).  0 for invalid sizes.  The forward needs none. */
 size_t ls_gated_linear_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn);
 
 /* --- The norm of many gradients, clipping, and the update ---------------------

@@ -79,7 +79,7 @@ class Case:
 
 SIZES = [(1, 8, 8), (1, 1280, 5120), (2, 64, 128), (3, 72, 136), (5, 40, 1000), (16, 520, 264), (17, 128, 64), (31, 256, 520),
          (64, 200, 328), (100, 1032, 72), (127, 64, 264), (128, 72, 256), (129, 136, 128), (255, 64, 136), (257, 328, 520),
-         (300, 8, 2056), (513, 264, 8), (700, 512, 1032), (1000, 72, 4104)]
+         (300, 8, 2056), (513, 264, 8), (700, 512, 1032), (1000, 72, 4104), (5000, 136, 264)]
 
 
 def name(v):
@@ -114,7 +114,7 @@ def test_activations(act, rows):
             ref.check(got, want, bound + ref.half_step(c.t, want), "dweight")
 
 
-@pytest.mark.parametrize("sizes", [(1, 64, 136), (70, 264, 520), (400, 72, 1032)], ids=name)
+@pytest.mark.parametrize("sizes", [(1, 64, 136), (70, 264, 520), (400, 72, 1032), (3000, 264, 136)], ids=name)
 def test_gradients_added_in_fp32_and_left_out(sizes):
     c = Case("bf16", *sizes, seed=4)
     _, _, dx, edx, dw, edw = c.exact()

@@ -61,10 +61,11 @@ struct GatedArgs {
     // kOut
     int slices, slice_blocks;  // of dx's K, dg's columns and then du's
     int x_units, w_units;      // units of dx in a slice; units of both dW
-    int w_tiles;               // of one dW
+    int w_tiles;               // of one dW, in a slice
+    int w_slice_blocks;        // of the rows
     int h_tiles, f_blocks;
     int w_kb0, w_k_blocks;     // the rows that dW's sums run over in this launch
-    bool w_first, x_partial, w_f32, w_add;
+    bool w_first, x_partial, w_partial, w_f32, w_add;  // partial: FP32 sums of slices go to scratch
     int pairs1, first_short1;  // how the shorter units are dealt, see Deal
 };
 
@@ -102,10 +103,12 @@ template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const GatedAr
         const bool weight = (r >= first) != a.w_first;
         if (r >= first) r -= first;
         if (weight) {
+            t.slice = r / (2 * a.w_tiles);
+            r -= t.slice * 2 * a.w_tiles;
             t.weight = 1 + r / a.w_tiles;
             r -= (t.weight - 1) * a.w_tiles;
-            t.kb0 = a.w_kb0;
-            t.kbs = a.w_k_blocks;
+            t.kb0 = a.w_kb0 + t.slice * a.w_slice_blocks;
+            t.kbs = min(a.w_slice_blocks, a.w_k_blocks - t.slice * a.w_slice_blocks);
         } else {
             t.slice = r / a.x_units;
             r -= t.slice * a.x_units;
@@ -344,6 +347,19 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                             dh[c][v] = c < cs && row < a.rows && f < a.ffn ? ld16(d + f) : make_uint4(0, 0, 0, 0);
                         }
                 }
+                if constexpr (MODE == kGrad) {  // and the next tile's on its way to L2
+                    PairUnits<MODE> q = p;
+                    q.advance();
+                    if (q.there()) {
+                        const Unit n = unit_of<MODE>(q.u, a);
+                        const int r = n.m0 + static_cast<int>(rank) * 128 + quad * 32 + lane, f = n.n0 + c0 * 32;
+                        if (r < a.rows && f < a.ffn) {
+                            const T* d = static_cast<const T*>(a.dh) + static_cast<int64_t>(r) * a.ffn + f;
+                            prefetch_l2(d);
+                            prefetch_l2(d + min(cs * 32, a.ffn - f) - 1);
+                        }
+                    }
+                }
                 if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
                 tc_fence_after();
                 const uint32_t cols = lanes + acc * kTileN;
@@ -425,8 +441,8 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                         for (int j = 0; j < 8; ++j)
                             put16(box, lane, j, f2u4(make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3])));
                         close_box([&] {
-                            if (!t.weight)
-                                tma_store_3d(&maps.out, n0 + c * 32, row0, t.slice, box);
+                            if (!t.weight || a.w_partial)
+                                tma_store_3d(t.weight ? w_out : &maps.out, n0 + c * 32, row0, t.slice, box);
                             else if (a.w_add)
                                 tma_add_2d(w_out, n0 + c * 32, row0, box);
                             else
@@ -468,13 +484,17 @@ __global__ void __launch_bounds__(64) wait_selftest_kernel(uint32_t polls) {
     wait_bar(&bar, 0, &dead, polls);
 }
 
-// out = the sum over the slices' FP32 sums, in slice order.
-template <typename T>
+// out (+)= the sum over the slices' FP32 sums, in slice order; for blockIdx.y == 1 out2, of the sums behind them.
+template <typename O>
 __global__ void __launch_bounds__(256)
-join_kernel(T* __restrict__ out, const float* __restrict__ part, int slices, int64_t nvec) {
+join_kernel(O* __restrict__ out, O* __restrict__ out2, const float* __restrict__ part, int slices, int64_t nvec, bool add) {
     pdl_enter();
     const int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (v >= nvec) return;
+    if (blockIdx.y) {
+        out = out2;
+        part += slices * nvec * kVec;
+    }
     float acc[kVec];
     load8f<float>(part + v * kVec, acc);
     for (int s = 1; s < slices; ++s) {
@@ -483,7 +503,13 @@ join_kernel(T* __restrict__ out, const float* __restrict__ part, int slices, int
 #pragma unroll
         for (int j = 0; j < kVec; ++j) acc[j] += f[j];
     }
-    store8f<T>(out + v * kVec, acc);
+    if (add) {
+        float f[kVec];
+        load8f<O>(out + v * kVec, f);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) acc[j] += f[j];
+    }
+    store8f<O>(out + v * kVec, acc);
 }
 
 // --- host ----------------------------------------------------------------------
@@ -520,7 +546,9 @@ struct Deal {
         const int64_t pairs = std::min<int64_t>(kPairs, n_long + n_short), base = n_long / pairs;
         pairs1 = n_long % pairs;
         most = INT64_MAX;
-        for (int64_t each1 = 0; each1 <= ceil_div(n_short, pairs); ++each1) {
+        // both kinds of pairs end together near this number, which the rounding up moves by one at most
+        const int64_t even = (n_short * len_short - len_long * (pairs - pairs1)) / (len_short * pairs);
+        for (int64_t each1 = std::max<int64_t>(0, even - 1); each1 <= std::max<int64_t>(0, even + 2); ++each1) {
             const int64_t s1 = std::min(n_short, pairs1 * each1);
             const int64_t load1 = pairs1 ? (base + 1) * len_long + ceil_div(s1, pairs1) * len_short : 0;
             const int64_t load0 = base * len_long + ceil_div(n_short - s1, pairs - pairs1) * len_short;
@@ -534,33 +562,43 @@ struct Deal {
 // Slices and workspace layout; they depend on the shapes alone.  Time is counted in K blocks of a pair's tile
 // (256 x 256 x 64 products, about 0.25 us).
 struct GatedPlan {
-    int64_t slices, slice_blocks;  // of dx's K
+    int64_t slices, slice_blocks;      // of dx's K
+    int64_t w_slices, w_slice_blocks;  // of the rows, for dW
     bool w_first;
     size_t du, partial, w_partial, bytes;
     GatedPlan(int64_t rows, int64_t hidden, int64_t ffn) {
         const int64_t m_tiles = ceil_div(rows, kTileM), h_tiles = ceil_div(hidden, kTileN);
-        const int64_t kb = 2 * ceil_div(ffn, kBlockK);
-        const int64_t w_units = 2 * ceil_div(ffn, kTileM) * h_tiles, w_len = ceil_div(rows, kBlockK) + 1;
+        const int64_t kb = 2 * ceil_div(ffn, kBlockK), row_blocks = ceil_div(rows, kBlockK);
+        const int64_t w_tiles = 2 * ceil_div(ffn, kTileM) * h_tiles;
+        // joining slices: a launch, and their bytes at about 1.7 MB for a K block's time
+        auto join = [](int64_t n, int64_t elements) { return n > 1 ? 12 + n * elements * 4 / 1700000 : 0; };
         int64_t best = INT64_MAX;
-        for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
-            const int64_t len = ceil_div(kb, s);
-            if (ceil_div(kb, len) != s || len * kBlockK > kMostColumns) continue;
-            const int64_t x_units = s * m_tiles * h_tiles, x_len = len + 1 + (s > 1);
-            const bool longer_w = w_len > x_len;
-            const int64_t out = longer_w ? Deal(w_units, w_len, x_units, x_len).most : Deal(x_units, x_len, w_units, w_len).most;
-            // joining the slices: their bytes at about 1.7 MB for a K block's time
-            const int64_t t = out + (s > 1 ? 12 + s * rows * hidden * 4 / 1700000 : 0);
-            if (t < best) {
+        // Rows are cut where a small model's weights would leave most pairs without a tile of dW.
+        const int64_t most_w = w_tiles < kPairs && rows <= kMostRows ? std::min<int64_t>(row_blocks, 8) : 1;
+        for (int64_t sw = 1; sw <= most_w; ++sw) {
+            const int64_t w_part = ceil_div(row_blocks, sw), w_len = w_part + 1 + (sw > 1);
+            if (ceil_div(row_blocks, w_part) != sw) continue;
+            for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
+                const int64_t len = ceil_div(kb, s);
+                if (ceil_div(kb, len) != s || len * kBlockK > kMostColumns) continue;
+                const int64_t x_units = s * m_tiles * h_tiles, x_len = len + 1 + (s > 1), w_units = sw * w_tiles;
+                const bool longer_w = w_len > x_len;
+                const int64_t out = longer_w ? Deal(w_units, w_len, x_units, x_len).most : Deal(x_units, x_len, w_units, w_len).most;
+                const int64_t t = out + join(s, rows * hidden) + join(sw, 2 * ffn * hidden);
+                if (t >= best) continue;
                 best = t;
                 slices = s;
                 slice_blocks = len;
+                w_slices = sw;
+                w_slice_blocks = w_part;
                 w_first = longer_w;
             }
         }
         du = round256(static_cast<size_t>(rows * ffn) * 2);
         partial = 2 * du;
         w_partial = partial + (slices > 1 ? round256(static_cast<size_t>(slices * rows * hidden) * 4) : 0);
-        bytes = w_partial + (rows > kMostRows ? 2 * round256(static_cast<size_t>(ffn * hidden) * 4) : 0);
+        const bool scratch = w_slices > 1 || rows > kMostRows;
+        bytes = w_partial + (scratch ? round256(static_cast<size_t>(2 * w_slices * ffn * hidden) * 4) : 0);
     }
 };
 
@@ -599,9 +637,10 @@ cudaError_t launch_tiles(void* out, void* out2, const void* dh, const void* x, c
     return launch_gated<T, MODE>(maps, a, static_cast<int64_t>(a.m_tiles) * a.n_tiles, s);
 }
 
-template <typename T> cudaError_t join(void* out, const float* part, int64_t slices, int64_t n, cudaStream_t s) {
-    return launch_pdl(join_kernel<T>, dim3(static_cast<unsigned>(ceil_div(n / kVec, 256))), dim3(256), 0, s,
-                      static_cast<T*>(out), part, static_cast<int>(slices), n / kVec);
+template <typename O>
+cudaError_t join(void* out, void* out2, const float* part, int64_t slices, int64_t n, bool add, cudaStream_t s) {
+    return launch_pdl(join_kernel<O>, dim3(static_cast<unsigned>(ceil_div(n / kVec, 256)), out2 ? 2 : 1), dim3(256), 0, s,
+                      static_cast<O*>(out), static_cast<O*>(out2), part, static_cast<int>(slices), n / kVec, add);
 }
 
 template <typename T>
@@ -624,7 +663,9 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
     a.slice_blocks = static_cast<int>(p.slice_blocks);
     a.x_units = dx ? static_cast<int>(ceil_div(sh.rows, kTileM)) * a.h_tiles : 0;
     a.w_tiles = static_cast<int>(ceil_div(sh.ffn, kTileM)) * a.h_tiles;
-    a.w_units = dwg ? 2 * a.w_tiles : 0;
+    a.w_slice_blocks = static_cast<int>(p.w_slice_blocks);
+    a.w_partial = dwg && p.w_slices > 1;
+    a.w_units = dwg ? static_cast<int>(p.w_slices) * 2 * a.w_tiles : 0;
     a.w_first = p.w_first;
     a.x_partial = p.slices > 1;
     GatedMaps m = {};
@@ -640,24 +681,28 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
     else if (dx)
         LS_CUDA(make_map<T>(&m.out, dx, sh.hidden, sh.rows, sh.hidden, 32));
     // dW's sums over the rows, kMostRows of them at a time: added to FP32 gradients, or to scratch.
-    const bool scratch = dwg && !f32 && sh.rows > kMostRows;
+    const bool scratch = dwg && (a.w_partial || (!f32 && sh.rows > kMostRows));
     const int64_t w_elements = sh.ffn * sh.hidden;
-    float* scratch2 = w_partial + round256(static_cast<size_t>(w_elements) * 4) / 4;
     a.w_f32 = f32 || scratch;
-    if (dwg && a.w_f32) {
-        LS_CUDA(make_map<float>(&m.out2, scratch ? w_partial : dwg, sh.hidden, sh.ffn, sh.hidden, 32));
-        LS_CUDA(make_map<float>(&m.out3, scratch ? scratch2 : dwu, sh.hidden, sh.ffn, sh.hidden, 32));
+    if (scratch) {
+        const int64_t depth = a.w_partial ? p.w_slices : 0;
+        LS_CUDA(make_map<float>(&m.out2, w_partial, sh.hidden, sh.ffn, sh.hidden, 32, depth));
+        LS_CUDA(make_map<float>(&m.out3, w_partial + p.w_slices * w_elements, sh.hidden, sh.ffn, sh.hidden, 32, depth));
+    } else if (dwg && f32) {
+        LS_CUDA(make_map<float>(&m.out2, dwg, sh.hidden, sh.ffn, sh.hidden, 32));
+        LS_CUDA(make_map<float>(&m.out3, dwu, sh.hidden, sh.ffn, sh.hidden, 32));
     } else if (dwg) {
         LS_CUDA(make_map<T>(&m.out2, dwg, sh.hidden, sh.ffn, sh.hidden, 32));
         LS_CUDA(make_map<T>(&m.out3, dwu, sh.hidden, sh.ffn, sh.hidden, 32));
     }
-    a.w_add = f32;
+    a.w_add = f32 && !a.w_partial;
     const int64_t row_blocks = ceil_div(sh.rows, kBlockK), most = kMostRows / kBlockK;
     for (int64_t kb = 0; kb < (dwg ? row_blocks : 1); kb += most) {
         a.w_kb0 = static_cast<int>(kb);
         a.w_k_blocks = static_cast<int>(std::min(most, row_blocks - kb));
         const int64_t x_units = static_cast<int64_t>(a.slices) * a.x_units;
-        const int64_t x_len = a.slice_blocks + 1 + (a.slices > 1), w_len = a.w_k_blocks + 1;
+        if (!a.w_partial) a.w_slice_blocks = a.w_k_blocks;
+        const int64_t x_len = a.slice_blocks + 1 + (a.slices > 1), w_len = a.w_slice_blocks + 1 + (p.w_slices > 1);
         const Deal d(a.w_first ? a.w_units : x_units, a.w_first ? w_len : x_len, a.w_first ? x_units : a.w_units,
                      a.w_first ? x_len : w_len);
         a.pairs1 = static_cast<int>(d.pairs1);
@@ -666,11 +711,11 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
         a.x_units = 0;
         a.w_add = true;
     }
-    if (scratch) {
-        LS_CUDA(join<T>(dwg, w_partial, 1, w_elements, s));
-        LS_CUDA(join<T>(dwu, scratch2, 1, w_elements, s));
-    }
-    if (dx && a.x_partial) LS_CUDA(join<T>(dx, partial, p.slices, sh.rows * sh.hidden, s));
+    if (scratch && f32)
+        LS_CUDA(join<float>(dwg, dwu, w_partial, p.w_slices, w_elements, true, s));
+    else if (scratch)
+        LS_CUDA(join<T>(dwg, dwu, w_partial, p.w_slices, w_elements, false, s));
+    if (dx && a.x_partial) LS_CUDA(join<T>(dx, nullptr, partial, p.slices, sh.rows * sh.hidden, false, s));
     return cudaSuccess;
 }
 

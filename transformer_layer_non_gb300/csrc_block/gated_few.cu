@@ -20,7 +20,7 @@
 namespace ls {
 namespace {
 
-constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
+constexpr int kFewThreads = 128, kFewWarps = kFewThreads / 32;
 constexpr int kFewStep = 32;    // values of K for a warp's load: 8 for each of four lanes of a row
 constexpr int64_t kMostFew = 16;  // rows of x
 
@@ -46,9 +46,10 @@ struct FewArgs {
     int rows, hidden, ffn, act;
 };
 
-// NT: groups of 8 rows of x.  U: a warp's steps in flight.
+// NT: groups of 8 rows of x.  U: a warp's steps in flight; with six CTAs of four warps on an SM (four for NT = 2,
+// whose registers hold more of x) 4 of them, 8 warps or 8 steps are slower (1 x 1280 x 5120: 4.0 us; 5.8 and 4.7).
 template <typename T, int NT, int U>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 6 : 4)
 few_kernel(T* __restrict__ h, const T* __restrict__ x, const T* __restrict__ wg, const T* __restrict__ wu,
            const __grid_constant__ FewArgs a) {
     __shared__ float part[kFewWarps][32][4 * NT + 1];
@@ -110,7 +111,7 @@ template <typename T>
 cudaError_t launch(void* h, const void* x, const void* wg, const void* wu, const GatedShape& sh, cudaStream_t s) {
     const FewArgs a{static_cast<int>(sh.rows), static_cast<int>(sh.hidden), static_cast<int>(sh.ffn),
                     static_cast<int>(sh.act)};
-    return launch_pdl(sh.rows <= 8 ? few_kernel<T, 1, 8> : few_kernel<T, 2, 4>, dim3(static_cast<unsigned>(sh.ffn / 8)),
+    return launch_pdl(sh.rows <= 8 ? few_kernel<T, 1, 4> : few_kernel<T, 2, 4>, dim3(static_cast<unsigned>(sh.ffn / 8)),
                       dim3(kFewThreads), 0, s, static_cast<T*>(h), static_cast<const T*>(x), static_cast<const T*>(wg),
                       static_cast<const T*>(wu), a);
 }
