@@ -7,10 +7,12 @@
 //
 // Many tensors go through one launch: a table of addresses and sizes in the
 // kernel's arguments (no copy, and a graph captures it by value), 48 or 1024
-// tensors of it.  Tensors are cut into chunks of 16384 elements; each of a fixed
-// number of CTAs takes an equal run of the chunks, so that what a CTA adds
-// depends on the sizes alone.  Scaling goes through the same runs backwards: what
-// the norm read last is still in L2.
+// tensors of it.  Tensors are cut into chunks of 32768 elements, dealt to a fixed
+// number of CTAs in turn, so that what a CTA adds depends on the sizes alone, and
+// that the CTAs read neighbouring memory at about the same time (1.0 G BF16
+// gradients, norm and scaling: 897 us, 6.7 TB/s; an equal run of chunks for each
+// CTA 914, chunks of 8192 1035).  Scaling goes through them backwards: what the
+// norm read last is still in L2.
 //
 // Squares of BF16 and FP32 values leave FP32's range at 2^64 and 2^-63.  Each
 // thread adds the squares of its part of a chunk in FP32, and goes through it
@@ -28,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kNormCtas = 912;      // six on each of 152 SMs
-constexpr int kChunk = 16384;       // elements
+constexpr int kChunk = 32768;       // elements
 constexpr int kSlots = 8;           // vectors in flight for each thread, of the norm
 constexpr int kScaleSlots = 4;      // and of scaling (8 of them spill)
 constexpr int kFew = 48, kMany = 1024;  // tensors of a launch
@@ -49,22 +51,17 @@ template <int N> struct Table {
 // The chunks of this CTA, the last of them first if `backwards`.  f(entry index, first element, elements).
 template <int N, typename F>
 __device__ __forceinline__ void for_chunks(const Table<N>& t, bool backwards, F&& f) {
-    const uint32_t begin = static_cast<uint32_t>(static_cast<uint64_t>(t.chunks) * blockIdx.x / gridDim.x);
-    const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
-    if (begin >= end) return;
-    const uint32_t start = backwards ? end - 1 : begin;
-    int lo = 0, hi = t.count - 1;  // the last tensor whose first chunk is not behind `start`
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (t.first[mid] <= start)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    for (uint32_t i = 0; i < end - begin; ++i) {
-        const uint32_t c = backwards ? end - 1 - i : begin + i;
-        while (lo + 1 < t.count && t.first[lo + 1] <= c) ++lo;  // empty tensors have no chunk: the last that fits
-        while (t.first[lo] > c) --lo;
+    const uint32_t n = t.chunks > blockIdx.x ? (t.chunks - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t c = blockIdx.x + (backwards ? n - 1 - i : i) * gridDim.x;
+        int lo = 0, hi = t.count - 1;  // the last tensor whose first chunk is not behind c
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (t.first[mid] <= c)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
         const int64_t e0 = static_cast<int64_t>(c - t.first[lo]) * kChunk;
         f(lo, e0, static_cast<int>(min(static_cast<int64_t>(kChunk), t.e[lo].n - e0)));
     }
@@ -341,9 +338,10 @@ cudaError_t scale_gradients(const ls_tensor* out, const ls_tensor* in, int64_t c
 
 template <typename T>
 cudaError_t adam(void* param, const void* grad, float* m, float* v, const AdamArgs& a, cudaStream_t s) {
-    // a grid that fills the GPU's 152 SMs several times over; each thread strides through the rest
+    // One vector for each thread: the seven streams stay closer together in memory than with a grid that strides
+    // (134 M FP16 parameters with the norm: 477 us, with 1216 CTAs 555).
     const int64_t want = static_cast<int64_t>((a.nv + kThreads - 1) / kThreads);
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(want, 152 * 8));
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(want, 1 << 30));
     return launch_pdl(adam_scaled_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, static_cast<T*>(param),
                       static_cast<const T*>(grad), m, v, a);
 }
