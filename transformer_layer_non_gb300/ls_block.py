@@ -168,37 +168,65 @@ class Rotation:
         self.scale = float(default.value if scale is None else scale)
         # fixed-point numbers of 64 bits, whose upper half int64 shows as negative
         values = [t - (t >> 63 << 64) for t in turns[:self.rotary_dim // 2]]
-        self.turns = torch.tensor(values, dtype=torch.int64, device=device)
+        self._tensor = torch.tensor(values, dtype=torch.int64, device=device)
+        self._turns, self._device = self._tensor.data_ptr(), self._tensor.get_device()
+
+    @property
+    def turns(self):
+        return self._tensor
 
     def _packed(self, positions, first_position, batch, seq, device):
-        if self.turns.get_device() != device:
+        if self._device != device:
             raise ValueError(f"rotation is on {self.turns.device}, the current device is cuda:{device}")
-        at = 0
-        if positions is not None:
-            if tuple(positions.shape) not in ((batch, seq), (batch * seq,)):
-                raise ValueError(f"positions must have the shape {(batch, seq)}, got "
-                                 f"{tuple(positions.shape)}")
-            at = _v._tensor("positions", positions, positions.shape, _v._int32, device)
-        elif not -2 ** 63 <= first_position < 2 ** 63:
-            raise ValueError(f"first_position = {first_position} is not an int64")
-        return _ROTATION.pack(self.turns.data_ptr(), self.rotary_dim, self.interleaved, self.scale, at,
-                              0 if at else first_position)
+        if positions is None:
+            if not -2 ** 63 <= first_position < 2 ** 63:
+                raise ValueError(f"first_position = {first_position} is not an int64")
+            return _ROTATION.pack(self._turns, self.rotary_dim, self.interleaved, self.scale, 0,
+                                  first_position)
+        shape = getattr(positions, "shape", None)
+        if shape is None:
+            raise TypeError(f"positions must be a tensor, got {type(positions).__name__}")
+        if shape != (batch, seq) and shape != (batch * seq,):
+            raise ValueError(f"positions must have the shape {(batch, seq)}, got {tuple(shape)}")
+        return _ROTATION.pack(self._turns, self.rotary_dim, self.interleaved, self.scale,
+                              _v._tensor("positions", positions, shape, _v._int32, device), 0)
 
 
-def _view(name, t, dtype, device, batch, seq, dim):
-    """The packed ls_head_view of t."""
+def _views(device, *named):
+    """The packed ls_head_views of tensors that agree with the first one (None
+    stays None), given as names and tensors in turn; and its sizes."""
+    like = named[1]
     try:
-        if t.dtype is dtype and t.get_device() == device:
+        batch, seq, _, dim = like.shape
+        dtype = like.dtype
+        packed = []
+        for i in range(1, len(named), 2):
+            t = named[i]
+            if t is None and i > 1:
+                packed.append(None)
+                continue
             b, l, heads, d = t.shape
             s = t.stride()
-            if b == batch and l == seq and d == dim and s[3] == 1:
-                return _VIEW.pack(t.data_ptr(), heads, s[0], s[1], s[2])
-    except AttributeError:
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}") from None
-    except ValueError:
-        pass
-    if t.dim() != 4 or (t.shape[0], t.shape[1], t.shape[3]) != (batch, seq, dim):
-        raise ValueError(f"{name} must have the shape ({batch}, {seq}, heads, {dim}), got {tuple(t.shape)}")
+            if (b != batch or l != seq or d != dim or s[3] != 1 or t.dtype is not dtype
+                    or t.get_device() != device):
+                _bad_view(named[i - 1], t, dtype, device, batch, seq, dim)
+            packed.append(_VIEW.pack(t.data_ptr(), heads, s[0], s[1], s[2]))
+    except (AttributeError, ValueError):
+        for name, t in zip(named[::2], named[1::2]):  # the reason
+            if t is None and t is not like:
+                continue
+            if not hasattr(t, "shape"):
+                raise TypeError(f"{name} must be a tensor, got {type(t).__name__}") from None
+            if len(t.shape) != 4:
+                raise ValueError(f"{name} must have 4 dimensions, got {len(t.shape)}") from None
+        raise
+    return packed, batch, seq, dim, dtype
+
+
+def _bad_view(name, t, dtype, device, batch, seq, dim):
+    shape = tuple(t.shape)
+    if (shape[0], shape[1], shape[3]) != (batch, seq, dim):
+        raise ValueError(f"{name} must have the shape ({batch}, {seq}, heads, {dim}), got {shape}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
@@ -208,31 +236,13 @@ def _view(name, t, dtype, device, batch, seq, dim):
     raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
-def _sizes(name, t):
-    try:
-        batch, seq, _, dim = t.shape
-    except AttributeError:
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}") from None
-    except ValueError:
-        raise ValueError(f"{name} must have 4 dimensions, got {t.dim()}") from None
-    return batch, seq, dim, t.dtype
-
-
-def _pair(names, tensors, dtype, device, batch, seq, dim):
-    """The packed views of a call's two tensors; the second may be None."""
-    return (_view(names[0], tensors[0], dtype, device, batch, seq, dim),
-            None if tensors[1] is None else _view(names[1], tensors[1], dtype, device, batch, seq, dim))
-
-
 def ls_rotary_fwd(q_out, k_out, q, k, rotation: Rotation, positions=None, first_position: int = 0,
                   stream=None):
     """Rotated queries and keys (k and k_out may be None); an output may be its
     input.  positions: int32 [batch, seq], or None for first_position onwards."""
     dev = _v._device()
-    batch, seq, dim, dtype = _sizes("q", q)
-    x = _pair(("q", "k"), (q, k), dtype, dev, batch, seq, dim)
-    y = _pair(("q_out", "k_out"), (q_out, k_out), dtype, dev, batch, seq, dim)
-    _check(load().ls_rotary_fwd(_v._storage_code(q), y[0], y[1], x[0], x[1], batch, seq, dim,
+    p, batch, seq, dim, _ = _views(dev, "q", q, "k", k, "q_out", q_out, "k_out", k_out)
+    _check(load().ls_rotary_fwd(_v._storage_code(q), p[2], p[3], p[0], p[1], batch, seq, dim,
                                 rotation._packed(positions, first_position, batch, seq, dev),
                                 _v._stream_of(stream, dev)))
 
@@ -242,10 +252,8 @@ def ls_rotary_bwd(dq, dk, dq_out, dk_out, rotation: Rotation, positions=None, fi
     """Gradients of queries and keys from those of the rotated ones (dk and
     dk_out may be None); dq may be dq_out."""
     dev = _v._device()
-    batch, seq, dim, dtype = _sizes("dq_out", dq_out)
-    x = _pair(("dq_out", "dk_out"), (dq_out, dk_out), dtype, dev, batch, seq, dim)
-    y = _pair(("dq", "dk"), (dq, dk), dtype, dev, batch, seq, dim)
-    _check(load().ls_rotary_bwd(_v._storage_code(dq_out), y[0], y[1], x[0], x[1], batch, seq, dim,
+    p, batch, seq, dim, _ = _views(dev, "dq_out", dq_out, "dk_out", dk_out, "dq", dq, "dk", dk)
+    _check(load().ls_rotary_bwd(_v._storage_code(dq_out), p[2], p[3], p[0], p[1], batch, seq, dim,
                                 rotation._packed(positions, first_position, batch, seq, dev),
                                 _v._stream_of(stream, dev)))
 
@@ -255,12 +263,11 @@ def ls_qk_norm_rotary_fwd(q_out, k_out, q, k, q_weight, k_weight, rotation: Rota
     """Queries and keys normalised head by head, weighted ([head_dim] or None
     for ones) and rotated (rotation None: not)."""
     dev = _v._device()
-    batch, seq, dim, dtype = _sizes("q", q)
-    x = _pair(("q", "k"), (q, k), dtype, dev, batch, seq, dim)
-    y = _pair(("q_out", "k_out"), (q_out, k_out), dtype, dev, batch, seq, dim)
+    p, batch, seq, dim, dtype = _views(dev, "q", q, "k", k, "q_out", q_out, "k_out", k_out)
     rot = None if rotation is None else rotation._packed(positions, first_position, batch, seq, dev)
     _check(load().ls_qk_norm_rotary_fwd(
-        _v._storage_code(q), y[0], y[1], x[0], x[1], _v._optional("q_weight", q_weight, (dim,), dtype, dev),
+        _v._storage_code(q), p[2], p[3], p[0], p[1],
+        _v._optional("q_weight", q_weight, (dim,), dtype, dev),
         _v._optional("k_weight", k_weight, (dim,), dtype, dev), eps, batch, seq, dim, rot,
         _v._stream_of(stream, dev)))
 
@@ -271,16 +278,14 @@ def ls_qk_norm_rotary_bwd(dq, dk, dq_weight, dk_weight, dq_out, dk_out, q, k, q_
     """Gradients of queries, keys and their weights (None: not wanted) from the
     forward's inputs and the gradients of its outputs; dq may be dq_out or q."""
     dev = _v._device()
-    batch, seq, dim, dtype = _sizes("q", q)
-    x = _pair(("q", "k"), (q, k), dtype, dev, batch, seq, dim)
-    g = _pair(("dq_out", "dk_out"), (dq_out, dk_out), dtype, dev, batch, seq, dim)
-    y = _pair(("dq", "dk"), (dq, dk), dtype, dev, batch, seq, dim)
+    p, batch, seq, dim, dtype = _views(dev, "q", q, "k", k, "dq_out", dq_out, "dk_out", dk_out, "dq", dq,
+                                       "dk", dk)
     rot = None if rotation is None else rotation._packed(positions, first_position, batch, seq, dev)
     ws, ws_bytes = _v._workspace(workspace, dev)
     w = [_v._optional(name, t, (dim,), dtype, dev) for name, t in
          (("dq_weight", dq_weight), ("dk_weight", dk_weight), ("q_weight", q_weight), ("k_weight", k_weight))]
     _check(load().ls_qk_norm_rotary_bwd(
-        _v._storage_code(q), y[0], y[1], w[0], w[1], g[0], g[1], x[0], x[1], w[2], w[3], eps, batch, seq, dim,
+        _v._storage_code(q), p[4], p[5], w[0], w[1], p[2], p[3], p[0], p[1], w[2], w[3], eps, batch, seq, dim,
         rot, ws, ws_bytes, _v._stream_of(stream, dev)))
 
 

@@ -80,6 +80,7 @@ class LinkedParameters:
             self.grad_norm, self._factor = (self.exp_avg.new_empty(1) for _ in range(2))
             self._norm_ws = ls_block.new_workspace(ls_block.grad_norm_workspace_bytes(),
                                                    self.grad_ws.device)
+        if self._grad_list is None or self._grad_list.tensors[0] is not self.grad_ws:
             self._grad_list = ls_block.TensorList([self.grad_ws])
         ls_block.ls_grad_norm(self.grad_norm, self._factor, self._grad_list, max_norm, grad_scale,
                               workspace=self._norm_ws, stream=stream)
