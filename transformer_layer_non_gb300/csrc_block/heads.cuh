@@ -9,25 +9,26 @@
 // operations an element.  What else could cost is the angles.  An angle is
 // turns * position in 64-bit fixed point, a full circle being 2^64, so the
 // reduction to one turn is the multiplication's overflow and exact at any
-// position; sincospif gets at most an eighth of a turn.  A warp takes a few tokens
-// with all their heads (or, of few tokens, some of them), works out its tokens'
-// cosines and sines once, while its first rows are on their way, and each lane
-// keeps those of its token in registers while it goes through the heads.  Warps
-// share nothing until the end, so none waits for another.
+// position; the polynomials get at most an eighth of a turn.  A warp takes a few
+// tokens with all their heads (or, of few tokens, some of them), works out its
+// tokens' cosines and sines once, while its first rows are on their way, and goes
+// through the rows.  Warps share nothing until the end, so none waits for another.
 //
-// A group of LPR lanes holds a row, each lane two 16-byte vectors (of 16-bit
-// elements) that contain both members of its pairs: vectors (s, s + r/16) of the
-// half layout, any two of the interleaved one, so that the rotation needs no
-// exchange.  Rotary dimensions whose halves are no multiple of a vector (a
-// quarter of a head of 80, say) take the narrow layout: a warp for a row, single
-// elements.
+// A group of LPR lanes holds a row, each lane 8 pairs of its elements, so that the
+// rotation needs no exchange.  Interleaved: any two vectors of 8 elements.  Halves:
+// as many chunks of W elements of the first half as of the second, W being what
+// divides the half, 8 or fewer: chunk n and chunk n + half / W.  What is not rotated
+// is paired the same way.
 //
 // The weights' gradients are summed per lane over the warp's rows, then over the
 // CTA's groups, then over the CTAs by a second launch, each in a fixed order; the
 // number of CTAs depends on the shapes alone.
 #pragma once
 
+#include <string.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "../csrc_vocab/vec.cuh"
 #include "block_internal.h"
@@ -38,7 +39,8 @@ namespace {
 constexpr int kHeadsThreads = 128;
 constexpr int kHeadsWarps = kHeadsThreads / 32;
 
-enum HeadsLayout { kHalf = 0, kInterleaved = 1, kNarrow = 2 };
+// A layout is the chunks' width of halves, 8 (16-bit storage), 4, 2 or 1, or
+constexpr int kInterleaved = 0;
 enum HeadsMode { kRotate = 0, kNormFwd = 1, kNormBwd = 2 };
 
 struct HeadsView {
@@ -50,16 +52,16 @@ struct HeadsArgs {
     HeadsView x[2], g[2], y[2];
     const void* w[2];
     int heads[2];
-    int tok_shift[2];    // log2 of a unit's tokens
+    int tok_shift[2];    // log2 of a unit's tokens that are side by side
+    int sub_shift[2];    // and of those that a group goes through one after the other
     int split_shift[2];  // log2 of the units that share a token's heads
-    int units[2];        // of a warp
-    int iters[2];        // heads that a group goes through
+    uint32_t units[2];   // of a warp
+    int iters[2];        // heads of a token that a group goes through
     int ctas0;           // CTAs of the first tensor; the others have the second
     int tokens;
     FastDiv by_seq;
-    int dim, vecs, pairs;    // head_dim, its vectors, rotary_dim / 2
+    int dim, pairs;          // head_dim, rotary_dim / 2
     FastDiv by_pairs;
-    bool interleaved;        // for the narrow layout
     bool skip_rest[2];       // in place without the norm: elements behind rotary_dim stay untouched
     const uint64_t* turns;
     const int32_t* positions;
@@ -73,94 +75,146 @@ struct HeadsArgs {
 __device__ __forceinline__ void turn_sincos(uint64_t frac, float& s, float& c) {
     const uint32_t q = static_cast<uint32_t>((frac + (uint64_t{1} << 61)) >> 62);  // the nearest quarter
     const int64_t r = static_cast<int64_t>(frac - (static_cast<uint64_t>(q) << 62));
-    // |r| <= 2^61, an eighth of a turn; its upper half, in units of half a turn
-    float sr, cr;
-    sincospif(static_cast<float>(static_cast<int32_t>(r >> 32)) * 0x1p-31f, &sr, &cr);
+    // |r| <= 2^61, an eighth of a turn; its upper half, in radians, and Taylor's series, whose next terms are below
+    // 2e-9 and 1e-10
+    const float x = static_cast<float>(static_cast<int32_t>(r >> 32)) * 1.4629180792671596e-9f, z = x * x;
+    const float sr = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+    const float cr = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
     s = q & 1 ? cr : sr;
     c = q & 1 ? sr : cr;
     if (q & 2) s = -s;
     if ((q + 1) & 2) c = -c;
 }
 
-// What a lane holds of a row: the places of its 8 pairs.  The lanes' first vectors lie side by side, and so do
-// their second ones: a group's access covers whole sectors of memory.
-template <int LAYOUT> struct LanePlace {
-    int a, b;        // wide: first elements of its two vectors, -1 if there is none; narrow: the lane
-    uint32_t rot;    // bit j: pair j is rotated
+// W elements of the storage type, as they lie in memory.
+template <typename T, int W> struct Chunk {
+    using Word = std::conditional_t<W * sizeof(T) == 2, uint16_t, uint32_t>;
+    static constexpr int kWords = W * sizeof(T) / sizeof(Word);
+    Word w[kWords];
 };
-
-template <int LAYOUT> __device__ __forceinline__ LanePlace<LAYOUT> lane_place(int s, const HeadsArgs& a) {
-    LanePlace<LAYOUT> l;
-    if constexpr (LAYOUT == kHalf) {
-        const int hv = a.pairs / kVec;  // vectors of half of the rotated part
-        const int rest = a.vecs - 2 * hv, v = s < hv ? s : s + hv, v2 = s < hv ? s + hv : v + (rest + 1) / 2;
-        l.a = s < hv || s - hv < (rest + 1) / 2 ? v * kVec : -1;
-        l.b = l.a >= 0 && v2 < a.vecs ? v2 * kVec : -1;
-        l.rot = s < hv ? 0xffu : 0u;
-    } else if constexpr (LAYOUT == kInterleaved) {
-        const int v = s, v2 = s + (a.vecs + 1) / 2;
-        l.a = v < (a.vecs + 1) / 2 ? v * kVec : -1;
-        l.b = l.a >= 0 && v2 < a.vecs ? v2 * kVec : -1;
-        l.rot = (l.a >= 0 && v * (kVec / 2) < a.pairs ? 0x0fu : 0u) | (l.b >= 0 && v2 * (kVec / 2) < a.pairs ? 0xf0u : 0u);
-    } else {
-        l.a = l.b = s;
-        l.rot = 0;
+template <typename T, int W> __device__ __forceinline__ Chunk<T, W> load_chunk(const T* p) {
+    Chunk<T, W> c;
+    if constexpr (W * sizeof(T) >= 16) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (s + 32 * j < a.pairs) l.rot |= 1u << j;
+        for (int i = 0; i < c.kWords; i += 4) {
+            const uint4 v = ld16(reinterpret_cast<const uint32_t*>(p) + i);
+            c.w[i] = v.x, c.w[i + 1] = v.y, c.w[i + 2] = v.z, c.w[i + 3] = v.w;
+        }
+    } else if constexpr (W * sizeof(T) == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        c.w[0] = v.x, c.w[1] = v.y;
+    } else {
+        c.w[0] = *reinterpret_cast<const typename Chunk<T, W>::Word*>(p);
     }
-    return l;
+    return c;
 }
-
-// Narrow: the elements of pair number p (of dim / 2), the rotated ones first.
-__device__ __forceinline__ int2 narrow_pair(int p, const HeadsArgs& a) {
-    if (p >= a.pairs || a.interleaved) return make_int2(2 * p, 2 * p + 1);
-    return make_int2(p, p + a.pairs);
+template <typename T, int W> __device__ __forceinline__ void store_chunk(T* p, const Chunk<T, W>& c) {
+    if constexpr (W * sizeof(T) >= 16) {
+#pragma unroll
+        for (int i = 0; i < c.kWords; i += 4)
+            st16(reinterpret_cast<uint32_t*>(p) + i, make_uint4(c.w[i], c.w[i + 1], c.w[i + 2], c.w[i + 3]));
+    } else if constexpr (W * sizeof(T) == 8) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(c.w[0], c.w[1]);
+    } else {
+        *reinterpret_cast<typename Chunk<T, W>::Word*>(p) = c.w[0];
+    }
 }
-
-template <typename T, int LAYOUT> struct RowRaw {
-    Raw8<T> a, b;
-};
-template <typename T> struct RowRaw<T, kNarrow> {
-    float a[kVec], b[kVec];
-};
-
-// A lane's part of the row at p; zeros for what does not exist.
-template <typename T, int LAYOUT>
-__device__ __forceinline__ void load_row(RowRaw<T, LAYOUT>& r, const T* p, bool on, const LanePlace<LAYOUT>& l,
-                                         const HeadsArgs& a) {
-    if constexpr (LAYOUT != kNarrow) {
-        r.a = on && l.a >= 0 ? load8<T>(p + l.a) : zero8<T>();
-        r.b = on && l.b >= 0 ? load8<T>(p + l.b) : zero8<T>();
+// Into f[k .. k + W), and back.
+template <typename T, int W> __device__ __forceinline__ void unpack_chunk(const Chunk<T, W>& c, float (&f)[kVec], int k) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) f[k + i] = __uint_as_float(c.w[i]);
+    } else if constexpr (W == 1) {
+        T v;
+        memcpy(&v, &c.w[0], 2);
+        f[k] = to_f32(v);
     } else {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const int n = l.a + 32 * j;
-            const bool there = on && 2 * n < a.dim;
-            const int2 e = narrow_pair(n, a);
-            r.a[j] = there ? to_f32(p[e.x]) : 0.f;
-            r.b[j] = there ? to_f32(p[e.y]) : 0.f;
+        for (int i = 0; i < W / 2; ++i) {
+            const float2 t = std::is_same<T, bf16>::value ? b2f(c.w[i]) : h2f(c.w[i]);
+            f[k + 2 * i] = t.x, f[k + 2 * i + 1] = t.y;
         }
     }
 }
+template <typename T, int W> __device__ __forceinline__ Chunk<T, W> pack_chunk(const float (&f)[kVec], int k) {
+    Chunk<T, W> c;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) c.w[i] = __float_as_uint(f[k + i]);
+    } else if constexpr (W == 1) {
+        const T v = from_f32<T>(f[k]);
+        memcpy(&c.w[0], &v, 2);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) c.w[i] = pack2<T>(f[k + 2 * i], f[k + 2 * i + 1]);
+    }
+    return c;
+}
+
+// Where a lane's 8 pairs are: J chunks of W elements with the first members and J with the second ones (halves), or
+// 2 J vectors of neighbours (interleaved).  The lanes' chunks j lie side by side: a group's access covers whole sectors
+// of memory.
+template <typename T, int LAYOUT> constexpr int chunk_width() { return LAYOUT == kInterleaved ? 16 / sizeof(T) : LAYOUT; }
+template <typename T, int LAYOUT, int LPR> struct LanePlace {
+    static constexpr int W = chunk_width<T, LAYOUT>(), J = kVec / W;
+    int lane, all;   // chunks of a row
+    int turned;      // halves: chunk pairs that are rotated
+    int apart;       // halves: the chunks from a pair that is not rotated to its second one
+    uint32_t rot;    // bit k: pair k is rotated
+
+    __device__ __forceinline__ LanePlace(int s, const HeadsArgs& a) : lane(s), all(a.dim / W), turned(0), apart(0), rot(0) {
+        if constexpr (LAYOUT == kInterleaved) {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                const int n = s + LPR * (k / (W / 2));
+                if (n < all && n * (W / 2) + k % (W / 2) < a.pairs) rot |= 1u << k;
+            }
+        } else {
+            turned = a.pairs / W;
+            apart = (all - 2 * turned + 1) / 2;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (s + LPR * j < turned) rot |= ((1u << W) - 1) << (j * W);
+        }
+    }
+    // The elements where its chunks j begin, and whether they exist.
+    __device__ __forceinline__ int first(int j, bool& there) const {
+        const int n = lane + LPR * j;
+        there = n < (LAYOUT == kInterleaved ? all : turned + apart);
+        return (LAYOUT == kInterleaved || n < turned ? n : n + turned) * W;
+    }
+    __device__ __forceinline__ int second(int j, bool& there) const {
+        const int n = lane + LPR * j;
+        const int c = LAYOUT == kInterleaved ? n + LPR * J : n < turned ? n + turned : n + turned + apart;
+        there = c < all && (LAYOUT == kInterleaved || n < turned + apart);
+        return c * W;
+    }
+    // Which of the W elements of a first chunk j (with `later` a second one) are rotated: a bit for each, or for each
+    // two (interleaved).
+    static constexpr uint32_t kWhole = (1u << (LAYOUT == kInterleaved ? W / 2 : W)) - 1;
+    __device__ __forceinline__ uint32_t rotated(int j, bool later) const {
+        return rot >> (LAYOUT == kInterleaved ? (j + (later ? J : 0)) * (W / 2) : j * W) & kWhole;
+    }
+};
+
 // Its 8 pairs in FP32: the first members, and the second ones.  Two neighbours share a float2, so that the
 // arithmetic takes one instruction for both.
 constexpr int kHalfVec = kVec / 2;
 struct Pairs {
     float2 x[kHalfVec], y[kHalfVec];
 };
+// A lane's chunks, in order: the first members' and the second ones'.
+template <typename T, int LAYOUT> struct RowRaw {
+    static constexpr int W = chunk_width<T, LAYOUT>(), J = kVec / W;
+    Chunk<T, W> a[J], b[J];
+};
 template <typename T, int LAYOUT> __device__ __forceinline__ Pairs pairs_of(const RowRaw<T, LAYOUT>& r) {
     Pairs p;
     float u[kVec], v[kVec];
-    if constexpr (LAYOUT == kNarrow) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            u[j] = r.a[j];
-            v[j] = r.b[j];
-        }
-    } else {
-        unpack(r.a, u);
-        unpack(r.b, v);
+    for (int j = 0; j < r.J; ++j) {
+        unpack_chunk(r.a[j], u, j * r.W);
+        unpack_chunk(r.b[j], v, j * r.W);
     }
 #pragma unroll
     for (int j = 0; j < kHalfVec; ++j) {
@@ -176,8 +230,8 @@ template <typename T, int LAYOUT> __device__ __forceinline__ Pairs pairs_of(cons
     }
     return p;
 }
-// Back to the lane's two vectors, in the row's order (narrow: first and second members).
-template <int LAYOUT> __device__ __forceinline__ void vectors_of(const Pairs& p, float (&u)[kVec], float (&v)[kVec]) {
+// Back to the lane's chunks, one after the other.
+template <int LAYOUT> __device__ __forceinline__ void chunks_of(const Pairs& p, float (&u)[kVec], float (&v)[kVec]) {
 #pragma unroll
     for (int j = 0; j < kHalfVec; ++j) {
         if constexpr (LAYOUT == kInterleaved) {
@@ -195,71 +249,176 @@ template <int LAYOUT> __device__ __forceinline__ void vectors_of(const Pairs& p,
         }
     }
 }
-template <typename T, int LAYOUT>
-__device__ __forceinline__ void store_row(T* p, const Pairs& r, bool skip_rest, const LanePlace<LAYOUT>& l,
-                                          const HeadsArgs& a) {
-    float u[kVec], v[kVec];
-    vectors_of<LAYOUT>(r, u, v);
-    if constexpr (LAYOUT == kNarrow) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const int n = l.a + 32 * j;
-            if (2 * n >= a.dim || (skip_rest && n >= a.pairs)) continue;
-            const int2 e = narrow_pair(n, a);
-            p[e.x] = from_f32<T>(u[j]);
-            p[e.y] = from_f32<T>(v[j]);
-        }
-    } else {
-        // in place without the norm, vectors that hold nothing rotated are left
-        const uint32_t first = LAYOUT == kHalf ? 0xffu : 0x0fu, second = LAYOUT == kHalf ? 0xffu : 0xf0u;
-        if (l.a >= 0 && !(skip_rest && !(l.rot & first))) store8f<T>(p + l.a, u);
-        if (l.b >= 0 && !(skip_rest && !(l.rot & second))) store8f<T>(p + l.b, v);
-    }
+
+// 16 bytes from memory to shared memory, without registers.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// At most N of this thread's groups of copies are still under way.
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The ring that a warp's rows come through: slots of a row for each group, in memory's vectors of 16 bytes.  Where
+// chunks are such vectors (kOwn) each lane copies, reads and stores its own ones, and no lane waits for another;
+// narrower chunks are read from, and put back into, the row as it lies in memory.
+template <typename T, int LAYOUT, int LPR> struct Ring {
+    using Place = LanePlace<T, LAYOUT, LPR>;
+    static constexpr int W = Place::W, J = Place::J;
+    static constexpr bool kOwn = W * sizeof(T) == 16;
+    static constexpr int kVecs = sizeof(T);            // vectors of a lane: 16 elements
+    static constexpr int kElems = 16 / sizeof(T);      // elements of a vector
+    // 16 bytes more for a row that lanes read across, so that not all of a warp's rows begin in the same bank.
+    static constexpr uint32_t kRowBytes = LPR * kVecs * 16 + (kOwn ? 0 : 16);
+    static constexpr uint32_t kSlotBytes = 32 / LPR * kRowBytes;
+
+    // The elements where a lane's vector i begins, whether it exists, and where it is in a slot.
+    static __device__ __forceinline__ int element(const Place& l, int i, bool& there) {
+        if constexpr (kOwn) {
+            return i < J ? l.first(i, there) : l.second(i - J, there);
+        } else {
+            const int v = l.lane + LPR * i;
+            there = v < l.all * W / kElems;
+            return v * kElems;
+        }
+    }
+    static __device__ __forceinline__ uint32_t place(const Place& l, int i) {
+        const uint32_t in_warp = threadIdx.x % 32;
+        if constexpr (kOwn) return (i * 32 + in_warp) * 16;
+        return in_warp / LPR * kRowBytes + (l.lane + LPR * i) * 16;
+    }
+    static __device__ __forceinline__ T* row(unsigned char* slot) {
+        return reinterpret_cast<T*>(slot + threadIdx.x % 32 / LPR * kRowBytes);
+    }
+    // Zeros for vectors that do not exist: they are never copied over.
+    static __device__ __forceinline__ void clear(unsigned char* slot, const Place& l) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            bool there;
+            element(l, i, there);
+            if (!there) st16(slot + place(l, i), make_uint4(0, 0, 0, 0));
+        }
+    }
+    static __device__ __forceinline__ void load(unsigned char* slot, const T* p, const Place& l) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            bool there;
+            const int e = element(l, i, there);
+            if (there) copy16(smem_u32(slot + place(l, i)), p + e);
+        }
+    }
+    // A lane's chunks of the row in the slot; zeros for those that do not exist.
+    static __device__ __forceinline__ RowRaw<T, LAYOUT> read(unsigned char* slot, const Place& l) {
+        RowRaw<T, LAYOUT> r;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if constexpr (kOwn) {
+                r.a[j] = load_chunk<T, W>(reinterpret_cast<const T*>(slot + place(l, j)));
+                r.b[j] = load_chunk<T, W>(reinterpret_cast<const T*>(slot + place(l, J + j)));
+            } else {
+                bool ta, tb;
+                const int a = l.first(j, ta), b = l.second(j, tb);
+                r.a[j] = ta ? load_chunk<T, W>(row(slot) + a) : Chunk<T, W>{};
+                r.b[j] = tb ? load_chunk<T, W>(row(slot) + b) : Chunk<T, W>{};
+            }
+        }
+        return r;
+    }
+    // From registers to memory.  keep: what is not rotated is stored as it was read (raw); skip: it is not stored.
+    static __device__ __forceinline__ void store(unsigned char* slot, T* p, const Pairs& r, const RowRaw<T, LAYOUT>& raw,
+                                                 bool there, bool keep, bool skip, int rotated, const Place& l) {
+        float u[kVec], v[kVec];
+        chunks_of<LAYOUT>(r, u, v);
+        if constexpr (kOwn) {
+            if (!there) return;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                bool is;
+                const int e = element(l, i, is), j = i % J;
+                const float(&f)[kVec] = i < J ? u : v;
+                const uint32_t bits = l.rotated(j, i >= J);
+                Chunk<T, W> c = pack_chunk<T, W>(f, j * W);
+                if (keep && sizeof(T) == 2 && bits != Place::kWhole) {
+#pragma unroll
+                    for (int k = 0; k < c.kWords; ++k)  // two neighbours; of halves, all or nothing
+                        if (!(bits >> k & 1u)) c.w[k] = (i < J ? raw.a[j] : raw.b[j]).w[k];
+                }
+                if (!is) continue;
+                if (!skip || bits == Place::kWhole) {
+                    store_chunk<T, W>(p + e, c);
+                } else if (LAYOUT == kInterleaved) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        if (bits >> k / 2 & 1u) p[e + k] = from_f32<T>(f[j * W + k]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                bool ta, tb;
+                const int a = l.first(j, ta), b = l.second(j, tb);
+                if (keep && !l.rotated(j, false)) continue;
+                if (ta) store_chunk<T, W>(row(slot) + a, pack_chunk<T, W>(u, j * W));
+                if (tb) store_chunk<T, W>(row(slot) + b, pack_chunk<T, W>(v, j * W));
+            }
+            __syncwarp();
+            if (there) {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    bool is;
+                    const int e = element(l, i, is);
+                    if (!is || (skip && e >= rotated)) continue;
+                    if (!skip || e + kElems <= rotated)
+                        st16(p + e, ld16(row(slot) + e));
+                    else
+                        for (int k = e; k < rotated; ++k) p[k] = row(slot)[k];
+                }
+            }
+            __syncwarp();  // the slot is free
+        }
+    }
+};
 
 // Where the cosine of pair f of a warp's token k stands in its table, its sine two floats on: a float4 holds the
-// cosines and the sines of two neighbours of a lane, those of the lanes side by side.
-template <int LAYOUT, int LPR> __device__ __forceinline__ int table_place(int k, int f, const HeadsArgs& a) {
-    int lane, j;
-    if constexpr (LAYOUT == kHalf) {
-        lane = f / kVec, j = f % kVec;
-    } else if constexpr (LAYOUT == kInterleaved) {
-        const int v = f / (kVec / 2), first = (a.vecs + 1) / 2;
-        lane = v < first ? v : v - first;
-        j = f % (kVec / 2) + (v < first ? 0 : kVec / 2);
-    } else {
-        lane = f % 32, j = f / 32;
-    }
-    return ((k * kHalfVec + j / 2) * LPR + lane) * 4 + (j & 1);
+// cosines and the sines of two neighbours of a lane, those of the lanes and tokens side by side.
+template <typename T, int LAYOUT, int LPR> __device__ __forceinline__ int table_place(int k, int f, int unit_shift) {
+    constexpr int W = LAYOUT == kInterleaved ? chunk_width<T, LAYOUT>() / 2 : chunk_width<T, LAYOUT>();
+    const int n = f / W, j = n / LPR * W + f % W;
+    return (((j / 2 << unit_shift) + k) * LPR + n % LPR) * 4 + (j & 1);
 }
 
-// Rows in flight for each lane, with 16 warps on an SM.  The backward has two inputs and the weights' sums in its
-// registers: two rows for each lane spill, and more warps with fewer registers are slower too (8199 x 40 x 128
-// BF16, both directions: 88 us; two rows 91, five CTAs on an SM 86, but 30 instead of 20 at 4096 x 24 x 64 FP16).
-template <typename T, int LAYOUT, int MODE> constexpr int heads_unroll() {
-    return LAYOUT == kNarrow || MODE == kNormBwd ? 1 : sizeof(T) == 2 ? 4 : 2;
-}
+// Slots of a warp's ring: 128 bytes for each lane, and two rows at least.
+template <typename T, int MODE> constexpr int ring_slots() { return sizeof(T) == 2 && MODE != kNormBwd ? 4 : 2; }
 constexpr int kHeadsCtas = 4;  // on an SM
+// Tokens that a group goes through, of a unit.
+constexpr int kMostSub = 2;  // log2
 
 template <typename T, int LAYOUT, int LPR, int MODE>
 __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const __grid_constant__ HeadsArgs a) {
     constexpr int G = kHeadsThreads / LPR, GW = 32 / LPR;  // groups of a CTA, of a warp
-    constexpr int U = heads_unroll<T, LAYOUT, MODE>();
+    constexpr int D = ring_slots<T, MODE>();
     constexpr bool kCsRegs = MODE == kRotate;  // cosines and sines in registers
-    constexpr int kTable = 32 * kVec;  // GW tokens of LPR * 8 pairs, at the most
-    __shared__ __align__(16) float tables[kHeadsWarps * 2 * kTable];
+    using R = Ring<T, LAYOUT, LPR>;
+    constexpr uint32_t kRow = R::kSlotBytes * (MODE == kNormBwd ? 2 : 1);  // x, and the gradient behind it
+    // For each warp its ring; behind them its table of cosines and sines.
+    extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x % LPR, warp = threadIdx.x / 32, in_warp = threadIdx.x % 32, group = in_warp / LPR;
-    float* const table = tables + warp * 2 * kTable;
+    unsigned char* const ring = smem + warp * D * kRow;
     const int which = blockIdx.x >= a.ctas0;
-    const int cta = blockIdx.x - (which ? a.ctas0 : 0), ctas = which ? gridDim.x - a.ctas0 : a.ctas0;
+    const uint32_t cta = blockIdx.x - (which ? a.ctas0 : 0), ctas = which ? gridDim.x - a.ctas0 : a.ctas0;
     const HeadsView vx = a.x[which], vg = a.g[which], vy = a.y[which];
     const T* x = static_cast<const T*>(vx.p);
     const T* gy = static_cast<const T*>(vg.p);
     T* y = static_cast<T*>(const_cast<void*>(vy.p));
-    const int shift = a.tok_shift[which], split = a.split_shift[which], heads = a.heads[which], iters = a.iters[which];
+    const int shift = a.tok_shift[which], unit_shift = shift + a.sub_shift[which];
+    const int turn_shift = unit_shift + __popc(LPR - 1);
+    const int split = a.split_shift[which], heads = a.heads[which], iters = a.iters[which];
     const int side = GW >> shift, head_step = side << split, my_token = group & ((1 << shift) - 1);
     const bool skip_rest = a.skip_rest[which];
-    const LanePlace<LAYOUT> place = lane_place<LAYOUT>(lane, a);
+    const LanePlace<T, LAYOUT, LPR> place(lane, a);
+    float* const table = reinterpret_cast<float*>(smem + kHeadsWarps * D * kRow) + (warp << unit_shift) * (LPR * 2 * kVec);
+    if constexpr (R::kOwn)
+#pragma unroll
+        for (uint32_t at = 0; at < D * kRow; at += R::kSlotBytes) R::clear(ring + at, place);
     pdl_enter();
 
     Pairs sum = {};  // of the weights' gradients
@@ -269,7 +428,13 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const 
         Pairs w;
         if (pw) {
             RowRaw<T, LAYOUT> r;
-            load_row<T, LAYOUT>(r, pw, true, place, a);
+#pragma unroll
+            for (int j = 0; j < r.J; ++j) {
+                bool ta, tb;
+                const int ea = place.first(j, ta), eb = place.second(j, tb);
+                r.a[j] = ta ? load_chunk<T, r.W>(pw + ea) : Chunk<T, r.W>{};
+                r.b[j] = tb ? load_chunk<T, r.W>(pw + eb) : Chunk<T, r.W>{};
+            }
             w = pairs_of<T, LAYOUT>(r);
         } else {
 #pragma unroll
@@ -281,47 +446,79 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const 
         __syncthreads();
     }
 
-    for (int unit = cta * kHeadsWarps + warp; unit < a.units[which]; unit += ctas * kHeadsWarps) {
-        const int t0 = (unit >> split) << shift, t = t0 + my_token;
-        const int head0 = (group >> shift) + side * (unit & ((1 << split) - 1));
-        const bool on = t < a.tokens;
-        const int64_t b = fdiv(on ? t : 0, a.by_seq), l = fmod_(on ? t : 0, a.by_seq);
-        const T* px = x + b * vx.bs + l * vx.ss;
-        const T* pg = gy + b * vg.bs + l * vg.ss;
-        T* py = y + b * vy.bs + l * vy.ss;
-        // Rows on their way, each loaded into the place of the one that has just been used.
-        RowRaw<T, LAYOUT> rx[U], rg[MODE == kNormBwd ? U : 1];
-        auto load = [&](int u, int i) {
-            const int h = head0 + i * head_step;
-            const bool there = on && h < heads;
-            load_row<T, LAYOUT>(rx[u], px + h * vx.hs, there, place, a);
-            if constexpr (MODE == kNormBwd) load_row<T, LAYOUT>(rg[u], pg + h * vg.hs, there, place, a);
+    for (uint32_t unit = cta * kHeadsWarps + warp; unit < a.units[which]; unit += ctas * kHeadsWarps) {
+        const int t0 = static_cast<int>(unit >> split) << unit_shift;
+        const int head0 = (group >> shift) + side * static_cast<int>(unit & ((1u << split) - 1));
+        // The rows of a group: heads head0, head0 + head_step, .. of token t0 + my_token, then of the one 2^shift
+        // further on.  Two places in them: of the row to be loaded next, and of the one to be stored next.
+        const T *px, *pg;
+        T* py;
+        int load_t = t0 + my_token, load_head = head0, to_load = iters << a.sub_shift[which];
+        int t = load_t, head = head0, to_store = to_load, load_i = iters, store_i = iters;
+        bool load_on, on;
+        auto open_load = [&] {
+            load_on = load_t < a.tokens;
+            const int64_t b = fdiv(load_on ? load_t : 0, a.by_seq), l = fmod_(load_on ? load_t : 0, a.by_seq);
+            px = x + (b * vx.bs + l * vx.ss + head0 * vx.hs);
+            if constexpr (MODE == kNormBwd) pg = gy + (b * vg.bs + l * vg.ss + head0 * vg.hs);
         };
+        auto open_store = [&] {
+            on = t < a.tokens;
+            const int64_t b = fdiv(on ? t : 0, a.by_seq), l = fmod_(on ? t : 0, a.by_seq);
+            py = y + (b * vy.bs + l * vy.ss + head0 * vy.hs);
+        };
+        // Rows on their way; each goes into the slot of one that has been used.
+        uint32_t load_slot = 0, slot = 0;
+        auto load = [&] {
+            if (to_load > 0) {
+                --to_load;
+                if (load_on && load_head < heads) {
+                    R::load(ring + load_slot, px, place);
+                    if constexpr (MODE == kNormBwd) R::load(ring + load_slot + R::kSlotBytes, pg, place);
+                }
+                load_head += head_step;
+                px += head_step * vx.hs;
+                if constexpr (MODE == kNormBwd) pg += head_step * vg.hs;
+                if (--load_i == 0 && to_load > 0) {
+                    load_i = iters;
+                    load_head = head0;
+                    load_t += 1 << shift;
+                    open_load();
+                }
+                load_slot = load_slot + kRow == D * kRow ? 0 : load_slot + kRow;
+            }
+            copies_commit();
+        };
+        open_load();
+        open_store();
 #pragma unroll
-        for (int u = 0; u < U; ++u) load(u, u);
+        for (int u = 0; u < D; ++u) load();
         __syncwarp();  // the table's readers are done
-        for (int i = in_warp; i < a.pairs << shift; i += 32) {
+        for (int i = in_warp; i < a.pairs << unit_shift; i += 32) {
             const int k = static_cast<int>(fdiv(i, a.by_pairs)), f = i - k * a.pairs;
             const int tk = min(t0 + k, a.tokens - 1);
             const int64_t at = a.positions ? a.positions[tk] : a.first + static_cast<int64_t>(fmod_(tk, a.by_seq));
             float s, c;
             turn_sincos(static_cast<uint64_t>(at) * a.turns[f], s, c);
-            float* e = table + table_place<LAYOUT, LPR>(k, f, a);
+            float* e = table + table_place<T, LAYOUT, LPR>(k, f, unit_shift);
             e[0] = c * a.scale;
             e[2] = s * a.scale * a.sign;
         }
         __syncwarp();
-        const float4* turns = reinterpret_cast<const float4*>(table) + my_token * kHalfVec * LPR + lane;
+        const float4* turns = reinterpret_cast<const float4*>(table) + my_token * LPR + lane;  // its tokens' j'th at j << turn_shift
         float4 cs[kCsRegs ? kHalfVec : 1];
-        if constexpr (kCsRegs)
+        auto take_turns = [&] {
+            if constexpr (kCsRegs)
 #pragma unroll
-            for (int j = 0; j < kHalfVec; ++j) cs[j] = turns[j * LPR];
+                for (int j = 0; j < kHalfVec; ++j) cs[j] = turns[j << turn_shift];
+        };
+        take_turns();
         auto turn = [&](Pairs& p) {
             if (place.rot == 0) return;
             const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
             for (int j = 0; j < kHalfVec; ++j) {
-                const float4 q = kCsRegs ? cs[kCsRegs ? j : 0] : turns[j * LPR];
+                const float4 q = kCsRegs ? cs[kCsRegs ? j : 0] : turns[j << turn_shift];
                 const float2 c = make_float2(q.x, q.y), s = make_float2(q.z, q.w);
                 const float2 u = fma2(mul2(p.y[j], s), minus, mul2(p.x[j], c)), v = fma2(p.x[j], s, mul2(p.y[j], c));
                 if (place.rot == 0xffu) {
@@ -339,84 +536,95 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const 
                 }
             }
         };
-        for (int i0 = 0; i0 < iters; i0 += U) {
+        while (to_store > 0) {
+            --to_store;
+            const bool there = on && head < heads;
+            copies_wait<D - 1>();
+            if constexpr (!R::kOwn) __syncwarp();
+            const RowRaw<T, LAYOUT> raw = R::read(ring + slot, place);
+            Pairs p = pairs_of<T, LAYOUT>(raw), g;
+            if constexpr (MODE == kNormBwd) g = pairs_of<T, LAYOUT>(R::read(ring + slot + R::kSlotBytes, place));
+            if constexpr (R::kOwn) load();
+            if constexpr (MODE != kRotate) {
+                float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = head0 + (i0 + u) * head_step;
-                const bool there = on && h < heads;
-                Pairs p = pairs_of<T, LAYOUT>(rx[u]), g;
-                if constexpr (MODE == kNormBwd) g = pairs_of<T, LAYOUT>(rg[u]);
-                load(u, i0 + u + U);
-                if constexpr (MODE != kRotate) {
-                    float2 q = make_float2(0.f, 0.f);
+                for (int j = 0; j < kHalfVec; ++j) q = fma2(p.x[j], p.x[j], fma2(p.y[j], p.y[j], q));
+                const float r = rsqrtf(group_sum<LPR>(q.x + q.y) * a.inv_dim + a.eps);
+                const float2 rr = make_float2(r, r);
+                if constexpr (MODE == kNormFwd) {
 #pragma unroll
-                    for (int j = 0; j < kHalfVec; ++j) q = fma2(p.x[j], p.x[j], fma2(p.y[j], p.y[j], q));
-                    const float r = rsqrtf(group_sum<LPR>(q.x + q.y) * a.inv_dim + a.eps);
-                    const float2 rr = make_float2(r, r);
-                    if constexpr (MODE == kNormFwd) {
-#pragma unroll
-                        for (int j = 0; j < kHalfVec; ++j) {
-                            const float4 wj = ws[j][lane];
-                            p.x[j] = mul2(mul2(p.x[j], rr), make_float2(wj.x, wj.y));
-                            p.y[j] = mul2(mul2(p.y[j], rr), make_float2(wj.z, wj.w));
-                        }
-                        turn(p);
-                    } else {
-                        turn(g);
-                        // with g r and w g r in the place of g: dw = sum (g r) x, dx = w g r - x r^2 mean(w g r x)
-                        q = make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int j = 0; j < kHalfVec; ++j) {
-                            g.x[j] = mul2(g.x[j], rr);
-                            g.y[j] = mul2(g.y[j], rr);
-                            if (there) {  // r of a row that does not exist is infinite for eps = 0
-                                sum.x[j] = fma2(g.x[j], p.x[j], sum.x[j]);
-                                sum.y[j] = fma2(g.y[j], p.y[j], sum.y[j]);
-                            }
-                            const float4 wj = ws[j][lane];
-                            g.x[j] = mul2(g.x[j], make_float2(wj.x, wj.y));
-                            g.y[j] = mul2(g.y[j], make_float2(wj.z, wj.w));
-                            q = fma2(g.x[j], p.x[j], fma2(g.y[j], p.y[j], q));
-                        }
-                        const float d = -group_sum<LPR>(q.x + q.y) * a.inv_dim * r * r;
-                        const float2 dd = make_float2(d, d);
-#pragma unroll
-                        for (int j = 0; j < kHalfVec; ++j) {
-                            p.x[j] = fma2(p.x[j], dd, g.x[j]);
-                            p.y[j] = fma2(p.y[j], dd, g.y[j]);
-                        }
+                    for (int j = 0; j < kHalfVec; ++j) {
+                        const float4 wj = ws[j][lane];
+                        p.x[j] = mul2(mul2(p.x[j], rr), make_float2(wj.x, wj.y));
+                        p.y[j] = mul2(mul2(p.y[j], rr), make_float2(wj.z, wj.w));
                     }
-                } else {
                     turn(p);
+                } else {
+                    turn(g);
+                    // with g r and w g r in the place of g: dw = sum (g r) x, dx = w g r - x r^2 mean(w g r x)
+                    q = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < kHalfVec; ++j) {
+                        g.x[j] = mul2(g.x[j], rr);
+                        g.y[j] = mul2(g.y[j], rr);
+                        if (there) {  // r of a row that does not exist is infinite for eps = 0
+                            sum.x[j] = fma2(g.x[j], p.x[j], sum.x[j]);
+                            sum.y[j] = fma2(g.y[j], p.y[j], sum.y[j]);
+                        }
+                        const float4 wj = ws[j][lane];
+                        g.x[j] = mul2(g.x[j], make_float2(wj.x, wj.y));
+                        g.y[j] = mul2(g.y[j], make_float2(wj.z, wj.w));
+                        q = fma2(g.x[j], p.x[j], fma2(g.y[j], p.y[j], q));
+                    }
+                    const float d = -group_sum<LPR>(q.x + q.y) * a.inv_dim * r * r;
+                    const float2 dd = make_float2(d, d);
+#pragma unroll
+                    for (int j = 0; j < kHalfVec; ++j) {
+                        p.x[j] = fma2(p.x[j], dd, g.x[j]);
+                        p.y[j] = fma2(p.y[j], dd, g.y[j]);
+                    }
                 }
-                if (there) store_row<T, LAYOUT>(py + h * vy.hs, p, skip_rest, place, a);
+            } else {
+                turn(p);
+            }
+            R::store(ring + slot, py, p, raw, there, MODE == kRotate, skip_rest, 2 * a.pairs, place);
+            if constexpr (!R::kOwn) load();
+            slot = slot + kRow == D * kRow ? 0 : slot + kRow;
+            head += head_step;
+            py += head_step * vy.hs;
+            if (--store_i == 0 && to_store > 0) {
+                store_i = iters;
+                head = head0;
+                t += 1 << shift;
+                open_store();
+                turns += LPR << shift;
+                take_turns();
             }
         }
     }
     if constexpr (MODE == kNormBwd) {
         if (!a.partial) return;
         // the groups' sums, in the row's order, added in the groups' order
-        __syncthreads();
-        float* mine = tables + (warp * GW + group) * a.dim;
+        __syncthreads();  // the rings are free
+        float* const sums = reinterpret_cast<float*>(smem);
+        float* mine = sums + (warp * GW + group) * a.dim;
         float u[kVec], v[kVec];
-        vectors_of<LAYOUT>(sum, u, v);
+        chunks_of<LAYOUT>(sum, u, v);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            if constexpr (LAYOUT == kNarrow) {
-                const int n = lane + 32 * j;
-                if (2 * n >= a.dim) continue;
-                const int2 e = narrow_pair(n, a);
-                mine[e.x] = u[j];
-                mine[e.y] = v[j];
-            } else {
-                if (place.a >= 0) mine[place.a + j] = u[j];
-                if (place.b >= 0) mine[place.b + j] = v[j];
+        for (int j = 0; j < RowRaw<T, LAYOUT>::J; ++j) {
+            constexpr int W = RowRaw<T, LAYOUT>::W;
+            bool ta, tb;
+            const int ea = place.first(j, ta), eb = place.second(j, tb);
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                if (ta) mine[ea + k] = u[j * W + k];
+                if (tb) mine[eb + k] = v[j * W + k];
             }
         }
         __syncthreads();
         for (int j = threadIdx.x; j < a.dim; j += kHeadsThreads) {
             float total = 0.f;
-            for (int k = 0; k < G; ++k) total += tables[k * a.dim + j];
+            for (int k = 0; k < G; ++k) total += sums[k * a.dim + j];
             a.partial[static_cast<int64_t>(blockIdx.x) * a.dim + j] = total;
         }
     }
@@ -437,7 +645,7 @@ heads_dweight_kernel(T* __restrict__ dw0, T* __restrict__ dw1, const float* __re
     const int begin = n * threadIdx.y / 32, end = n * (threadIdx.y + 1) / 32;
     float sum = 0.f;
     if (j < dim)
-#pragma unroll 4
+#pragma unroll 10
         for (int k = begin; k < end; ++k) sum += partial[static_cast<int64_t>(first + k) * dim + j];
     part[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
@@ -447,20 +655,38 @@ heads_dweight_kernel(T* __restrict__ dw0, T* __restrict__ dw1, const float* __re
     }
 }
 
+template <typename T, int LAYOUT, int LPR, int MODE>
+cudaError_t launch_kernel(const HeadsArgs& a, int ctas, cudaStream_t s) {
+    static int done[kMaxDevices];
+    const cudaError_t e = allow_max_dynamic_smem(heads_kernel<T, LAYOUT, LPR, MODE>, done);
+    if (e != cudaSuccess) return e;
+    const int tokens = 1 << std::max(a.tok_shift[0] + a.sub_shift[0], a.tok_shift[1] + a.sub_shift[1]);
+    const size_t row = Ring<T, LAYOUT, LPR>::kSlotBytes * (MODE == kNormBwd ? 2 : 1);
+    const size_t smem = kHeadsWarps * (ring_slots<T, MODE>() * row + static_cast<size_t>(tokens) * LPR * kVec * 8);
+    return launch_pdl(heads_kernel<T, LAYOUT, LPR, MODE>, dim3(static_cast<unsigned>(ctas)), dim3(kHeadsThreads), smem, s, a);
+}
+
 template <typename T, int LAYOUT, int LPR>
 cudaError_t launch_mode(const HeadsArgs& a, const HeadsCall& c, int ctas, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(ctas)), block(kHeadsThreads);
-    if (!c.norm) return launch_pdl(heads_kernel<T, LAYOUT, LPR, kRotate>, grid, block, 0, s, a);
-    if (!c.backward) return launch_pdl(heads_kernel<T, LAYOUT, LPR, kNormFwd>, grid, block, 0, s, a);
-    return launch_pdl(heads_kernel<T, LAYOUT, LPR, kNormBwd>, grid, block, 0, s, a);
+    if (!c.norm) return launch_kernel<T, LAYOUT, LPR, kRotate>(a, ctas, s);
+    if (!c.backward) return launch_kernel<T, LAYOUT, LPR, kNormFwd>(a, ctas, s);
+    return launch_kernel<T, LAYOUT, LPR, kNormBwd>(a, ctas, s);
 }
 
 template <typename T, int LAYOUT>
 cudaError_t launch_width(int lpr, const HeadsArgs& a, const HeadsCall& c, int ctas, cudaStream_t s) {
+    if (lpr == 1) return launch_mode<T, LAYOUT, 1>(a, c, ctas, s);
+    if (lpr == 2) return launch_mode<T, LAYOUT, 2>(a, c, ctas, s);
     if (lpr == 4) return launch_mode<T, LAYOUT, 4>(a, c, ctas, s);
     if (lpr == 8) return launch_mode<T, LAYOUT, 8>(a, c, ctas, s);
     if (lpr == 16) return launch_mode<T, LAYOUT, 16>(a, c, ctas, s);
     return launch_mode<T, LAYOUT, 32>(a, c, ctas, s);
+}
+
+template <typename T> cudaError_t launch_halves(int width, int lpr, const HeadsArgs& a, const HeadsCall& c, int ctas, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2)
+        if (width == 8) return launch_width<T, 8>(lpr, a, c, ctas, s);
+    return launch_width<T, 4>(lpr, a, c, ctas, s);
 }
 
 HeadsView view_of(const ls_head_view* v) {
@@ -468,25 +694,28 @@ HeadsView view_of(const ls_head_view* v) {
 }
 
 // A unit's tokens, and the units that share their heads.  The groups that share a token go through its heads
-// side by side: few of them leave each more heads to use its cosines on, many end sooner.  Counted in rounds of
-// the warps that the GPU holds (`slots` of them are this tensor's), a round being the heads that a group goes
-// through and about one and a half more for the angles.
+// side by side: few of them leave each more heads to use its cosines on, many end sooner; heads that are few leave
+// room for more tokens one after the other.  Counted in rounds of the warps that the GPU holds (`slots` of them are
+// this tensor's): a unit takes as long as three rows, a row counting 2, and what its rows and its angles take.
 void plan_units(HeadsArgs& a, int which, int groups, int64_t slots) {
     int64_t best = INT64_MAX;
     for (int split = 0; split <= 5; ++split)
-        for (int shift = 0; (1 << shift) <= groups; ++shift) {
-            const int64_t step = static_cast<int64_t>(groups >> shift) << split;
-            if (split > 0 && step >= 2 * a.heads[which]) continue;
-            const int64_t iters = (a.heads[which] + step - 1) / step;
-            const int64_t units = ((static_cast<int64_t>(a.tokens) + (1 << shift) - 1) >> shift) << split;
-            const int64_t t = (units + slots - 1) / slots * (2 * iters + 3);
-            if (units > INT32_MAX / 2 || t > best || (t == best && split > a.split_shift[which])) continue;
-            best = t;
-            a.tok_shift[which] = shift;
-            a.split_shift[which] = split;
-            a.iters[which] = static_cast<int>(iters);
-            a.units[which] = static_cast<int>(units);
-        }
+        for (int shift = 0; (1 << shift) <= groups; ++shift)
+            for (int sub = 0; sub <= kMostSub; ++sub) {
+                const int64_t step = static_cast<int64_t>(groups >> shift) << split;
+                if (split > 0 && (sub > 0 || step >= 2 * a.heads[which])) continue;
+                const int64_t iters = (a.heads[which] + step - 1) / step;
+                const int64_t units = ((static_cast<int64_t>(a.tokens) + (1 << (shift + sub)) - 1) >> (shift + sub)) << split;
+                const int64_t angles = ((static_cast<int64_t>(a.pairs) << (shift + sub)) + 31) / 32;
+                const int64_t t = (units + slots - 1) / slots * (2 * (iters << sub) + angles + 3);
+                if (units > int64_t{1} << 30 || t > best || (t == best && split > a.split_shift[which])) continue;
+                best = t;
+                a.tok_shift[which] = shift;
+                a.sub_shift[which] = sub;
+                a.split_shift[which] = split;
+                a.iters[which] = static_cast<int>(iters);
+                a.units[which] = static_cast<uint32_t>(units);
+            }
 }
 
 }  // namespace
@@ -496,24 +725,23 @@ template <typename T> cudaError_t launch_heads(const HeadsCall& c, cudaStream_t 
     a.tokens = static_cast<int>(c.batch * c.seq);
     a.by_seq = make_fastdiv(static_cast<uint32_t>(c.seq));
     a.dim = static_cast<int>(c.dim);
-    a.vecs = a.dim / kVec;
     a.eps = c.eps;
     a.inv_dim = 1.f / static_cast<float>(a.dim);
     a.sign = c.backward ? -1.f : 1.f;
     a.scale = 1.f;
     if (const ls_rotation* r = c.rotation) {
         a.pairs = static_cast<int>(r->rotary_dim / 2);
-        a.interleaved = r->interleaved != 0;
         a.turns = r->turns;
         a.positions = r->positions;
         a.first = r->first_position;
         a.scale = r->scale;
     }
     a.by_pairs = make_fastdiv(static_cast<uint32_t>(std::max(a.pairs, 1)));
-    const int layout = a.pairs % (a.interleaved ? kVec / 2 : kVec) ? kNarrow : a.interleaved ? kInterleaved : kHalf;
-    int lpr = 32;
-    if (layout != kNarrow)
-        for (lpr = 4; 2 * lpr < a.vecs;) lpr *= 2;
+    int layout = 16 / sizeof(T);
+    if (c.rotation && c.rotation->interleaved) layout = kInterleaved;
+    while (layout > 1 && a.pairs % layout) layout /= 2;
+    int lpr = 1;
+    while (2 * kVec * lpr < a.dim) lpr *= 2;
     const bool partial = c.norm && c.backward && (c.dweight[0] || c.dweight[1]);
     int64_t rows[2] = {0, 0};
     for (int k = 0; k < 2; ++k) {
@@ -543,9 +771,10 @@ template <typename T> cudaError_t launch_heads(const HeadsCall& c, cudaStream_t 
     const int all = static_cast<int>(ctas[0] + ctas[1]);
     cudaError_t e = cudaSuccess;
     if (all > 0) {
-        e = layout == kNarrow         ? launch_mode<T, kNarrow, 32>(a, c, all, s)
-            : layout == kInterleaved ? launch_width<T, kInterleaved>(lpr, a, c, all, s)
-                                     : launch_width<T, kHalf>(lpr, a, c, all, s);
+        e = layout == kInterleaved ? launch_width<T, kInterleaved>(lpr, a, c, all, s)
+            : layout >= 4          ? launch_halves<T>(layout, lpr, a, c, all, s)
+            : layout == 2          ? launch_width<T, 2>(lpr, a, c, all, s)
+                                   : launch_width<T, 1>(lpr, a, c, all, s);
     }
     if (e != cudaSuccess || !partial) return e;
     // zeros for a tensor without rows
