@@ -65,25 +65,26 @@ struct HeadsArgs {
     bool skip_rest[2];       // in place without the norm: elements behind rotary_dim stay untouched
     const uint64_t* turns;
     const int32_t* positions;
-    int64_t first;
+    int32_t first;
     float scale, sign;       // sign: -1 transposes the rotation
     float eps, inv_dim;
     float* partial;          // [kPartialCtas][dim]
 };
 
-// sin and cos of frac * 2^-64 of a circle.
-__device__ __forceinline__ void turn_sincos(uint64_t frac, float& s, float& c) {
-    const uint32_t q = static_cast<uint32_t>((frac + (uint64_t{1} << 61)) >> 62);  // the nearest quarter
-    const int64_t r = static_cast<int64_t>(frac - (static_cast<uint64_t>(q) << 62));
-    // |r| <= 2^61, an eighth of a turn; its upper half, in radians, and Taylor's series, whose next terms are below
-    // 2e-9 and 1e-10
-    const float x = static_cast<float>(static_cast<int32_t>(r >> 32)) * 1.4629180792671596e-9f, z = x * x;
+// sin and cos of turns * position * 2^-64 of a circle: the upper 32 bits of the product (below them 1.5e-9 of an angle).
+__device__ __forceinline__ void turn_sincos(uint64_t turns, int32_t position, float& s, float& c) {
+    const uint32_t lo = static_cast<uint32_t>(turns), hi = static_cast<uint32_t>(turns >> 32);
+    const uint32_t at = static_cast<uint32_t>(position);
+    const uint32_t frac = __umulhi(lo, at) + hi * at - (position < 0 ? lo : 0u);
+    const uint32_t q = (frac + (1u << 29)) >> 30;  // the nearest quarter
+    const int32_t r = static_cast<int32_t>(frac - (q << 30));
+    // at most an eighth of a turn; in radians, and Taylor's series, whose next terms are below 2e-9 and 1e-10
+    const float x = static_cast<float>(r) * 1.4629180792671596e-9f, z = x * x;
     const float sr = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
     const float cr = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
-    s = q & 1 ? cr : sr;
-    c = q & 1 ? sr : cr;
-    if (q & 2) s = -s;
-    if ((q + 1) & 2) c = -c;
+    // quarters turn (c, s) into (-s, c), (-c, -s) and (s, -c)
+    s = __uint_as_float(__float_as_uint(q & 1 ? cr : sr) ^ ((q << 30) & 0x80000000u));
+    c = __uint_as_float(__float_as_uint(q & 1 ? sr : cr) ^ (((q + 1) << 30) & 0x80000000u));
 }
 
 // W elements of the storage type, as they lie in memory.
@@ -446,6 +447,10 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const 
         __syncthreads();
     }
 
+    const float sine_scale = a.scale * a.sign;
+    const int seq = static_cast<int>(a.by_seq.d), table_tokens = a.pairs ? 1 << unit_shift : 0;
+    const int first_k = static_cast<int>(fdiv(in_warp, a.by_pairs)), first_f = in_warp - first_k * a.pairs;
+    const int step_k = static_cast<int>(fdiv(32, a.by_pairs)), step_f = 32 - step_k * a.pairs;
     for (uint32_t unit = cta * kHeadsWarps + warp; unit < a.units[which]; unit += ctas * kHeadsWarps) {
         const int t0 = static_cast<int>(unit >> split) << unit_shift;
         const int head0 = (group >> shift) + side * static_cast<int>(unit & ((1u << split) - 1));
@@ -494,15 +499,27 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const 
 #pragma unroll
         for (int u = 0; u < D; ++u) load();
         __syncwarp();  // the table's readers are done
-        for (int i = in_warp; i < a.pairs << unit_shift; i += 32) {
-            const int k = static_cast<int>(fdiv(i, a.by_pairs)), f = i - k * a.pairs;
-            const int tk = min(t0 + k, a.tokens - 1);
-            const int64_t at = a.positions ? a.positions[tk] : a.first + static_cast<int64_t>(fmod_(tk, a.by_seq));
+        // pair f of token k, and 32 pairs on
+        const int l0 = static_cast<int>(fmod_(t0, a.by_seq));
+        for (int k = first_k, f = first_f; k < table_tokens;) {
+            int32_t at;
+            if (a.positions) {
+                at = a.positions[min(t0 + k, a.tokens - 1)];
+            } else {
+                const int l = l0 + k;
+                at = a.first + (l < seq ? l : static_cast<int>(fmod_(l, a.by_seq)));
+            }
             float s, c;
-            turn_sincos(static_cast<uint64_t>(at) * a.turns[f], s, c);
+            turn_sincos(a.turns[f], at, s, c);
             float* e = table + table_place<T, LAYOUT, LPR>(k, f, unit_shift);
             e[0] = c * a.scale;
-            e[2] = s * a.scale * a.sign;
+            e[2] = s * sine_scale;
+            f += step_f;
+            k += step_k;
+            if (f >= a.pairs) {
+                f -= a.pairs;
+                ++k;
+            }
         }
         __syncwarp();
         const float4* turns = reinterpret_cast<const float4*>(table) + my_token * LPR + lane;  // its tokens' j'th at j << turn_shift
@@ -521,7 +538,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const 
                 const float4 q = kCsRegs ? cs[kCsRegs ? j : 0] : turns[j << turn_shift];
                 const float2 c = make_float2(q.x, q.y), s = make_float2(q.z, q.w);
                 const float2 u = fma2(mul2(p.y[j], s), minus, mul2(p.x[j], c)), v = fma2(p.x[j], s, mul2(p.y[j], c));
-                if (place.rot == 0xffu) {
+                if ((MODE == kRotate && sizeof(T) == 2) || place.rot == 0xffu) {  // the former stores the others as it read them
                     p.x[j] = u;
                     p.y[j] = v;
                 } else {  // what the others hold (a NaN, say) stays out of them
@@ -733,7 +750,7 @@ template <typename T> cudaError_t launch_heads(const HeadsCall& c, cudaStream_t 
         a.pairs = static_cast<int>(r->rotary_dim / 2);
         a.turns = r->turns;
         a.positions = r->positions;
-        a.first = r->first_position;
+        a.first = static_cast<int32_t>(r->first_position);
         a.scale = r->scale;
     }
     a.by_pairs = make_fastdiv(static_cast<uint32_t>(std::max(a.pairs, 1)));
