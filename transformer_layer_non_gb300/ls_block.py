@@ -131,7 +131,7 @@ def grad_norm_workspace_bytes() -> int:
 # --- queries and keys ---------------------------------------------------------
 _VIEW = struct.Struct("@P4q")        # ls_head_view
 _ROTATION = struct.Struct("@PqifPq")  # ls_rotation
-_TENSOR = struct.Struct("@P2q")      # ls_tensor
+_TENSOR = struct.Struct("@P2q")      # ls_tensor, as TensorList packs many of them
 
 
 class Rotation:
@@ -344,12 +344,18 @@ class TensorList:
     def __init__(self, tensors):
         dev = _v._device()
         self.tensors = list(tensors)
-        packed = []
-        for i, t in enumerate(self.tensors):
-            name = f"tensors[{i}]"
-            p, _ = _v._shaped(name, t, t.dim() if hasattr(t, "dim") else 0, None, dev)
-            packed.append(_TENSOR.pack(p, t.numel(), _v._storage_code(t)))
-        self.packed, self.device = b"".join(packed), dev
+        fields, codes = [], _v._codes
+        try:  # one look at each; what is wrong is only looked for when something is
+            for t in self.tensors:
+                if not t.is_contiguous() or t.get_device() != dev:
+                    raise ValueError
+                fields += (t.data_ptr(), t.numel(), codes[t.dtype])
+        except (AttributeError, KeyError, TypeError, ValueError):
+            for i, t in enumerate(self.tensors):
+                _v._shaped(f"tensors[{i}]", t, len(getattr(t, "shape", ())), None, dev)
+                _v._storage_code(t)
+            raise
+        self.packed, self.device = struct.pack(f"@{len(fields)}q", *fields), dev
 
     def __len__(self):
         return len(self.tensors)
