@@ -1,7 +1,8 @@
 """Build the C-ABI operator libraries for sm_103a with nvcc: ``libls_ops.so``
 (the layer operators, ``csrc/``), ``libls_vocab.so`` (the vocabulary
 operators, ``csrc_vocab/``) and ``libls_block.so`` (the decoder block's
-operators, ``csrc_block/``).
+operators, ``csrc_block/``); with g++ the compiled half of the last one's
+Python binding.
 
 A library's translation units compile in parallel and link into
 ``transformer_layer_non_gb300/_build/``.  A rebuild happens only when a source
@@ -18,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -29,6 +31,9 @@ VOCAB_CSRC = os.path.join(PKG, "csrc_vocab")
 VOCAB_LIB = os.path.join(BUILD, "libls_vocab.so")
 BLOCK_CSRC = os.path.join(PKG, "csrc_block")
 BLOCK_LIB = os.path.join(BUILD, "libls_block.so")
+# The compiled half of ls_block.py, a Python extension module.
+BINDING_SRC = os.path.join(BLOCK_CSRC, "binding.cpp")
+BINDING_LIB = os.path.join(BUILD, "_ls_block_call.so")
 # The benchmark's reference streaming kernel (not part of the operator library).
 FLOOR_SRC = os.path.join(PKG, "floor", "stream_floor.cu")
 FLOOR_LIB = os.path.join(BUILD, "libls_floor.so")
@@ -142,6 +147,21 @@ def build_block(force: bool = False, verbose: bool = False, ptxas_verbose: bool 
                              ptxas_verbose)
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the compiled half of ls_block.py; returns its path."""
+    if not force and _newer_than(BINDING_LIB, [BINDING_SRC, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return BINDING_LIB
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = BINDING_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden", "-I",
+           sysconfig.get_paths()["include"], "-I", INCLUDE, "-o", tmp, BINDING_SRC]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
+
+
 def build_floor(force: bool = False) -> str:
     """Compile the benchmark's reference streaming kernel into libls_floor.so."""
     if (not force and os.path.exists(FLOOR_LIB)
@@ -167,4 +187,5 @@ if __name__ == "__main__":
     print(build(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
     print(build_vocab(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
     print(build_block(force=a.force or a.ptxas, verbose=a.verbose, ptxas_verbose=a.ptxas))
+    print(build_binding(force=a.force))
     print(build_floor(force=a.force))

@@ -91,7 +91,39 @@ def load(build_if_needed: bool = True):
         fn.restype = res
         fn.argtypes = args
     _lib = lib
+    _load_binding(lib, build_if_needed)
     return lib
+
+
+class _Closer:
+    """In the compiled half's place until it is loaded: every call looks closer."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
+_call = _Closer()
+
+
+def _load_binding(lib, build_if_needed: bool):
+    """Load the compiled half of this binding (csrc_block/binding.cpp), which has
+    each operator's common case."""
+    global _call
+    import importlib.machinery
+    import importlib.util
+
+    path = _build.build_binding() if build_if_needed else _build.BINDING_LIB
+    spec = importlib.util.spec_from_file_location(
+        "_ls_block_call", path, loader=importlib.machinery.ExtensionFileLoader("_ls_block_call", path))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _device_of_calls, stream = _v._device, lambda device: _v._stream_of(None, device)
+    if _v._device() >= 0:  # the functions themselves, where there is a device
+        stream_of = getattr(_v._torch._C, "_cuda_getCurrentRawStream", None)
+        _device_of_calls, stream = _v._get_device, stream_of or stream
+    module.setup(_v._codes, ACTIVATIONS, _device_of_calls, stream, _v._float32, _v._int32, TensorList,
+                 {name: ctypes.cast(getattr(lib, name), _P).value for name in EXPORTS})
+    _call = module
 
 
 def last_error() -> str:
@@ -100,6 +132,12 @@ def last_error() -> str:
 
 def _check(status: int):
     if status != LS_OK:
+        raise LsError(status, last_error())
+
+
+def _made(status: int):
+    """After the compiled half made a call."""
+    if status:
         raise LsError(status, last_error())
 
 
@@ -240,6 +278,9 @@ def ls_rotary_fwd(q_out, k_out, q, k, rotation: Rotation, positions=None, first_
                   stream=None):
     """Rotated queries and keys (k and k_out may be None); an output may be its
     input.  positions: int32 [batch, seq], or None for first_position onwards."""
+    status = _call.rotary_fwd(q_out, k_out, q, k, rotation, positions, first_position, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     p, batch, seq, dim, _ = _views(dev, "q", q, "k", k, "q_out", q_out, "k_out", k_out)
     _check(load().ls_rotary_fwd(_v._storage_code(q), p[2], p[3], p[0], p[1], batch, seq, dim,
@@ -251,6 +292,9 @@ def ls_rotary_bwd(dq, dk, dq_out, dk_out, rotation: Rotation, positions=None, fi
                   stream=None):
     """Gradients of queries and keys from those of the rotated ones (dk and
     dk_out may be None); dq may be dq_out."""
+    status = _call.rotary_bwd(dq, dk, dq_out, dk_out, rotation, positions, first_position, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     p, batch, seq, dim, _ = _views(dev, "dq_out", dq_out, "dk_out", dk_out, "dq", dq, "dk", dk)
     _check(load().ls_rotary_bwd(_v._storage_code(dq_out), p[2], p[3], p[0], p[1], batch, seq, dim,
@@ -262,6 +306,9 @@ def ls_qk_norm_rotary_fwd(q_out, k_out, q, k, q_weight, k_weight, rotation: Rota
                           eps: float = 1e-6, positions=None, first_position: int = 0, stream=None):
     """Queries and keys normalised head by head, weighted ([head_dim] or None
     for ones) and rotated (rotation None: not)."""
+    status = _call.norm_fwd(q_out, k_out, q, k, q_weight, k_weight, rotation, eps, positions, first_position, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     p, batch, seq, dim, dtype = _views(dev, "q", q, "k", k, "q_out", q_out, "k_out", k_out)
     rot = None if rotation is None else rotation._packed(positions, first_position, batch, seq, dev)
@@ -277,6 +324,10 @@ def ls_qk_norm_rotary_bwd(dq, dk, dq_weight, dk_weight, dq_out, dk_out, q, k, q_
                           first_position: int = 0, workspace=None, stream=None):
     """Gradients of queries, keys and their weights (None: not wanted) from the
     forward's inputs and the gradients of its outputs; dq may be dq_out or q."""
+    status = _call.norm_bwd(dq, dk, dq_weight, dk_weight, dq_out, dk_out, q, k, q_weight, k_weight, rotation, eps,
+                              positions, first_position, workspace, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     p, batch, seq, dim, dtype = _views(dev, "q", q, "k", k, "dq_out", dq_out, "dk_out", dk_out, "dq", dq,
                                        "dk", dk)
@@ -300,6 +351,9 @@ def _activation(name) -> int:
 def ls_gated_linear_fwd(h, x, gate_weight, up_weight, activation: str = "silu", stream=None):
     """h [rows, ffn] = act(x gate_weight^T) * (x up_weight^T) for x [rows,
     hidden] and weights [ffn, hidden]."""
+    status = _call.gated_fwd(h, x, gate_weight, up_weight, activation, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     px, (rows, hidden) = _v._shaped("x", x, 2, None, dev)
     pg, (ffn, wide) = _v._shaped("gate_weight", gate_weight, 2, x.dtype, dev)
@@ -316,6 +370,10 @@ def ls_gated_linear_bwd(dx, dgate_weight, dup_weight, dh, x, gate_weight, up_wei
     """Gradients of x and of both weights (dx, or both of the weights', may be
     None).  Weights' gradients in the storage dtype are written; float32 ones
     are added to."""
+    status = _call.gated_bwd(dx, dgate_weight, dup_weight, dh, x, gate_weight, up_weight, activation, workspace,
+                               stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     px, (rows, hidden) = _v._shaped("x", x, 2, None, dev)
     pg, (ffn, wide) = _v._shaped("gate_weight", gate_weight, 2, x.dtype, dev)
@@ -375,6 +433,9 @@ def ls_grad_norm(norm, factor, grads, max_norm: float = float("inf"), grad_scale
     """The global norm of the gradients (a TensorList, or tensors) times
     grad_scale, and the factor that unscales and clips them; both FP32 of one
     element, either may be None."""
+    status = _call.grad_norm(norm, factor, grads, max_norm, grad_scale, workspace, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     grads = _list(grads)
     pn = _v._optional("norm", norm, (1,), _v._float32, dev)
@@ -386,6 +447,9 @@ def ls_grad_norm(norm, factor, grads, max_norm: float = float("inf"), grad_scale
 
 def ls_scale_gradients(out, grads, factor, stream=None):
     """out[t] = factor * grads[t] (TensorLists, or tensors; out may be grads)."""
+    status = _call.scale_gradients(out, grads, factor, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     out, grads = _list(out), _list(grads)
     if len(out) != len(grads):
@@ -399,6 +463,9 @@ def ls_adam_update_scaled(param, grad, exp_avg, exp_avg_sq, factor, lr: float, b
                           stream=None):
     """``ls_ops.ls_adam_update`` with the gradient's factor (FP32 of one
     element) in device memory, such as ls_grad_norm leaves it."""
+    status = _call.adam(param, grad, exp_avg, exp_avg_sq, factor, lr, beta1, beta2, eps, weight_decay, step, stream)
+    if status >= 0:
+        return _made(status)
     dev = _v._device()
     pp, (n,) = _v._shaped("param", param, 1, None, dev)
     pg = _v._tensor("grad", grad, (n,), param.dtype, dev)
