@@ -183,7 +183,8 @@ ls_status ls_gated_linear_fwd(ls_dtype dtype, void* h, const void* x, const void
 
 /* Backward of the above, from its inputs (g and u, the two sums, are computed
  * again; the forward keeps nothing):
- *   dg = dh u act'(g),  du = dh act(g)                    (rounded once to the storage dtype)
+ *   dg = dh u act'(g),  du = dh act(g)                    (rounded once to the storage dtype; of up
+ *                                to 32 rows and 16384 elements to two numbers of it each)
  *   dx = dg gate_weight + du up_weight,  dgate_weight = dg^T x,  dup_weight = du^T x
  * dx: [rows, hidden] in the storage dtype, written, or NULL.  dgate_weight and
  * dup_weight: [ffn, hidden], both or neither NULL; with dweight_dtype == dtype
@@ -199,7 +200,7 @@ ls_status ls_gated_linear_bwd(ls_dtype dtype, void* dx, void* dgate_weight, void
                               int64_t hidden, int64_t ffn, ls_activation activation,
                               void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of ls_gated_linear_bwd: dg and du, up to 16 FP32 copies of
+/* Workspace bytes of ls_gated_linear_bwd: dg and du (of few elements twice), up to 16 FP32 copies of
  * dx, and FP32 sums of the weights' gradients (one of each beyond 16384 rows, up
  * to 8 of small weights).  0 for invalid sizes.  The forward needs none. */
 size_t ls_gated_linear_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn);

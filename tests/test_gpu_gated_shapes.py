@@ -34,3 +34,17 @@ def test_activations(act, rows):
 @pytest.mark.parametrize("rows", [20, 50, 700])
 def test_a_nan_stays_in_its_row(rows):
     gated.test_a_nan_stays_in_its_row(rows)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("sizes", [(1, 344, 480), (2, 72, 2000), (3, 376, 240), (8, 1280, 136), (17, 64, 520), (32, 264, 512)],
+                         ids=gated.name)
+def test_few_terms_are_rounded_once(sizes, dtype):
+    """Where dg and du have few elements, so that one of them shows, the gradients are as good as their own rounding:
+    what they are made of keeps 16 bits at the least, 2^-16 of a term beside a result's 2^-11 or 2^-8."""
+    c = gated.Case(dtype, *sizes, seed=9)
+    _, _, dx, _, dw, _ = c.exact()
+    gx, gw = c.backward()
+    for got, want in ((gx, dx), *zip(gw, dw)):
+        alone = torch.linalg.norm(want.to(c.t).double() - want)
+        assert torch.linalg.norm(got.double() - want) <= 1.1 * alone

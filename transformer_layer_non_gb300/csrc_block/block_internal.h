@@ -58,10 +58,11 @@ cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg
 cudaError_t launch_gated_bwd(ls_dtype dt, void* dx, void* dwg, void* dwu, bool f32_dweight,
                              const void* dh, const void* x, const void* wg, const void* wu,
                              const GatedShape& sh, void* workspace, cudaStream_t s);
-// Few rows (gated_few.cu): whether these sizes are its own; h, or with dh dg (in h's place) and du.
+// Few rows (gated_few.cu): whether these sizes are its own; h, or with dh dg (in h's place) and du, with the rest of
+// their rounding in dg_low and du_low unless these are NULL.
 bool gated_few_rows(int64_t rows, int64_t hidden, int64_t ffn);
 cudaError_t launch_gated_few(ls_dtype dt, void* h, void* du, const void* dh, const void* x, const void* wg, const void* wu,
-                             const GatedShape& sh, cudaStream_t s);
+                             const GatedShape& sh, void* dg_low, void* du_low, cudaStream_t s);
 cudaError_t launch_block_wait_selftest(uint32_t polls, cudaStream_t s);
 cudaError_t gated_take_device_error(unsigned int* flags);
 

@@ -46,6 +46,12 @@ constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * 
 constexpr int kGroupM = 16;   // row tiles that share a sweep over the columns
 constexpr int kPairs = 76;    // pairs of SMs; a constant, so that plans depend on the shapes alone
 constexpr int kMostHalf = 128;
+// dg and du are rounded to 16 bits before they are summed up to gradients.  Of many elements that adds as much again
+// to the gradients' own rounding, as a whole (1.4 times the error); of few, single ones show (3 x 376 x 240: 1.5
+// times), so these are kept as two 16-bit numbers each.  Up to kPairRows rows, whose K block of dW has room for the
+// second ones; dx takes twice the K blocks (1 x 344 x 480, step: 10.1 -> 10.7 us).
+constexpr int kPairRows = 32;
+constexpr int64_t kPairElements = 16384;
 
 enum Mode { kFwd = 0, kGrad = 1, kOut = 2 };
 
@@ -65,7 +71,8 @@ struct GatedArgs {
     int w_tiles;               // of one dW, in a slice
     int width;                 // columns of a tile: 128 or 256
     int w_slice_blocks;        // of the rows
-    int h_tiles, f_blocks;
+    int h_tiles, f_blocks, x_blocks;  // x_blocks: K blocks of dx
+    bool pairs;                // dg and du as sums of two 16-bit numbers, of which the second ones are apart
     int w_kb0, w_k_blocks;     // the rows that dW's sums run over in this launch
     bool w_first, x_partial, w_partial, w_f32, w_add;  // partial: FP32 sums of slices go to scratch
     int pairs1, first_short1;  // how the shorter units are dealt, see Deal
@@ -74,6 +81,7 @@ struct GatedArgs {
 struct GatedMaps {
     CUtensorMap a, b, b2;      // kFwd, kGrad: x, Wg, Wu;  kOut: dg for dx, Wg, Wu
     CUtensorMap a2;            // kOut: du for dx
+    CUtensorMap a_low, a2_low, wa_low, wa2_low;  // kOut: the second numbers of dg and du
     CUtensorMap wa, wa2, wb;   // kOut: dg, du, x for dW;  kFwd, kGrad: Wg, Wu for halved tiles
     CUtensorMap out, out2, out3;  // h; dg, du; dx, dWg, dWu
 };
@@ -119,7 +127,7 @@ template <int MODE> __device__ __forceinline__ Unit unit_of(int u, const GatedAr
             t.slice = r / a.x_units;
             r -= t.slice * a.x_units;
             t.kb0 = t.slice * a.slice_blocks;
-            t.kbs = min(a.slice_blocks, 2 * a.f_blocks - t.kb0);
+            t.kbs = min(a.slice_blocks, a.x_blocks - t.kb0);
         }
         t.half = 0;
         t.n0 = (r % a.h_tiles) * a.width;
@@ -255,12 +263,27 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                         if (has_a) tma_load_2d(pa, &maps.a, k, m, bar);
                         tma_load_2d(pb, b_map, k, n, bar);
                     } else if (!t.weight) {
-                        const bool up = t.kb0 + kb >= a.f_blocks;
-                        const int k = (t.kb0 + kb - (up ? a.f_blocks : 0)) * kBlockK;
+                        int b = t.kb0 + kb;  // of dg, du, and the second numbers of both
+                        const bool low = b >= 2 * a.f_blocks;
+                        if (low) b -= 2 * a.f_blocks;
+                        const bool up = b >= a.f_blocks;
+                        const int k = (b - (up ? a.f_blocks : 0)) * kBlockK;
                         const CUtensorMap* w = up ? &maps.b2 : &maps.b;
-                        if (has_a) tma_load_2d(pa, up ? &maps.a2 : &maps.a, k, m, bar);
+                        const CUtensorMap* d = low ? (up ? &maps.a2_low : &maps.a_low) : up ? &maps.a2 : &maps.a;
+                        if (has_a) tma_load_2d(pa, d, k, m, bar);
                         tma_load_2d(pb, w, n, k, bar);
                         if (b_rows > 64) tma_load_2d(pb + kOperandBytes / 2, w, n + 64, k, bar);
+                    } else if (a.pairs) {  // 32 rows of the first numbers, the same of the second ones; x twice
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const CUtensorMap* d = t.weight == 2 ? (h ? &maps.wa2_low : &maps.wa2) : h ? &maps.wa_low : &maps.wa;
+                            unsigned char* const da = pa + h * (kPairRows * 128);
+                            unsigned char* const db = pb + h * (kPairRows * 128);
+                            tma_load_2d(da, d, m, 0, bar);
+                            tma_load_2d(da + kOperandBytes / 2, d, m + 64, 0, bar);
+                            tma_load_2d(db, &maps.wb, n, 0, bar);
+                            if (b_rows > 64) tma_load_2d(db + kOperandBytes / 2, &maps.wb, n + 64, 0, bar);
+                        }
                     } else {
                         const int k = (t.kb0 + kb) * kBlockK;
                         const CUtensorMap* d = t.weight == 2 ? &maps.wa2 : &maps.wa;
@@ -584,13 +607,15 @@ struct GatedPlan {
     int64_t w_slices, w_slice_blocks;  // of the rows, for dW
     int64_t x_len;                     // what a unit of dx takes
     bool w_first;
+    bool pairs;                        // dg and du as two numbers each
     size_t du, partial, w_partial, bytes;
     static int64_t length(int64_t width, int64_t blocks, bool joined) {
         return blocks * (width == kTileN ? 20 : 15) + (joined ? 2 : 1) * (width == kTileN ? 20 : 14);
     }
     GatedPlan(int64_t rows, int64_t hidden, int64_t ffn) {
         const int64_t m_tiles = ceil_div(rows, kTileM);
-        const int64_t kb = 2 * ceil_div(ffn, kBlockK), row_blocks = ceil_div(rows, kBlockK);
+        pairs = rows <= kPairRows && rows * ffn <= kPairElements;
+        const int64_t kb = (pairs ? 4 : 2) * ceil_div(ffn, kBlockK), row_blocks = ceil_div(rows, kBlockK);
         // joining slices: a launch, and their bytes at about 1.7 MB for a K block's time
         auto join = [](int64_t n, int64_t elements) { return n > 1 ? n * elements * 4 / 85000 : 0; };
         int64_t best = INT64_MAX;
@@ -620,7 +645,7 @@ struct GatedPlan {
             }
         }
         du = round256(static_cast<size_t>(rows * ffn) * 2);
-        partial = 2 * du;
+        partial = (pairs ? 4 : 2) * du;
         w_partial = partial + (slices > 1 ? round256(static_cast<size_t>(slices * rows * hidden) * 4) : 0);
         const bool scratch = w_slices > 1 || rows > kMostRows;
         bytes = w_partial + (scratch ? round256(static_cast<size_t>(2 * w_slices * ffn * hidden) * 4) : 0);
@@ -676,10 +701,11 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
     const GatedPlan p(sh.rows, sh.hidden, sh.ffn);
     char* ws = static_cast<char*>(workspace);
     void *dg = ws, *du = ws + p.du;
+    void *dg_low = p.pairs ? ws + 2 * p.du : nullptr, *du_low = p.pairs ? ws + 3 * p.du : nullptr;
     float* partial = reinterpret_cast<float*>(ws + p.partial);
     float* w_partial = reinterpret_cast<float*>(ws + p.w_partial);
     if (gated_few_rows(sh.rows, sh.hidden, sh.ffn))
-        LS_CUDA(launch_gated_few(std::is_same<T, bf16>::value ? LS_BF16 : LS_F16, dg, du, dh, x, wg, wu, sh, s));
+        LS_CUDA(launch_gated_few(std::is_same<T, bf16>::value ? LS_BF16 : LS_F16, dg, du, dh, x, wg, wu, sh, dg_low, du_low, s));
     else
         LS_CUDA((launch_tiles<T, kGrad>(dg, du, dh, x, wg, wu, sh, s)));
     GatedArgs a = {};
@@ -690,6 +716,8 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
     a.width = static_cast<int>(p.width);
     a.h_tiles = static_cast<int>(ceil_div(sh.hidden, p.width));
     a.f_blocks = static_cast<int>(ceil_div(sh.ffn, kBlockK));
+    a.pairs = p.pairs;
+    a.x_blocks = (p.pairs ? 4 : 2) * a.f_blocks;
     a.slices = static_cast<int>(p.slices);
     a.slice_blocks = static_cast<int>(p.slice_blocks);
     a.x_units = dx ? static_cast<int>(ceil_div(sh.rows, kTileM)) * a.h_tiles : 0;
@@ -704,9 +732,16 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
     LS_CUDA(make_map<T>(&m.a2, du, sh.ffn, sh.rows, sh.ffn, a.row_box));
     LS_CUDA(make_map<T>(&m.b, wg, sh.hidden, sh.ffn, sh.hidden, 64));
     LS_CUDA(make_map<T>(&m.b2, wu, sh.hidden, sh.ffn, sh.hidden, 64));
-    LS_CUDA(make_map<T>(&m.wa, dg, sh.ffn, sh.rows, sh.ffn, 64));
-    LS_CUDA(make_map<T>(&m.wa2, du, sh.ffn, sh.rows, sh.ffn, 64));
-    LS_CUDA(make_map<T>(&m.wb, x, sh.hidden, sh.rows, sh.hidden, 64));
+    const int w_rows = p.pairs ? kPairRows : kBlockK;
+    LS_CUDA(make_map<T>(&m.wa, dg, sh.ffn, sh.rows, sh.ffn, w_rows));
+    LS_CUDA(make_map<T>(&m.wa2, du, sh.ffn, sh.rows, sh.ffn, w_rows));
+    LS_CUDA(make_map<T>(&m.wb, x, sh.hidden, sh.rows, sh.hidden, w_rows));
+    if (p.pairs) {
+        LS_CUDA(make_map<T>(&m.a_low, dg_low, sh.ffn, sh.rows, sh.ffn, a.row_box));
+        LS_CUDA(make_map<T>(&m.a2_low, du_low, sh.ffn, sh.rows, sh.ffn, a.row_box));
+        LS_CUDA(make_map<T>(&m.wa_low, dg_low, sh.ffn, sh.rows, sh.ffn, w_rows));
+        LS_CUDA(make_map<T>(&m.wa2_low, du_low, sh.ffn, sh.rows, sh.ffn, w_rows));
+    }
     if (dx && a.x_partial)
         LS_CUDA(make_map<float>(&m.out, partial, sh.hidden, sh.rows, sh.hidden, 32, p.slices));
     else if (dx)
@@ -767,7 +802,7 @@ size_t gated_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn) { return
 
 cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg, const void* wu,
                              const GatedShape& sh, cudaStream_t s) {
-    if (gated_few_rows(sh.rows, sh.hidden, sh.ffn)) return launch_gated_few(dt, h, nullptr, nullptr, x, wg, wu, sh, s);
+    if (gated_few_rows(sh.rows, sh.hidden, sh.ffn)) return launch_gated_few(dt, h, nullptr, nullptr, x, wg, wu, sh, nullptr, nullptr, s);
     if (dt == LS_F16) return launch_tiles<__half, kFwd>(h, nullptr, nullptr, x, wg, wu, sh, s);
     return launch_tiles<bf16, kFwd>(h, nullptr, nullptr, x, wg, wu, sh, s);
 }

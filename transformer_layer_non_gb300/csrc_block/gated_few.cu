@@ -59,7 +59,7 @@ struct FewArgs {
 template <typename T, bool GRAD, int NT, int MT, int U, int CTAS>
 __global__ void __launch_bounds__(kFewThreads, CTAS)
 few_kernel(T* __restrict__ h, T* __restrict__ du, const T* __restrict__ dh, const T* __restrict__ x, const T* __restrict__ wg,
-           const T* __restrict__ wu, const __grid_constant__ FewArgs a) {
+           const T* __restrict__ wu, T* __restrict__ dg_low, T* __restrict__ du_low, const __grid_constant__ FewArgs a) {
     __shared__ float part[kFewWarps][32][4 * NT * MT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, k8 = (lane & 3) * kVec;  // this lane's row of a group of 8, and its place in a step
@@ -124,8 +124,14 @@ few_kernel(T* __restrict__ h, T* __restrict__ du, const T* __restrict__ dh, cons
         const int64_t o = static_cast<int64_t>(t) * a.ffn + f0 + f;
         if constexpr (GRAD) {
             const float d = to_f32(dh[o]);
-            h[o] = from_f32<T>(d * su * v.slope);
-            du[o] = from_f32<T>(d * v.a);
+            const float gg = d * su * v.slope, gu = d * v.a;
+            h[o] = from_f32<T>(gg);
+            du[o] = from_f32<T>(gu);
+            if (dg_low) {  // what the rounding left; nothing of an infinity
+                const float rg = gg - to_f32(from_f32<T>(gg)), ru = gu - to_f32(from_f32<T>(gu));
+                dg_low[o] = from_f32<T>(fabsf(rg) < INFINITY ? rg : 0.f);
+                du_low[o] = from_f32<T>(fabsf(ru) < INFINITY ? ru : 0.f);
+            }
         } else {
             h[o] = from_f32<T>(v.a * su);
         }
@@ -134,7 +140,7 @@ few_kernel(T* __restrict__ h, T* __restrict__ du, const T* __restrict__ dh, cons
 
 template <typename T, bool GRAD>
 cudaError_t launch(void* h, void* du, const void* dh, const void* x, const void* wg, const void* wu, const GatedShape& sh,
-                   cudaStream_t s) {
+                   void* dg_low, void* du_low, cudaStream_t s) {
     const FewArgs a{static_cast<int>(sh.rows), static_cast<int>(sh.hidden), static_cast<int>(sh.ffn),
                     static_cast<int>(sh.act)};
     // With six CTAs of four warps on an SM (fewer for more rows, whose registers hold more of x) 4 steps in flight are
@@ -155,7 +161,7 @@ cudaError_t launch(void* h, void* du, const void* dh, const void* x, const void*
     }
     return launch_pdl(kernel, dim3(static_cast<unsigned>((sh.ffn + columns - 1) / columns)), dim3(kFewThreads), 0, s,
                       static_cast<T*>(h), static_cast<T*>(du), static_cast<const T*>(dh), static_cast<const T*>(x),
-                      static_cast<const T*>(wg), static_cast<const T*>(wu), a);
+                      static_cast<const T*>(wg), static_cast<const T*>(wu), static_cast<T*>(dg_low), static_cast<T*>(du_low), a);
 }
 
 }  // namespace
@@ -165,10 +171,12 @@ bool gated_few_rows(int64_t rows, int64_t hidden, int64_t ffn) {
 }
 
 cudaError_t launch_gated_few(ls_dtype dt, void* h, void* du, const void* dh, const void* x, const void* wg, const void* wu,
-                             const GatedShape& sh, cudaStream_t s) {
+                             const GatedShape& sh, void* dg_low, void* du_low, cudaStream_t s) {
     if (dt == LS_F16)
-        return dh ? launch<__half, true>(h, du, dh, x, wg, wu, sh, s) : launch<__half, false>(h, du, dh, x, wg, wu, sh, s);
-    return dh ? launch<bf16, true>(h, du, dh, x, wg, wu, sh, s) : launch<bf16, false>(h, du, dh, x, wg, wu, sh, s);
+        return dh ? launch<__half, true>(h, du, dh, x, wg, wu, sh, dg_low, du_low, s)
+                  : launch<__half, false>(h, du, dh, x, wg, wu, sh, dg_low, du_low, s);
+    return dh ? launch<bf16, true>(h, du, dh, x, wg, wu, sh, dg_low, du_low, s)
+              : launch<bf16, false>(h, du, dh, x, wg, wu, sh, dg_low, du_low, s);
 }
 
 }  // namespace ls
