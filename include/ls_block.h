@@ -222,7 +222,8 @@ typedef struct {
  * grads: host array; the types may differ.  The sum neither overflows nor
  * underflows as long as the norm is an FP32 number.  A NaN among the gradients
  * gives a NaN for both, an infinite one the norm inf and, for a finite
- * max_norm, the factor 0.  max_norm: at least 0, inf for none; grad_scale:
+ * max_norm, the factor 0 (of which an infinity makes a NaN: a step to be left
+ * out).  max_norm: at least 0, inf for none; grad_scale:
  * finite.  workspace: at least ls_grad_norm_workspace_bytes() bytes. */
 ls_status ls_grad_norm(float* norm, float* factor, const ls_tensor* grads, int64_t count,
                        float max_norm, float grad_scale, void* workspace, size_t workspace_bytes,

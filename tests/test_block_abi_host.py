@@ -113,6 +113,15 @@ def test_norm_refusals(status, bad):
     assert ls_block.last_error()
 
 
+def test_no_tokens_reach_the_launch():
+    """The weights' gradients of no tokens are zeros, written by a kernel: without a GPU its launch fails."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    for empty in (dict(seq=0), dict(batch=0)):
+        assert norm_bwd(**empty) == ls_ops.LS_ERR_CUDA and "ls_qk_norm_rotary_bwd" in ls_block.last_error()
+
+
 def test_norm_workspace():
     bytes_of = ls_block.load().ls_qk_norm_rotary_workspace_bytes
     assert bytes_of(64) > 0 and bytes_of(0) == bytes_of(60) == bytes_of(520) == 0

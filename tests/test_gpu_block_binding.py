@@ -61,9 +61,10 @@ def everything(dtype=torch.float16):
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
 def test_both_ways_write_the_same(dtype, monkeypatch):
     require_gpu()
-    ls_block.load()
+    everything(dtype)  # the first call loads the compiled half
     made = []
     compiled = ls_block._call
+    assert not isinstance(compiled, (type(None), ls_block._Closer))
 
     class Counted:
         def __getattr__(self, name):
@@ -129,7 +130,7 @@ def refused():
 
 def test_both_ways_refuse_the_same(monkeypatch):
     require_gpu()
-    ls_block.load()
+    everything()
     for way in (ls_block._call, ls_block._Closer()):
         monkeypatch.setattr(ls_block, "_call", way)
         for i, (error, call) in enumerate(refused()):

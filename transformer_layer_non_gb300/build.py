@@ -147,8 +147,11 @@ def build_block(force: bool = False, verbose: bool = False, ptxas_verbose: bool 
                              ptxas_verbose)
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile the compiled half of ls_block.py; returns its path."""
+def build_binding(force: bool = False):
+    """Compile the compiled half of ls_block.py; returns its path, or None where
+    Python's headers are missing."""
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return None
     if not force and _newer_than(BINDING_LIB, [BINDING_SRC, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))):
         return BINDING_LIB
     os.makedirs(BUILD, exist_ok=True)

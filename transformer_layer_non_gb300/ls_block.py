@@ -80,6 +80,8 @@ def load(build_if_needed: bool = True):
     """Load libls_block.so (building it first if it is missing or stale)."""
     global _lib
     if _lib is not None:
+        if _call is None and _v._get_device is not None:
+            _load_binding(_lib, build_if_needed)
         return _lib
     path = _build.build_block() if build_if_needed else _build.BLOCK_LIB
     if not os.path.exists(path):
@@ -91,37 +93,37 @@ def load(build_if_needed: bool = True):
         fn.restype = res
         fn.argtypes = args
     _lib = lib
-    _load_binding(lib, build_if_needed)
-    return lib
+    return load(build_if_needed)
 
 
 class _Closer:
-    """In the compiled half's place until it is loaded: every call looks closer."""
+    """In the compiled half's place: every call looks closer."""
 
     def __getattr__(self, name):
         return lambda *args: -1
 
 
-_call = _Closer()
+_call = None  # the compiled half, loaded by the first call on a CUDA device
 
 
 def _load_binding(lib, build_if_needed: bool):
     """Load the compiled half of this binding (csrc_block/binding.cpp), which has
-    each operator's common case."""
+    each operator's common case.  Without Python's headers there is none, and
+    every call takes the longer way."""
     global _call
     import importlib.machinery
     import importlib.util
 
     path = _build.build_binding() if build_if_needed else _build.BINDING_LIB
+    if not path or not os.path.exists(path):
+        _call = _Closer()
+        return
     spec = importlib.util.spec_from_file_location(
         "_ls_block_call", path, loader=importlib.machinery.ExtensionFileLoader("_ls_block_call", path))
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
-    _device_of_calls, stream = _v._device, lambda device: _v._stream_of(None, device)
-    if _v._device() >= 0:  # the functions themselves, where there is a device
-        stream_of = getattr(_v._torch._C, "_cuda_getCurrentRawStream", None)
-        _device_of_calls, stream = _v._get_device, stream_of or stream
-    module.setup(_v._codes, ACTIVATIONS, _device_of_calls, stream, _v._float32, _v._int32, TensorList,
+    stream = getattr(_v._torch._C, "_cuda_getCurrentRawStream", lambda device: _v._stream_of(None, device))
+    module.setup(_v._codes, ACTIVATIONS, _v._get_device, stream, _v._float32, _v._int32, TensorList,
                  {name: ctypes.cast(getattr(lib, name), _P).value for name in EXPORTS})
     _call = module
 
@@ -278,7 +280,7 @@ def ls_rotary_fwd(q_out, k_out, q, k, rotation: Rotation, positions=None, first_
                   stream=None):
     """Rotated queries and keys (k and k_out may be None); an output may be its
     input.  positions: int32 [batch, seq], or None for first_position onwards."""
-    status = _call.rotary_fwd(q_out, k_out, q, k, rotation, positions, first_position, stream)
+    status = (_call or _Closer()).rotary_fwd(q_out, k_out, q, k, rotation, positions, first_position, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -292,7 +294,8 @@ def ls_rotary_bwd(dq, dk, dq_out, dk_out, rotation: Rotation, positions=None, fi
                   stream=None):
     """Gradients of queries and keys from those of the rotated ones (dk and
     dk_out may be None); dq may be dq_out."""
-    status = _call.rotary_bwd(dq, dk, dq_out, dk_out, rotation, positions, first_position, stream)
+    status = (_call or _Closer()).rotary_bwd(dq, dk, dq_out, dk_out, rotation, positions, first_position,
+        stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -306,7 +309,8 @@ def ls_qk_norm_rotary_fwd(q_out, k_out, q, k, q_weight, k_weight, rotation: Rota
                           eps: float = 1e-6, positions=None, first_position: int = 0, stream=None):
     """Queries and keys normalised head by head, weighted ([head_dim] or None
     for ones) and rotated (rotation None: not)."""
-    status = _call.norm_fwd(q_out, k_out, q, k, q_weight, k_weight, rotation, eps, positions, first_position, stream)
+    status = (_call or _Closer()).norm_fwd(q_out, k_out, q, k, q_weight, k_weight, rotation, eps,
+        positions, first_position, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -324,8 +328,8 @@ def ls_qk_norm_rotary_bwd(dq, dk, dq_weight, dk_weight, dq_out, dk_out, q, k, q_
                           first_position: int = 0, workspace=None, stream=None):
     """Gradients of queries, keys and their weights (None: not wanted) from the
     forward's inputs and the gradients of its outputs; dq may be dq_out or q."""
-    status = _call.norm_bwd(dq, dk, dq_weight, dk_weight, dq_out, dk_out, q, k, q_weight, k_weight, rotation, eps,
-                              positions, first_position, workspace, stream)
+    status = (_call or _Closer()).norm_bwd(dq, dk, dq_weight, dk_weight, dq_out, dk_out, q, k, q_weight,
+        k_weight, rotation, eps, positions, first_position, workspace, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -351,7 +355,7 @@ def _activation(name) -> int:
 def ls_gated_linear_fwd(h, x, gate_weight, up_weight, activation: str = "silu", stream=None):
     """h [rows, ffn] = act(x gate_weight^T) * (x up_weight^T) for x [rows,
     hidden] and weights [ffn, hidden]."""
-    status = _call.gated_fwd(h, x, gate_weight, up_weight, activation, stream)
+    status = (_call or _Closer()).gated_fwd(h, x, gate_weight, up_weight, activation, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -370,8 +374,8 @@ def ls_gated_linear_bwd(dx, dgate_weight, dup_weight, dh, x, gate_weight, up_wei
     """Gradients of x and of both weights (dx, or both of the weights', may be
     None).  Weights' gradients in the storage dtype are written; float32 ones
     are added to."""
-    status = _call.gated_bwd(dx, dgate_weight, dup_weight, dh, x, gate_weight, up_weight, activation, workspace,
-                               stream)
+    status = (_call or _Closer()).gated_bwd(dx, dgate_weight, dup_weight, dh, x, gate_weight, up_weight,
+        activation, workspace, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -433,7 +437,7 @@ def ls_grad_norm(norm, factor, grads, max_norm: float = float("inf"), grad_scale
     """The global norm of the gradients (a TensorList, or tensors) times
     grad_scale, and the factor that unscales and clips them; both FP32 of one
     element, either may be None."""
-    status = _call.grad_norm(norm, factor, grads, max_norm, grad_scale, workspace, stream)
+    status = (_call or _Closer()).grad_norm(norm, factor, grads, max_norm, grad_scale, workspace, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -447,7 +451,7 @@ def ls_grad_norm(norm, factor, grads, max_norm: float = float("inf"), grad_scale
 
 def ls_scale_gradients(out, grads, factor, stream=None):
     """out[t] = factor * grads[t] (TensorLists, or tensors; out may be grads)."""
-    status = _call.scale_gradients(out, grads, factor, stream)
+    status = (_call or _Closer()).scale_gradients(out, grads, factor, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
@@ -463,7 +467,8 @@ def ls_adam_update_scaled(param, grad, exp_avg, exp_avg_sq, factor, lr: float, b
                           stream=None):
     """``ls_ops.ls_adam_update`` with the gradient's factor (FP32 of one
     element) in device memory, such as ls_grad_norm leaves it."""
-    status = _call.adam(param, grad, exp_avg, exp_avg_sq, factor, lr, beta1, beta2, eps, weight_decay, step, stream)
+    status = (_call or _Closer()).adam(param, grad, exp_avg, exp_avg_sq, factor, lr, beta1, beta2, eps,
+        weight_decay, step, stream)
     if status >= 0:
         return _made(status)
     dev = _v._device()
