@@ -40,6 +40,11 @@ constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kWarpBoxes = 2;      // a warp's store boxes
 constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;  // one operand of one CTA and stage
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+// Tiles of which a CTA holds no more than 64 rows of B take two K blocks to a stage, in fewer stages: the two waits for
+// each stage, one in the copying and one in the multiplying warp, cost about 0.2 us, more than such a K block's products.
+constexpr int kPairStages = 3;
+constexpr uint32_t kPairStageBytes = 3 * kOperandBytes;
+static_assert(kPairStages * kPairStageBytes <= kStages * kStageBytes, "the stages' memory");
 constexpr uint32_t kStoreBytes = 32 * 128;             // one warp's store box
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * kWarpBoxes * kStoreBytes;
@@ -198,9 +203,13 @@ __device__ __forceinline__ void combine_act(int act, float (&g)[32], float (&u)[
     else combine<MODE, LS_ACT_RELU, T>(g, u, dh);
 }
 
-template <typename T, int MODE>
+// BLOCKS: K blocks of a stage.
+template <typename T, int MODE, int BLOCKS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedArgs a) {
+    // A stage has its blocks of A, and behind them those of B.
+    constexpr uint32_t kCount = BLOCKS == 1 ? kStages : kPairStages, kBytes = BLOCKS == 1 ? kStageBytes : kPairStageBytes;
+    constexpr uint32_t kStepB = kOperandBytes / BLOCKS;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_at;
@@ -250,47 +259,53 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
             const CUtensorMap* b_map = t.half == a.half ? (rank == 0 ? &maps.b : &maps.b2) : rank == 0 ? &maps.wa : &maps.wa2;
             const uint32_t bytes = 2 * b_rows * 128 + a_bytes(t.m0) + a_bytes(t.m0 + 128);  // of both CTAs
             const bool has_a = a_bytes(m) > 0;
-            for (int kb = 0; kb < t.kbs; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                if (!wait_bar(empty + s, ((it / kStages) & 1) ^ 1, &dead)) break;
+            for (int kb0 = 0; kb0 < t.kbs; kb0 += BLOCKS, ++it) {
+                const uint32_t s = it % kCount;
+                if (!wait_bar(empty + s, ((it / kCount) & 1) ^ 1, &dead)) break;
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+                    const int blocks = BLOCKS == 1 ? 1 : min(BLOCKS, t.kbs - kb0);
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, blocks * bytes);
                     const uint32_t bar = map_rank(full + s, 0);
-                    unsigned char* pa = smem + s * kStageBytes;
-                    unsigned char* pb = pa + kOperandBytes;
-                    if constexpr (MODE != kOut) {
-                        const int k = kb * kBlockK;
-                        if (has_a) tma_load_2d(pa, &maps.a, k, m, bar);
-                        tma_load_2d(pb, b_map, k, n, bar);
-                    } else if (!t.weight) {
-                        int b = t.kb0 + kb;  // of dg, du, and the second numbers of both
-                        const bool low = b >= 2 * a.f_blocks;
-                        if (low) b -= 2 * a.f_blocks;
-                        const bool up = b >= a.f_blocks;
-                        const int k = (b - (up ? a.f_blocks : 0)) * kBlockK;
-                        const CUtensorMap* w = up ? &maps.b2 : &maps.b;
-                        const CUtensorMap* d = low ? (up ? &maps.a2_low : &maps.a_low) : up ? &maps.a2 : &maps.a;
-                        if (has_a) tma_load_2d(pa, d, k, m, bar);
-                        tma_load_2d(pb, w, n, k, bar);
-                        if (b_rows > 64) tma_load_2d(pb + kOperandBytes / 2, w, n + 64, k, bar);
-                    } else if (a.pairs) {  // 32 rows of the first numbers, the same of the second ones; x twice
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const CUtensorMap* d = t.weight == 2 ? (h ? &maps.wa2_low : &maps.wa2) : h ? &maps.wa_low : &maps.wa;
-                            unsigned char* const da = pa + h * (kPairRows * 128);
-                            unsigned char* const db = pb + h * (kPairRows * 128);
-                            tma_load_2d(da, d, m, 0, bar);
-                            tma_load_2d(da + kOperandBytes / 2, d, m + 64, 0, bar);
-                            tma_load_2d(db, &maps.wb, n, 0, bar);
-                            if (b_rows > 64) tma_load_2d(db + kOperandBytes / 2, &maps.wb, n + 64, 0, bar);
+                    for (int j = 0; j < BLOCKS; ++j) {
+                        if (j >= blocks) break;
+                        const int kb = kb0 + j;
+                        unsigned char* pa = smem + s * kBytes + j * kOperandBytes;
+                        unsigned char* pb = smem + s * kBytes + BLOCKS * kOperandBytes + j * kStepB;
+                        if constexpr (MODE != kOut) {
+                            const int k = kb * kBlockK;
+                            if (has_a) tma_load_2d(pa, &maps.a, k, m, bar);
+                            tma_load_2d(pb, b_map, k, n, bar);
+                        } else if (!t.weight) {
+                            int b = t.kb0 + kb;  // of dg, du, and the second numbers of both
+                            const bool low = b >= 2 * a.f_blocks;
+                            if (low) b -= 2 * a.f_blocks;
+                            const bool up = b >= a.f_blocks;
+                            const int k = (b - (up ? a.f_blocks : 0)) * kBlockK;
+                            const CUtensorMap* w = up ? &maps.b2 : &maps.b;
+                            const CUtensorMap* d = low ? (up ? &maps.a2_low : &maps.a_low) : up ? &maps.a2 : &maps.a;
+                            if (has_a) tma_load_2d(pa, d, k, m, bar);
+                            tma_load_2d(pb, w, n, k, bar);
+                            if (b_rows > 64) tma_load_2d(pb + kOperandBytes / 2, w, n + 64, k, bar);
+                        } else if (a.pairs) {  // 32 rows of the first numbers, the same of the second ones; x twice
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const CUtensorMap* d = t.weight == 2 ? (h ? &maps.wa2_low : &maps.wa2) : h ? &maps.wa_low : &maps.wa;
+                                unsigned char* const da = pa + h * (kPairRows * 128);
+                                unsigned char* const db = pb + h * (kPairRows * 128);
+                                tma_load_2d(da, d, m, 0, bar);
+                                tma_load_2d(da + kOperandBytes / 2, d, m + 64, 0, bar);
+                                tma_load_2d(db, &maps.wb, n, 0, bar);
+                                if (b_rows > 64) tma_load_2d(db + kOperandBytes / 2, &maps.wb, n + 64, 0, bar);
+                            }
+                        } else {
+                            const int k = (t.kb0 + kb) * kBlockK;
+                            const CUtensorMap* d = t.weight == 2 ? &maps.wa2 : &maps.wa;
+                            tma_load_2d(pa, d, m, k, bar);
+                            tma_load_2d(pa + kOperandBytes / 2, d, m + 64, k, bar);
+                            tma_load_2d(pb, &maps.wb, n, k, bar);
+                            if (b_rows > 64) tma_load_2d(pb + kOperandBytes / 2, &maps.wb, n + 64, k, bar);
                         }
-                    } else {
-                        const int k = (t.kb0 + kb) * kBlockK;
-                        const CUtensorMap* d = t.weight == 2 ? &maps.wa2 : &maps.wa;
-                        tma_load_2d(pa, d, m, k, bar);
-                        tma_load_2d(pa + kOperandBytes / 2, d, m + 64, k, bar);
-                        tma_load_2d(pb, &maps.wb, n, k, bar);
-                        if (b_rows > 64) tma_load_2d(pb + kOperandBytes / 2, &maps.wb, n + 64, k, bar);
                     }
                 }
                 __syncwarp();
@@ -299,8 +314,8 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
         }
         // After a failed wait: the copies in flight land before the CTA ends.
         if (dead && rank == 0)
-            for (uint32_t s = 0; s < kStages && s < it; ++s) {
-                const uint32_t uses = (it - 1 - s) / kStages;  // its last use, counted from 0
+            for (uint32_t s = 0; s < kCount && s < it; ++s) {
+                const uint32_t uses = (it - 1 - s) / kCount;  // its last use, counted from 0
                 for (uint32_t i = 0; i < kWaitPolls; ++i)
                     if (mbar_try_wait(full + s, uses & 1)) break;
             }
@@ -319,19 +334,24 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                 const bool a_mn = MODE == kOut && t.weight, b_mn = MODE == kOut;
                 const uint32_t idesc = instr_desc(kBf16, a_mn, b_mn, kTileM, MODE == kOut ? a.width : 2 * t.half);
                 const uint64_t da = desc_at(a_mn ? mnmajor : kmajor, smem_u32(smem));
-                const uint64_t db = desc_at(b_mn ? mnmajor : kmajor, smem_u32(smem) + kOperandBytes);
+                const uint64_t db = desc_at(b_mn ? mnmajor : kmajor, smem_u32(smem) + BLOCKS * kOperandBytes);
                 // 16 values of K further on, in the descriptors' units of 16 bytes
                 const uint32_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
                 const uint32_t d = tmem + acc * kTileN;
-                for (int kb = 0; kb < t.kbs; ++kb, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!wait_bar(full + s, (it / kStages) & 1, &dead)) break;
+                for (int kb0 = 0; kb0 < t.kbs; kb0 += BLOCKS, ++it) {
+                    const uint32_t s = it % kCount;
+                    if (!wait_bar(full + s, (it / kCount) & 1, &dead)) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t at = s * (kStageBytes >> 4);
+                        const uint32_t at = s * (kBytes >> 4);
 #pragma unroll
-                        for (int k = 0; k < kBlockK / 16; ++k)
-                            tc_mma(d, da + (at + k * step_a), db + (at + k * step_b), idesc, kb + k > 0);
+                        for (int j = 0; j < BLOCKS; ++j) {
+                            if (kb0 + j >= t.kbs) break;
+                            const uint64_t ja = da + (at + j * (kOperandBytes >> 4)), jb = db + (at + j * (kStepB >> 4));
+#pragma unroll
+                            for (int k = 0; k < kBlockK / 16; ++k)
+                                tc_mma(d, ja + k * step_a, jb + k * step_b, idesc, kb0 + j + k > 0);
+                        }
                         tc_commit(empty + s);
                     }
                     __syncwarp();
@@ -652,13 +672,13 @@ struct GatedPlan {
     }
 };
 
-template <typename T, int MODE>
+template <typename T, int MODE, int BLOCKS>
 cudaError_t launch_gated(const GatedMaps& maps, const GatedArgs& a, int64_t units, cudaStream_t s) {
     static int done[kMaxDevices];
-    const cudaError_t e = allow_max_dynamic_smem(gated_kernel<T, MODE>, done);
+    const cudaError_t e = allow_max_dynamic_smem(gated_kernel<T, MODE, BLOCKS>, done);
     if (e != cudaSuccess) return e;
     const int64_t pairs = std::min<int64_t>(units, kPairs);
-    return launch_pdl(gated_kernel<T, MODE>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes, s, maps, a);
+    return launch_pdl(gated_kernel<T, MODE, BLOCKS>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes, s, maps, a);
 }
 
 // The forward's tiles, or with dh those of dg (out) and du (out2).
@@ -692,7 +712,8 @@ cudaError_t launch_tiles(void* out, void* out2, const void* dh, const void* x, c
     }
     LS_CUDA(make_map<T>(&maps.out, out, sh.ffn, sh.rows, sh.ffn, 32));
     if (MODE == kGrad) LS_CUDA(make_map<T>(&maps.out2, out2, sh.ffn, sh.rows, sh.ffn, 32));
-    return launch_gated<T, MODE>(maps, a, 2 * static_cast<int64_t>(tiles) - a.whole_tiles, s);
+    const int64_t units = 2 * static_cast<int64_t>(tiles) - a.whole_tiles;
+    return a.half <= 64 ? launch_gated<T, MODE, 2>(maps, a, units, s) : launch_gated<T, MODE, 1>(maps, a, units, s);
 }
 
 template <typename T>
@@ -773,7 +794,10 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
                      a.w_first ? p.x_len : w_len);
         a.pairs1 = static_cast<int>(d.pairs1);
         a.first_short1 = static_cast<int>((a.w_first ? x_units : a.w_units) - d.short1);
-        LS_CUDA((launch_gated<T, kOut>(m, a, x_units + a.w_units, s)));
+        if (a.width == kTileN)
+            LS_CUDA((launch_gated<T, kOut, 1>(m, a, x_units + a.w_units, s)));
+        else
+            LS_CUDA((launch_gated<T, kOut, 2>(m, a, x_units + a.w_units, s)));
         a.x_units = 0;
         a.w_add = true;
     }
