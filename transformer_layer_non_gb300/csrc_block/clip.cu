@@ -6,9 +6,9 @@
 // bounds them, and for small models the launches.
 //
 // Many tensors go through one launch: a table of addresses and sizes in the
-// kernel's arguments (no copy, and a graph captures it by value), 48 or 1024
-// tensors of it.  Tensors are cut into chunks of 32768 elements, dealt to a fixed
-// number of CTAs in turn, so that what a CTA adds depends on the sizes alone, and
+// kernel's arguments (no copy, and a graph captures it by value), 48,
+// 320 or 1024 tensors of it.  Tensors are cut into chunks of 32768 elements (of small models
+// fewer, down to 8192), dealt to a fixed number of CTAs in turn, so that what a CTA adds depends on the sizes alone, and
 // that the CTAs read neighbouring memory at about the same time (1.0 G BF16
 // gradients, norm and scaling: 897 us, 6.7 TB/s; an equal run of chunks for each
 // CTA 914, chunks of 8192 1035).  Scaling goes through them backwards: what the
@@ -30,10 +30,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kNormCtas = 912;      // six on each of 152 SMs
-constexpr int kChunk = 32768;       // elements
+constexpr int kMostChunk = 15, kLeastChunk = 13;  // log2 of a chunk's elements
 constexpr int kSlots = 8;           // vectors in flight for each thread, of the norm
 constexpr int kScaleSlots = 4;      // and of scaling (8 of them spill)
-constexpr int kFew = 48, kMany = 1024;  // tensors of a launch
+constexpr int kFew = 48, kSome = 320, kMany = 1024;  // tensors of a launch, whose table is copied with it: 29 bytes each
 
 struct Entry {
     void* p;         // the gradient, or the output
@@ -44,7 +44,7 @@ template <int N> struct Table {
     Entry e[N];
     uint32_t first[N];  // number of its first chunk
     uint8_t dtype[N];
-    int count;
+    int count, shift;   // shift: log2 of a chunk's elements
     uint32_t chunks;
 };
 
@@ -62,8 +62,8 @@ __device__ __forceinline__ void for_chunks(const Table<N>& t, bool backwards, F&
             else
                 hi = mid - 1;
         }
-        const int64_t e0 = static_cast<int64_t>(c - t.first[lo]) * kChunk;
-        f(lo, e0, static_cast<int>(min(static_cast<int64_t>(kChunk), t.e[lo].n - e0)));
+        const int64_t e0 = static_cast<int64_t>(c - t.first[lo]) << t.shift;
+        f(lo, e0, static_cast<int>(min(int64_t{1} << t.shift, t.e[lo].n - e0)));
     }
 }
 
@@ -139,7 +139,15 @@ template <typename T> __device__ __forceinline__ double chunk_squares(const T* p
     return total;
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+// The sum over the CTA's threads, in thread 0.  By its first warp: an FP64 addition of a warp takes about 16 cycles of
+// an SM, so that exchanges in all warps would be most of a small tensor's time.
+__device__ __forceinline__ double cta_sum(double v, double (&sm)[kThreads]) {
+    sm[threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0.0;
+    v = sm[threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) v += sm[threadIdx.x + 32 * w];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -149,7 +157,7 @@ __device__ __forceinline__ double warp_sum(double v) {
 template <int N>
 __global__ void __launch_bounds__(kThreads, 4)
 square_sum_kernel(const __grid_constant__ Table<N> t, double* __restrict__ partial, bool add) {
-    __shared__ double sm[kThreads / 32];
+    __shared__ double sm[kThreads];
     pdl_enter();
     double total = 0.0;
     for_chunks(t, false, [&](int k, int64_t e0, int n) {
@@ -160,28 +168,20 @@ square_sum_kernel(const __grid_constant__ Table<N> t, double* __restrict__ parti
         else
             total += chunk_squares(static_cast<const bf16*>(t.e[k].p) + e0, n);
     });
-    total = warp_sum(total);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = total;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) total += sm[w];
-        partial[blockIdx.x] = add ? partial[blockIdx.x] + total : total;
-    }
+    total = cta_sum(total, sm);
+    if (threadIdx.x == 0) partial[blockIdx.x] = add ? partial[blockIdx.x] + total : total;
 }
 
 // norm and factor from the CTAs' sums.
 __global__ void __launch_bounds__(kThreads)
 norm_factor_kernel(float* __restrict__ norm, float* __restrict__ factor, const double* __restrict__ partial, int n,
                    float max_norm, float grad_scale) {
-    __shared__ double sm[kThreads / 32];
+    __shared__ double sm[kThreads];
     pdl_enter();
     double total = 0.0;
     for (int i = threadIdx.x; i < n; i += kThreads) total += partial[i];
-    total = warp_sum(total);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = total;
-    __syncthreads();
+    total = cta_sum(total, sm);
     if (threadIdx.x != 0) return;
-    for (int w = 1; w < kThreads / 32; ++w) total += sm[w];
     const float v = static_cast<float>(sqrt(total) * fabs(static_cast<double>(grad_scale)));
     const float f = max_norm / (v + 1e-6f);
     if (norm) norm[0] = v;
@@ -287,18 +287,28 @@ adam_scaled_kernel(T* __restrict__ param, const T* __restrict__ grad, float* __r
 }
 
 // --- host ----------------------------------------------------------------------
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+// log2 of a chunk's elements: fewer of them where the tensors are too small for two chunks for each SM (norm and scaling
+// of 0.5 M BF16 elements 8.2 -> 6.6 us, of 2.5 M FP32 10.0 -> 9.4; smaller chunks, or more of them, cost more CTAs their
+// look at the table: 5.2 M FP16 in 107 tensors 10.2 us, with 632 chunks of 8192 13.4).
+int chunk_shift(const ls_tensor* t, int64_t count) {
+    int64_t n = 0;
+    for (int64_t k = 0; k < count; ++k) n += t[k].n;
+    int shift = kMostChunk;
+    while (shift > kLeastChunk && n >> shift < 2 * 152) --shift;
+    return shift;
+}
 
 // One launch after the other over tables of at most N tensors and 2^31 chunks: launch(table, number of launches before).
 template <int N, typename F> cudaError_t by_tables(const ls_tensor* out, const ls_tensor* in, int64_t count, F&& launch) {
     Table<N> t;
+    t.shift = chunk_shift(out, count);
     int64_t k = 0;
     for (int done = 0; k < count; ++done) {
         t.count = 0;
         int64_t chunks = 0;
         for (; k < count && t.count < N; ++k) {
             if (out[k].n == 0) continue;
-            const int64_t c = chunks_of(out[k].n);
+            const int64_t c = (out[k].n + (int64_t{1} << t.shift) - 1) >> t.shift;
             if (chunks + c > INT32_MAX && t.count > 0) break;
             t.e[t.count] = Entry{out[k].data, in ? in[k].data : nullptr, out[k].n};
             t.dtype[t.count] = static_cast<uint8_t>(out[k].dtype);
@@ -354,13 +364,15 @@ cudaError_t launch_grad_norm(float* norm, float* factor, const ls_tensor* grads,
                              float max_norm, float grad_scale, void* workspace, cudaStream_t s) {
     double* partial = static_cast<double*>(workspace);
     if (count <= kFew) return grad_norm<kFew>(norm, factor, grads, count, max_norm, grad_scale, partial, s);
+    if (count <= kSome) return grad_norm<kSome>(norm, factor, grads, count, max_norm, grad_scale, partial, s);
     return grad_norm<kMany>(norm, factor, grads, count, max_norm, grad_scale, partial, s);
 }
 
 cudaError_t launch_scale_gradients(const ls_tensor* out, const ls_tensor* in, int64_t count,
                                    const float* factor, cudaStream_t s) {
-    return count <= kFew ? scale_gradients<kFew>(out, in, count, factor, s)
-                         : scale_gradients<kMany>(out, in, count, factor, s);
+    return count <= kFew    ? scale_gradients<kFew>(out, in, count, factor, s)
+           : count <= kSome ? scale_gradients<kSome>(out, in, count, factor, s)
+                            : scale_gradients<kMany>(out, in, count, factor, s);
 }
 
 cudaError_t launch_adam_scaled(ls_dtype dt, void* param, const void* grad, float* m, float* v,

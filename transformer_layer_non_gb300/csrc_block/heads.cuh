@@ -716,18 +716,21 @@ HeadsView view_of(const ls_head_view* v) {
 // side by side: few of them leave each more heads to use its cosines on, many end sooner; heads that are few leave
 // room for more tokens one after the other.  Counted in rounds of the warps that the GPU holds (`slots` of them are
 // this tensor's): a unit takes as long as three rows, a row counting 2, and what its rows and its angles take.
-void plan_units(HeadsArgs& a, int which, int groups, int64_t slots) {
+void plan_units(HeadsArgs& a, int which, int log_groups, uint32_t slots) {
     int64_t best = INT64_MAX;
     for (int split = 0; split <= 5; ++split)
-        for (int shift = 0; (1 << shift) <= groups; ++shift)
+        for (int shift = 0; shift <= log_groups; ++shift)
             for (int sub = 0; sub <= kMostSub; ++sub) {
-                const int64_t step = static_cast<int64_t>(groups >> shift) << split;
-                if (split > 0 && (sub > 0 || step >= 2 * a.heads[which])) continue;
-                const int64_t iters = (a.heads[which] + step - 1) / step;
+                const int steps = log_groups - shift + split;  // log2 of the heads that are side by side
+                if (split > 0 && (sub > 0 || 1 << steps >= 2 * a.heads[which])) continue;
+                const int64_t iters = (a.heads[which] + (1 << steps) - 1) >> steps;
                 const int64_t units = ((static_cast<int64_t>(a.tokens) + (1 << (shift + sub)) - 1) >> (shift + sub)) << split;
                 const int64_t angles = ((static_cast<int64_t>(a.pairs) << (shift + sub)) + 31) / 32;
-                const int64_t t = (units + slots - 1) / slots * (2 * (iters << sub) + angles + 3);
-                if (units > int64_t{1} << 30 || t > best || (t == best && split > a.split_shift[which])) continue;
+                if (units > int64_t{1} << 30) continue;
+                // 32 bits: a division for each candidate is what this costs the host
+                const int64_t rounds = (static_cast<uint32_t>(units) + slots - 1) / slots;
+                const int64_t t = rounds * (2 * (iters << sub) + angles + 3);
+                if (t > best || (t == best && split > a.split_shift[which])) continue;
                 best = t;
                 a.tok_shift[which] = shift;
                 a.sub_shift[which] = sub;
@@ -759,8 +762,8 @@ template <typename T> cudaError_t launch_heads(const HeadsCall& c, cudaStream_t 
     int layout = 16 / sizeof(T);
     if (c.rotation && c.rotation->interleaved) layout = kInterleaved;
     while (layout > 1 && a.pairs % layout) layout /= 2;
-    int lpr = 1;
-    while (2 * kVec * lpr < a.dim) lpr *= 2;
+    int lpr = 1, log_groups = 5;  // log2 of a warp's groups
+    for (; 2 * kVec * lpr < a.dim; --log_groups) lpr *= 2;
     const bool partial = c.norm && c.backward && (c.dweight[0] || c.dweight[1]);
     int64_t rows[2] = {0, 0};
     for (int k = 0; k < 2; ++k) {
@@ -776,7 +779,7 @@ template <typename T> cudaError_t launch_heads(const HeadsCall& c, cudaStream_t 
     int64_t ctas[2] = {0, 0};
     for (int k = 0; k < 2; ++k) {
         if (!rows[k]) continue;
-        plan_units(a, k, 32 / lpr, std::max<int64_t>(1, 152 * 16 * rows[k] / (rows[0] + rows[1])));
+        plan_units(a, k, log_groups, static_cast<uint32_t>(std::max<int64_t>(1, 152 * 16 * rows[k] / (rows[0] + rows[1]))));
         ctas[k] = (a.units[k] + kHeadsWarps - 1) / kHeadsWarps;
     }
     if (partial && ctas[0] + ctas[1] > kPartialCtas) {  // in proportion to the rows, at least one each
