@@ -276,6 +276,18 @@ def test_scaled_update_refusals(status, bad):
     assert adam(n=0) == 0
 
 
+def test_copies_of_a_rotation_have_their_own_frequencies():
+    import copy
+    import pickle
+
+    pytest.importorskip("torch")
+    rot = ls_block.Rotation(16, scale=2.0, device="cpu")
+    for other in (copy.deepcopy(rot), pickle.loads(pickle.dumps(rot)), copy.copy(rot)):
+        assert other._turns == other.turns.data_ptr() and other._device == rot._device
+        assert (other.rotary_dim, other.interleaved, other.scale) == (16, False, 2.0)
+        assert other.turns.equal(rot.turns)
+
+
 # --- the binding -------------------------------------------------------------------------------
 def test_binding_refuses_what_the_library_could_not_see():
     torch = pytest.importorskip("torch")

@@ -11,6 +11,18 @@ from transformer_layer_non_gb300 import ls_block  # noqa: E402
 pytestmark = pytest.mark.gpu
 
 
+def test_copies_of_a_list_have_their_own_tensors():
+    import copy
+
+    require_gpu()
+    grads = ls_block.TensorList([torch.ones(100, device="cuda"), torch.ones(7, device="cuda").half()])
+    other = copy.deepcopy(grads)
+    grads.tensors[0].fill_(5.0)
+    assert clip.norm_of(other)[0] == clip.norm_of([torch.ones(107, device="cuda")])[0]
+    ls_block.ls_scale_gradients(other, other, torch.full((1,), 3.0, device="cuda"))
+    assert (other.tensors[0] == 3).all() and (other.tensors[1] == 3).all() and (grads.tensors[0] == 5).all()
+
+
 @pytest.mark.parametrize("count", [320, 321, 700])
 def test_many_tensors(count):
     clip.test_many_tensors(count)

@@ -208,7 +208,10 @@ class Rotation:
         self.scale = float(default.value if scale is None else scale)
         # fixed-point numbers of 64 bits, whose upper half int64 shows as negative
         values = [t - (t >> 63 << 64) for t in turns[:self.rotary_dim // 2]]
-        self._tensor = torch.tensor(values, dtype=torch.int64, device=device)
+        self.__setstate__({"_tensor": torch.tensor(values, dtype=torch.int64, device=device)})
+
+    def __setstate__(self, state):  # copies have an address of their own
+        self.__dict__.update(state)
         self._turns, self._device = self._tensor.data_ptr(), self._tensor.get_device()
 
     @property
@@ -418,6 +421,9 @@ class TensorList:
                 _v._storage_code(t)
             raise
         self.packed, self.device = struct.pack(f"@{len(fields)}q", *fields), dev
+
+    def __reduce__(self):  # copies have addresses of their own
+        return TensorList, (self.tensors,)
 
     def __len__(self):
         return len(self.tensors)
