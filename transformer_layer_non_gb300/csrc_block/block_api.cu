@@ -434,7 +434,7 @@ size_t ls_gated_linear_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn
     if (rows <= 0 || rows > ls::kMaxGatedRows || hidden <= 0 || hidden > ls::kMaxGatedCols ||
         hidden % 8 != 0 || ffn <= 0 || ffn > ls::kMaxGatedCols || ffn % 8 != 0)
         return 0;
-    return ls::gated_workspace_bytes(rows, hidden, ffn);
+    return ls::gated_plan(rows, hidden, ffn).bytes;
 }
 
 ls_status ls_gated_linear_fwd(ls_dtype dtype, void* h, const void* x, const void* gate_weight,
@@ -487,7 +487,8 @@ ls_status ls_gated_linear_bwd(ls_dtype dtype, void* dx, void* dgate_weight, void
     LS_TRY(check_ptr(x, "x", true));
     LS_TRY(check_ptr(gate_weight, "gate_weight", true));
     LS_TRY(check_ptr(up_weight, "up_weight", true));
-    const size_t need = ls::gated_workspace_bytes(rows, hidden, ffn);
+    const ls::GatedPlan plan = ls::gated_plan(rows, hidden, ffn);
+    const size_t need = plan.bytes;
     LS_TRY(check_workspace(fn, workspace, workspace_bytes, need));
     const size_t xb = static_cast<size_t>(rows * hidden) * 2;
     const Span outs[] = {{"dx", dx, xb},
@@ -501,7 +502,7 @@ ls_status ls_gated_linear_bwd(ls_dtype dtype, void* dx, void* dgate_weight, void
     LS_TRY(check_disjoint(outs, 4, ins, 4));
     const ls::GatedShape sh{rows, hidden, ffn, activation};
     return from_cuda(ls::launch_gated_bwd(dtype, dx, dgate_weight, dup_weight, f32, dh, x, gate_weight,
-                                          up_weight, sh, workspace, as_stream(stream)),
+                                          up_weight, sh, plan, workspace, as_stream(stream)),
                      fn);
 }
 

@@ -52,12 +52,22 @@ struct GatedShape {
     int64_t rows, hidden, ffn;
     ls_activation act;
 };
-size_t gated_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn);
+// How the gradients' sums are cut, and the workspace's layout; made once for a call.
+struct GatedPlan {
+    int64_t width;                     // of dx's and dW's tiles
+    int64_t slices, slice_blocks;      // of dx's K
+    int64_t w_slices, w_slice_blocks;  // of the rows, for dW
+    int64_t x_len;                     // what a unit of dx takes
+    bool w_first;
+    bool pairs;                        // dg and du as two numbers each
+    size_t du, partial, w_partial, bytes;
+};
+GatedPlan gated_plan(int64_t rows, int64_t hidden, int64_t ffn);
 cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg, const void* wu,
                              const GatedShape& sh, cudaStream_t s);
 cudaError_t launch_gated_bwd(ls_dtype dt, void* dx, void* dwg, void* dwu, bool f32_dweight,
                              const void* dh, const void* x, const void* wg, const void* wu,
-                             const GatedShape& sh, void* workspace, cudaStream_t s);
+                             const GatedShape& sh, const GatedPlan& plan, void* workspace, cudaStream_t s);
 // Few rows (gated_few.cu): whether these sizes are its own; h, or with dh dg (in h's place) and du, with the rest of
 // their rounding in dg_low and du_low unless these are NULL.
 bool gated_few_rows(int64_t rows, int64_t hidden, int64_t ffn);

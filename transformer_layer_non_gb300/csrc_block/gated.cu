@@ -626,56 +626,50 @@ struct Deal {
 
 // The tiles' width, slices and workspace layout; they depend on the shapes alone.  Time is counted in 20ths of a K
 // block of a pair's tile (256 x 256 x 64 products, about 0.3 us); one of 128 columns takes 15 of them.
-struct GatedPlan {
-    int64_t width;                     // of dx's and dW's tiles
-    int64_t slices, slice_blocks;      // of dx's K
-    int64_t w_slices, w_slice_blocks;  // of the rows, for dW
-    int64_t x_len;                     // what a unit of dx takes
-    bool w_first;
-    bool pairs;                        // dg and du as two numbers each
-    size_t du, partial, w_partial, bytes;
-    static int64_t length(int64_t width, int64_t blocks, bool joined) {
-        return blocks * (width == kTileN ? 20 : 15) + (joined ? 2 : 1) * (width == kTileN ? 20 : 14);
-    }
-    GatedPlan(int64_t rows, int64_t hidden, int64_t ffn) {
-        const int64_t m_tiles = ceil_div(rows, kTileM);
-        pairs = rows <= kPairRows && rows * ffn <= kPairElements;
-        const int64_t kb = (pairs ? 4 : 2) * ceil_div(ffn, kBlockK), row_blocks = ceil_div(rows, kBlockK);
-        // joining slices: a launch, and their bytes at about 1.7 MB for a K block's time
-        auto join = [](int64_t n, int64_t elements) { return n > 1 ? n * elements * 4 / 85000 : 0; };
-        int64_t best = INT64_MAX;
-        for (int64_t wide = kTileN; wide >= kTileN / 2; wide /= 2) {
-            const int64_t h_tiles = ceil_div(hidden, wide), w_tiles = 2 * ceil_div(ffn, kTileM) * h_tiles;
-            // Rows are cut where a small model's weights would leave most pairs without a tile of dW.
-            const int64_t most_w = w_tiles < kPairs && rows <= kMostRows ? std::min<int64_t>(row_blocks, 8) : 1;
-            for (int64_t sw = 1; sw <= most_w; ++sw) {
-                const int64_t w_part = ceil_div(row_blocks, sw), wl = length(wide, w_part, sw > 1);
-                if (ceil_div(row_blocks, w_part) != sw) continue;
-                for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
-                    const int64_t len = ceil_div(kb, s);
-                    if (ceil_div(kb, len) != s || len * kBlockK > kMostColumns) continue;
-                    const int64_t x_units = s * m_tiles * h_tiles, xl = length(wide, len, s > 1), w_units = sw * w_tiles;
-                    const int64_t out = wl > xl ? Deal(w_units, wl, x_units, xl).most : Deal(x_units, xl, w_units, wl).most;
-                    const int64_t t = out + (s > 1 || sw > 1 ? 240 : 0) + join(s, rows * hidden) + join(sw, 2 * ffn * hidden);
-                    if (t >= best) continue;
-                    best = t;
-                    width = wide;
-                    slices = s;
-                    slice_blocks = len;
-                    w_slices = sw;
-                    w_slice_blocks = w_part;
-                    x_len = xl;
-                    w_first = wl > xl;
-                }
+int64_t unit_length(int64_t width, int64_t blocks, bool joined) {
+    return blocks * (width == kTileN ? 20 : 15) + (joined ? 2 : 1) * (width == kTileN ? 20 : 14);
+}
+
+GatedPlan make_plan(int64_t rows, int64_t hidden, int64_t ffn) {
+    GatedPlan p = {};
+    const int64_t m_tiles = ceil_div(rows, kTileM);
+    p.pairs = rows <= kPairRows && rows * ffn <= kPairElements;
+    const int64_t kb = (p.pairs ? 4 : 2) * ceil_div(ffn, kBlockK), row_blocks = ceil_div(rows, kBlockK);
+    // joining slices: a launch, and their bytes at about 1.7 MB for a K block's time
+    auto join = [](int64_t n, int64_t elements) { return n > 1 ? n * elements * 4 / 85000 : 0; };
+    int64_t best = INT64_MAX;
+    for (int64_t wide = kTileN; wide >= kTileN / 2; wide /= 2) {
+        const int64_t h_tiles = ceil_div(hidden, wide), w_tiles = 2 * ceil_div(ffn, kTileM) * h_tiles;
+        // Rows are cut where a small model's weights would leave most pairs without a tile of dW.
+        const int64_t most_w = w_tiles < kPairs && rows <= kMostRows ? std::min<int64_t>(row_blocks, 8) : 1;
+        for (int64_t sw = 1; sw <= most_w; ++sw) {
+            const int64_t w_part = ceil_div(row_blocks, sw), wl = unit_length(wide, w_part, sw > 1);
+            if (ceil_div(row_blocks, w_part) != sw) continue;
+            for (int64_t s = 1; s <= std::min(kb, kMaxSlices); ++s) {
+                const int64_t len = ceil_div(kb, s);
+                if (ceil_div(kb, len) != s || len * kBlockK > kMostColumns) continue;
+                const int64_t x_units = s * m_tiles * h_tiles, xl = unit_length(wide, len, s > 1), w_units = sw * w_tiles;
+                const int64_t out = wl > xl ? Deal(w_units, wl, x_units, xl).most : Deal(x_units, xl, w_units, wl).most;
+                const int64_t t = out + (s > 1 || sw > 1 ? 240 : 0) + join(s, rows * hidden) + join(sw, 2 * ffn * hidden);
+                if (t >= best) continue;
+                best = t;
+                p.width = wide;
+                p.slices = s;
+                p.slice_blocks = len;
+                p.w_slices = sw;
+                p.w_slice_blocks = w_part;
+                p.x_len = xl;
+                p.w_first = wl > xl;
             }
         }
-        du = round256(static_cast<size_t>(rows * ffn) * 2);
-        partial = (pairs ? 4 : 2) * du;
-        w_partial = partial + (slices > 1 ? round256(static_cast<size_t>(slices * rows * hidden) * 4) : 0);
-        const bool scratch = w_slices > 1 || rows > kMostRows;
-        bytes = w_partial + (scratch ? round256(static_cast<size_t>(2 * w_slices * ffn * hidden) * 4) : 0);
     }
-};
+    p.du = round256(static_cast<size_t>(rows * ffn) * 2);
+    p.partial = (p.pairs ? 4 : 2) * p.du;
+    p.w_partial = p.partial + (p.slices > 1 ? round256(static_cast<size_t>(p.slices * rows * hidden) * 4) : 0);
+    const bool scratch = p.w_slices > 1 || rows > kMostRows;
+    p.bytes = p.w_partial + (scratch ? round256(static_cast<size_t>(2 * p.w_slices * ffn * hidden) * 4) : 0);
+    return p;
+}
 
 template <typename T, int MODE, int BLOCKS>
 cudaError_t launch_gated(const GatedMaps& maps, const GatedArgs& a, int64_t units, cudaStream_t s) {
@@ -723,8 +717,7 @@ cudaError_t launch_tiles(void* out, void* out2, const void* dh, const void* x, c
 
 template <typename T>
 cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const void* x, const void* wg, const void* wu,
-                const GatedShape& sh, void* workspace, cudaStream_t s) {
-    const GatedPlan p(sh.rows, sh.hidden, sh.ffn);
+                const GatedShape& sh, const GatedPlan& p, void* workspace, cudaStream_t s) {
     char* ws = static_cast<char*>(workspace);
     void *dg = ws, *du = ws + p.du;
     void *dg_low = p.pairs ? ws + 2 * p.du : nullptr, *du_low = p.pairs ? ws + 3 * p.du : nullptr;
@@ -794,7 +787,7 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
         a.w_k_blocks = static_cast<int>(std::min(most, row_blocks - kb));
         const int64_t x_units = static_cast<int64_t>(a.slices) * a.x_units;
         if (!a.w_partial) a.w_slice_blocks = a.w_k_blocks;
-        const int64_t w_len = GatedPlan::length(p.width, a.w_slice_blocks, p.w_slices > 1);
+        const int64_t w_len = unit_length(p.width, a.w_slice_blocks, p.w_slices > 1);
         const Deal d(a.w_first ? a.w_units : x_units, a.w_first ? w_len : p.x_len, a.w_first ? x_units : a.w_units,
                      a.w_first ? p.x_len : w_len);
         a.pairs1 = static_cast<int>(d.pairs1);
@@ -827,7 +820,7 @@ cudaError_t bwd(void* dx, void* dwg, void* dwu, bool f32, const void* dh, const 
 
 }  // namespace
 
-size_t gated_workspace_bytes(int64_t rows, int64_t hidden, int64_t ffn) { return GatedPlan(rows, hidden, ffn).bytes; }
+GatedPlan gated_plan(int64_t rows, int64_t hidden, int64_t ffn) { return make_plan(rows, hidden, ffn); }
 
 cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg, const void* wu,
                              const GatedShape& sh, cudaStream_t s) {
@@ -838,9 +831,9 @@ cudaError_t launch_gated_fwd(ls_dtype dt, void* h, const void* x, const void* wg
 
 cudaError_t launch_gated_bwd(ls_dtype dt, void* dx, void* dwg, void* dwu, bool f32_dweight,
                              const void* dh, const void* x, const void* wg, const void* wu,
-                             const GatedShape& sh, void* workspace, cudaStream_t s) {
-    if (dt == LS_F16) return bwd<__half>(dx, dwg, dwu, f32_dweight, dh, x, wg, wu, sh, workspace, s);
-    return bwd<bf16>(dx, dwg, dwu, f32_dweight, dh, x, wg, wu, sh, workspace, s);
+                             const GatedShape& sh, const GatedPlan& p, void* workspace, cudaStream_t s) {
+    if (dt == LS_F16) return bwd<__half>(dx, dwg, dwu, f32_dweight, dh, x, wg, wu, sh, p, workspace, s);
+    return bwd<bf16>(dx, dwg, dwu, f32_dweight, dh, x, wg, wu, sh, p, workspace, s);
 }
 
 cudaError_t launch_block_wait_selftest(uint32_t polls, cudaStream_t s) {
