@@ -175,8 +175,10 @@ typedef enum {
  * kernel.  x: [rows, hidden], gate_weight and up_weight: [ffn, hidden], h:
  * [rows, ffn], row-major and contiguous, LS_F16 or LS_BF16:
  *   h[i,f] = act(sum_c x[i,c] gate_weight[f,c]) * sum_c x[i,c] up_weight[f,c]
- * Both sums stay in FP32; h is rounded once.  hidden and ffn are multiples of
- * 8, at most 65536; rows at most 2^24. */
+ * Both sums stay in FP32; h is rounded once.  They run in the tensor cores'
+ * accumulators, which drop low bits, over at most 32768 columns (2e-4 of a sum
+ * of terms of one sign), and in FP32 from there on.  hidden and ffn are
+ * multiples of 8, at most 65536; rows at most 2^24. */
 ls_status ls_gated_linear_fwd(ls_dtype dtype, void* h, const void* x, const void* gate_weight,
                               const void* up_weight, int64_t rows, int64_t hidden, int64_t ffn,
                               ls_activation activation, void* stream);
@@ -190,9 +192,9 @@ ls_status ls_gated_linear_fwd(ls_dtype dtype, void* h, const void* x, const void
  * dup_weight: [ffn, hidden], both or neither NULL; with dweight_dtype == dtype
  * they are written; with dweight_dtype == LS_F32 the gradients are ADDED to
  * them.  rows == 0 writes zeros to weight gradients in the storage dtype.  The
- * sums run in the tensor cores' accumulators, which drop low bits, over at
- * most 16384 rows or 32768 columns (9e-5 and 2e-4 of a sum of terms of one
- * sign), and in FP32 from there on.  workspace: at least
+ * sums run in the tensor cores' accumulators as the forward's do, over at most
+ * 16384 rows or 32768 columns (9e-5 and 2e-4 of a sum of terms of one sign),
+ * and in FP32 from there on.  workspace: at least
  * ls_gated_linear_workspace_bytes bytes. */
 ls_status ls_gated_linear_bwd(ls_dtype dtype, void* dx, void* dgate_weight, void* dup_weight,
                               ls_dtype dweight_dtype, const void* dh, const void* x,

@@ -73,6 +73,7 @@ struct GatedArgs {
     int whole_tiles;       // the tiles behind these are halved, a unit each
     int row_box;           // rows of the copies with rows as M: 128, or all where there are fewer
     int k_blocks;
+    int part_blocks;       // of two accumulators for a tile: the K blocks that the first one takes
     const void* dh;        // kGrad
     void *out, *out2;      // tiles of fewer than 128 columns: h; dg and du
     // kOut
@@ -208,8 +209,18 @@ __device__ __forceinline__ void combine_act(int act, float (&g)[32], float (&u)[
     else combine<MODE, LS_ACT_RELU, T>(g, u, dh);
 }
 
-// BLOCKS: K blocks of a stage.
-template <typename T, int MODE, int BLOCKS>
+// z += 32 more columns of accumulators.
+__device__ __forceinline__ void add_columns(float (&z)[32], uint32_t cols) {
+    float more[32];
+    tmem_ld32(more, cols);
+    tmem_ld_wait(more);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z[i] += more[i];
+}
+
+// BLOCKS: K blocks of a stage.  PARTS: accumulators of a tile, 2 where one would add up too much (a parameter, since what
+// it adds to the multiplying warp's loop cost chains of K blocks 6 %).
+template <typename T, int MODE, int BLOCKS, int PARTS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedArgs a) {
     // A stage has its blocks of A, and behind them those of B.
@@ -330,8 +341,10 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
             constexpr bool kBf16 = std::is_same<T, bf16>::value;
             const uint64_t kmajor = desc_base(16), mnmajor = desc_base(kOperandBytes / 2);
             uint32_t it = 0, tile = 0;
-            for (PairUnits<MODE> p(pair, pairs, a); p.there(); p.advance(), ++tile) {
+            int done = 0;  // K blocks of the tile that are in its first accumulator
+            for (PairUnits<MODE> p(pair, pairs, a); p.there(); ++tile) {
                 const Unit t = unit_of<MODE>(p.u, a);
+                const int kbs = PARTS == 1 ? t.kbs : done > 0 ? t.kbs - done : a.part_blocks;
                 const uint32_t acc = tile & 1;
                 if (!wait_bar(acc_empty + acc, ((tile >> 1) & 1) ^ 1, &dead)) break;
                 tc_fence_after();
@@ -343,7 +356,7 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                 // 16 values of K further on, in the descriptors' units of 16 bytes
                 const uint32_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
                 const uint32_t d = tmem + acc * kTileN;
-                for (int kb0 = 0; kb0 < t.kbs; kb0 += BLOCKS, ++it) {
+                for (int kb0 = 0; kb0 < kbs; kb0 += BLOCKS, ++it) {
                     const uint32_t s = it % kCount;
                     if (!wait_bar(full + s, (it / kCount) & 1, &dead)) break;
                     tc_fence_after();
@@ -351,7 +364,7 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                         const uint32_t at = s * (kBytes >> 4);
 #pragma unroll
                         for (int j = 0; j < BLOCKS; ++j) {
-                            if (kb0 + j >= t.kbs) break;
+                            if (kb0 + j >= kbs) break;
                             const uint64_t ja = da + (at + j * (kOperandBytes >> 4)), jb = db + (at + j * (kStepB >> 4));
 #pragma unroll
                             for (int k = 0; k < kBlockK / 16; ++k)
@@ -364,6 +377,8 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                 if (dead) break;
                 if (elect_one()) tc_commit(acc_full + acc);
                 __syncwarp();
+                done = PARTS == 1 || done > 0 ? 0 : kbs;
+                if (done == 0) p.advance();
             }
             if (dead) {  // the products in flight end before their operands' memory is given back
                 if (elect_one()) tc_commit(&drained);
@@ -379,7 +394,7 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
         unsigned char* const boxes = smem + kStages * kStageBytes + (warp - 2) * kWarpBoxes * kStoreBytes;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         uint32_t tile = 0, opened = 0;
-        for (PairUnits<MODE> p(pair, pairs, a); p.there(); p.advance(), ++tile) {
+        for (PairUnits<MODE> p(pair, pairs, a); p.there(); p.advance(), tile += PARTS) {
             const Unit t = unit_of<MODE>(p.u, a);
             const uint32_t acc = tile & 1;
             const int row0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
@@ -388,6 +403,7 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty + acc, 0));
+                if (PARTS == 2 && lane == 0) mbar_arrive_cluster(map_rank(acc_empty + 1, 0));
             };
             if constexpr (MODE != kOut) {
                 const int chunks = t.half / 32, per = (chunks + 1) / 2;
@@ -418,6 +434,7 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                     }
                 }
                 if (!wait_bar(acc_full + acc, (tile >> 1) & 1, &dead)) break;
+                if (PARTS == 2 && !wait_bar(acc_full + 1, (tile >> 1) & 1, &dead)) break;  // of two, acc is 0
                 tc_fence_after();
                 const uint32_t cols = lanes + acc * kTileN;
                 const bool boxed = t.half == kMostHalf;
@@ -436,6 +453,10 @@ gated_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
                     tmem_ld32(zu, cols + t.half + (c0 + c) * 32);
                     tmem_ld_wait(zg);
                     tmem_ld_wait(zu);
+                    if constexpr (PARTS == 2) {
+                        add_columns(zg, cols + kTileN + (c0 + c) * 32);
+                        add_columns(zu, cols + kTileN + t.half + (c0 + c) * 32);
+                    }
                     if (c + 1 == cs) release();
                     combine_act<MODE, T>(a.act, zg, zu, dh[c]);
                     if (boxed) {
@@ -580,9 +601,11 @@ template <typename T> __global__ void __launch_bounds__(256) join_kernel(const _
 // --- host ----------------------------------------------------------------------
 constexpr int64_t kMaxSlices = 16;
 // Tensor cores drop low bits as they accumulate: a sum of terms of one sign loses about 5.6e-9 of itself for
-// each of them.  No accumulator adds up more than these; what it has then is added in FP32.
+// each of them.  No accumulator adds up more than these (of kFwd and kGrad kMostColumns of hidden); what it has then is
+// added in FP32.
 constexpr int64_t kMostRows = 16384;
 constexpr int64_t kMostColumns = 32768;
+static_assert(kMaxGatedCols <= 2 * kMostColumns, "a tile of kFwd and kGrad has two accumulators");
 
 // Columns of h in a tile: fewer than 128 for one or two tiles of rows where the busiest pair has less to do that
 // way.  A K block's time goes with the columns down to 64 of each projection, and a tile costs about one K block more.
@@ -671,13 +694,13 @@ GatedPlan make_plan(int64_t rows, int64_t hidden, int64_t ffn) {
     return p;
 }
 
-template <typename T, int MODE, int BLOCKS>
+template <typename T, int MODE, int BLOCKS, int PARTS = 1>
 cudaError_t launch_gated(const GatedMaps& maps, const GatedArgs& a, int64_t units, cudaStream_t s) {
     static int done[kMaxDevices];
-    const cudaError_t e = allow_max_dynamic_smem(gated_kernel<T, MODE, BLOCKS>, done);
+    const cudaError_t e = allow_max_dynamic_smem(gated_kernel<T, MODE, BLOCKS, PARTS>, done);
     if (e != cudaSuccess) return e;
     const int64_t pairs = std::min<int64_t>(units, kPairs);
-    return launch_pdl(gated_kernel<T, MODE, BLOCKS>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes, s, maps, a);
+    return launch_pdl(gated_kernel<T, MODE, BLOCKS, PARTS>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes, s, maps, a);
 }
 
 // The forward's tiles, or with dh those of dg (out) and du (out2).
@@ -712,6 +735,10 @@ cudaError_t launch_tiles(void* out, void* out2, const void* dh, const void* x, c
     LS_CUDA(make_map<T>(&maps.out, out, sh.ffn, sh.rows, sh.ffn, 32));
     if (MODE == kGrad) LS_CUDA(make_map<T>(&maps.out2, out2, sh.ffn, sh.rows, sh.ffn, 32));
     const int64_t units = 2 * static_cast<int64_t>(tiles) - a.whole_tiles;
+    if (sh.hidden > kMostColumns) {  // half of the sums in each accumulator, which the epilogue adds in FP32
+        a.part_blocks = static_cast<int>(2 * ceil_div(a.k_blocks, 4));  // even, as a stage may have two
+        return a.half <= 64 ? launch_gated<T, MODE, 2, 2>(maps, a, units, s) : launch_gated<T, MODE, 1, 2>(maps, a, units, s);
+    }
     return a.half <= 64 ? launch_gated<T, MODE, 2>(maps, a, units, s) : launch_gated<T, MODE, 1>(maps, a, units, s);
 }
 
