@@ -135,7 +135,9 @@ ls_status ls_rotary_bwd(ls_dtype dtype, const ls_head_view* dq, const ls_head_vi
  * dtype, shared by the heads, 16-byte aligned; NULL: ones).  rotation may be
  * NULL (no rotation); k with its output and weight may be NULL.  The mean of
  * squares is an FP32 number: BF16 and FP32 values up to 2^60 are within its
- * range.  An output may be its own input (the same view). */
+ * range, and squares below 2^-126 vanish, so that a row whose values are all
+ * below 2^-60 needs an eps above 2^-120.  An output may be its own input (the
+ * same view). */
 ls_status ls_qk_norm_rotary_fwd(ls_dtype dtype, const ls_head_view* q_out,
                                 const ls_head_view* k_out, const ls_head_view* q,
                                 const ls_head_view* k, const void* q_weight, const void* k_weight,

@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsCtas) heads_kernel(const 
                 float2 q = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < kHalfVec; ++j) q = fma2(p.x[j], p.x[j], fma2(p.y[j], p.y[j], q));
-                const float r = rsqrtf(group_sum<LPR>(q.x + q.y) * a.inv_dim + a.eps);
+                // a lane's part of the mean, and not of the sum, which leaves FP32 before the mean does
+                const float r = rsqrtf(group_sum<LPR>((q.x + q.y) * a.inv_dim) + a.eps);
                 const float2 rr = make_float2(r, r);
                 if constexpr (MODE == kNormFwd) {
 #pragma unroll
