@@ -50,7 +50,12 @@ class LinkedParameters:
         self.exp_avg_sq = torch.zeros(n, dtype=torch.float32, device=device)
         self.step = 0
         self.grad_norm = None  # of the last step with max_norm: FP32 [1] on the device
-        self._factor = self._norm_ws = self._grad_list = None
+        # Clipping's buffers are made here: what a step on another stream allocated would belong to the current one,
+        # whose earlier work may still use it.
+        self._norm = self._factor = self._norm_ws = self._grad_list = None
+        if device.type == "cuda":
+            self._norm, self._factor = (self.exp_avg.new_empty(1) for _ in range(2))
+            self._norm_ws = ls_block.new_workspace(ls_block.grad_norm_workspace_bytes(), device)
         with torch.no_grad():
             for p, off in zip(self.params, self.offsets):
                 k = p.numel()
@@ -76,14 +81,11 @@ class LinkedParameters:
                                   beta1, beta2, eps, weight_decay, self.step, grad_scale,
                                   stream=stream)
             return
-        if self.grad_norm is None:
-            self.grad_norm, self._factor = (self.exp_avg.new_empty(1) for _ in range(2))
-            self._norm_ws = ls_block.new_workspace(ls_block.grad_norm_workspace_bytes(),
-                                                   self.grad_ws.device)
         if self._grad_list is None or self._grad_list.tensors[0] is not self.grad_ws:
             self._grad_list = ls_block.TensorList([self.grad_ws])
-        ls_block.ls_grad_norm(self.grad_norm, self._factor, self._grad_list, max_norm, grad_scale,
+        ls_block.ls_grad_norm(self._norm, self._factor, self._grad_list, max_norm, grad_scale,
                               workspace=self._norm_ws, stream=stream)
+        self.grad_norm = self._norm
         ls_block.ls_adam_update_scaled(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq,
                                        self._factor, lr, beta1, beta2, eps, weight_decay, self.step,
                                        stream=stream)
