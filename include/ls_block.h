@@ -228,7 +228,7 @@ typedef struct {
  * underflows as long as the norm is an FP32 number.  A NaN among the gradients
  * gives a NaN for both, an infinite one the norm inf and, for a finite
  * max_norm, the factor 0 (of which an infinity makes a NaN: a step to be left
- * out).  max_norm: at least 0, inf for none; grad_scale:
+ * out, as ls_adam_update_clipped does).  max_norm: at least 0, inf for none; grad_scale:
  * finite.  workspace: at least ls_grad_norm_workspace_bytes() bytes. */
 ls_status ls_grad_norm(float* norm, float* factor, const ls_tensor* grads, int64_t count,
                        float max_norm, float grad_scale, void* workspace, size_t workspace_bytes,
@@ -251,6 +251,15 @@ ls_status ls_adam_update_scaled(ls_dtype dtype, void* param, const void* grad, f
                                 float* exp_avg_sq, int64_t n, float lr, float beta1, float beta2,
                                 float eps, float weight_decay, int64_t step, const float* factor,
                                 void* stream);
+
+/* The same for a step that may have overflowed, as one of a scaled loss may:
+ * where norm[0] (FP32 on the device, such as ls_grad_norm leaves it) is
+ * infinite or a NaN, nothing is written.  What takes a factor without its norm
+ * has no such guard: infinite or NaN gradients reach its outputs. */
+ls_status ls_adam_update_clipped(ls_dtype dtype, void* param, const void* grad, float* exp_avg,
+                                 float* exp_avg_sq, int64_t n, float lr, float beta1, float beta2,
+                                 float eps, float weight_decay, int64_t step, const float* norm,
+                                 const float* factor, void* stream);
 
 #ifdef __cplusplus
 }

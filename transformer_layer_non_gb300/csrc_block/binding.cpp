@@ -25,6 +25,7 @@ decltype(&ls_gated_linear_bwd) f_gated_bwd;
 decltype(&ls_grad_norm) f_grad_norm;
 decltype(&ls_scale_gradients) f_scale;
 decltype(&ls_adam_update_scaled) f_adam;
+decltype(&ls_adam_update_clipped) f_adam_clipped;
 
 PyObject *s_shape, *s_stride, *s_dtype, *s_data_ptr, *s_get_device, *s_is_contiguous, *s_nbytes, *s_turns, *s_device,
     *s_rotary_dim, *s_interleaved, *s_scale, *s_packed, *s_list_device;
@@ -355,13 +356,13 @@ PyObject* scale_gradients(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return made([&] { return f_scale(out, in, count, static_cast<const float*>(factor), c.stream); });
 }
 
-// (param, grad, exp_avg, exp_avg_sq, factor, lr, beta1, beta2, eps, weight_decay, step, stream)
-PyObject* adam(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// (param, grad, exp_avg, exp_avg_sq, [norm,] factor, lr, beta1, beta2, eps, weight_decay, step, stream)
+PyObject* update(PyObject* const* a, Py_ssize_t n, bool clipped) {
     Call c;
-    void *p, *g, *m, *v, *factor;
+    void *p, *g, *m, *v, *norm = nullptr, *factor;
     double h[5];
     int64_t size, step;
-    if (n != 12 || !c.open()) return look_closer();
+    if (n != 12 + clipped || !c.open()) return look_closer();
     {
         const Ref shape(PyObject_GetAttr(a[0], s_shape));
         if (!shape.p || !PyTuple_Check(shape.p) || PyTuple_GET_SIZE(shape.p) != 1 ||
@@ -370,17 +371,25 @@ PyObject* adam(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (!c.same_dtype(a[0]) || !c.dense(a[0], &p) || !c.same_dtype(a[1]) || !c.contiguous(a[1], 1, &size, &g) ||
         !c.typed(a[2], g_float32) || !c.contiguous(a[2], 1, &size, &m) || !c.typed(a[3], g_float32) ||
-        !c.contiguous(a[3], 1, &size, &v) || !c.typed(a[4], g_float32) || !c.contiguous(a[4], 1, kOne, &factor) ||
-        !as_i64(a[10], &step) || !c.take_stream(a[11]))
+        !c.contiguous(a[3], 1, &size, &v))
+        return look_closer();
+    a += 4;
+    if (clipped && (!c.typed(*a, g_float32) || !c.contiguous(*a++, 1, kOne, &norm))) return look_closer();
+    if (!c.typed(a[0], g_float32) || !c.contiguous(a[0], 1, kOne, &factor) || !as_i64(a[6], &step) || !c.take_stream(a[7]))
         return look_closer();
     for (int i = 0; i < 5; ++i)
-        if (!as_f64(a[5 + i], h + i)) return look_closer();
+        if (!as_f64(a[1 + i], h + i)) return look_closer();
+    const float lr = static_cast<float>(h[0]), b1 = static_cast<float>(h[1]), b2 = static_cast<float>(h[2]),
+                eps = static_cast<float>(h[3]), decay = static_cast<float>(h[4]);
+    float *fm = static_cast<float*>(m), *fv = static_cast<float*>(v);
+    const float *fn = static_cast<const float*>(norm), *ff = static_cast<const float*>(factor);
     return made([&] {
-        return f_adam(c.code, p, g, static_cast<float*>(m), static_cast<float*>(v), size, static_cast<float>(h[0]),
-                      static_cast<float>(h[1]), static_cast<float>(h[2]), static_cast<float>(h[3]), static_cast<float>(h[4]),
-                      step, static_cast<const float*>(factor), c.stream);
+        return clipped ? f_adam_clipped(c.code, p, g, fm, fv, size, lr, b1, b2, eps, decay, step, fn, ff, c.stream)
+                       : f_adam(c.code, p, g, fm, fv, size, lr, b1, b2, eps, decay, step, ff, c.stream);
     });
 }
+PyObject* adam(PyObject*, PyObject* const* a, Py_ssize_t n) { return update(a, n, false); }
+PyObject* adam_clipped(PyObject*, PyObject* const* a, Py_ssize_t n) { return update(a, n, true); }
 
 template <typename F> bool take_function(PyObject* addresses, const char* name, F* f) {
     void* p = nullptr;
@@ -405,7 +414,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !take_function(a[7], "ls_qk_norm_rotary_bwd", &f_norm_bwd) ||
         !take_function(a[7], "ls_gated_linear_fwd", &f_gated_fwd) ||
         !take_function(a[7], "ls_gated_linear_bwd", &f_gated_bwd) || !take_function(a[7], "ls_grad_norm", &f_grad_norm) ||
-        !take_function(a[7], "ls_scale_gradients", &f_scale) || !take_function(a[7], "ls_adam_update_scaled", &f_adam)) {
+        !take_function(a[7], "ls_scale_gradients", &f_scale) || !take_function(a[7], "ls_adam_update_scaled", &f_adam) ||
+        !take_function(a[7], "ls_adam_update_clipped", &f_adam_clipped)) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "setup: a function's address is missing");
         return nullptr;
     }
@@ -416,7 +426,7 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {LS_METHOD(setup),     LS_METHOD(rotary_fwd), LS_METHOD(rotary_bwd),
                          LS_METHOD(norm_fwd),  LS_METHOD(norm_bwd),   LS_METHOD(gated_fwd),
                          LS_METHOD(gated_bwd), LS_METHOD(grad_norm),  LS_METHOD(scale_gradients),
-                         LS_METHOD(adam),      {nullptr, nullptr, 0, nullptr}};
+                         LS_METHOD(adam),      LS_METHOD(adam_clipped), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ls_block_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

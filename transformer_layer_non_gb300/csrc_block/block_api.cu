@@ -281,6 +281,31 @@ ls_status check_tensors(const char* fn, const char* name, const ls_tensor* t, in
     return LS_OK;
 }
 
+ls_status run_adam(const char* fn, ls_dtype dtype, void* param, const void* grad, float* exp_avg,
+                   float* exp_avg_sq, int64_t n, const ls::AdamScaled& h, void* stream) {
+    LS_TRY(check_storage(fn, dtype, true));
+    LS_TRY(check_size(fn, "n", n, 0, int64_t{1} << 44));
+    LS_TRY(check_size(fn, "step", h.step, 1, INT64_MAX));
+    if (!(h.beta1 >= 0.f && h.beta1 < 1.f && h.beta2 >= 0.f && h.beta2 < 1.f))
+        return fail(LS_ERR_INVALID_ARGUMENT, "%s: betas %g, %g are not in [0, 1)", fn,
+                    static_cast<double>(h.beta1), static_cast<double>(h.beta2));
+    for (const float v : {h.lr, h.eps, h.weight_decay})
+        if (!(v >= 0.f && v < INFINITY))
+            return fail(LS_ERR_INVALID_ARGUMENT, "%s: lr, eps or weight_decay is not a finite number from 0 on", fn);
+    if (n == 0) return ok();
+    LS_TRY(check_ptr(param, "param", true));
+    LS_TRY(check_ptr(grad, "grad", true));
+    LS_TRY(check_ptr(exp_avg, "exp_avg", true));
+    LS_TRY(check_ptr(exp_avg_sq, "exp_avg_sq", true));
+    LS_TRY(check_ptr4(h.factor, "factor", true));
+    const size_t b = static_cast<size_t>(n) * elem_size(dtype), f = static_cast<size_t>(n) * 4;
+    const Span outs[] = {{"param", param, b}, {"exp_avg", exp_avg, f}, {"exp_avg_sq", exp_avg_sq, f}};
+    const Span ins[] = {{"grad", grad, b}, {"factor", h.factor, 4}, {"norm", h.norm, 4}};
+    LS_TRY(check_disjoint(outs, 3, ins, 3));
+    return from_cuda(ls::launch_adam_scaled(dtype, param, grad, exp_avg, exp_avg_sq, n, h, as_stream(stream)),
+                     fn);
+}
+
 size_t bytes_of(const ls_tensor& t) {
     return static_cast<size_t>(t.n) * elem_size(static_cast<ls_dtype>(t.dtype));
 }
@@ -559,29 +584,17 @@ ls_status ls_adam_update_scaled(ls_dtype dtype, void* param, const void* grad, f
                                 float* exp_avg_sq, int64_t n, float lr, float beta1, float beta2,
                                 float eps, float weight_decay, int64_t step, const float* factor,
                                 void* stream) {
-    const char* fn = "ls_adam_update_scaled";
-    LS_TRY(check_storage(fn, dtype, true));
-    LS_TRY(check_size(fn, "n", n, 0, int64_t{1} << 44));
-    LS_TRY(check_size(fn, "step", step, 1, INT64_MAX));
-    if (!(beta1 >= 0.f && beta1 < 1.f && beta2 >= 0.f && beta2 < 1.f))
-        return fail(LS_ERR_INVALID_ARGUMENT, "%s: betas %g, %g are not in [0, 1)", fn,
-                    static_cast<double>(beta1), static_cast<double>(beta2));
-    for (const float v : {lr, eps, weight_decay})
-        if (!(v >= 0.f && v < INFINITY))
-            return fail(LS_ERR_INVALID_ARGUMENT, "%s: lr, eps or weight_decay is not a finite number from 0 on", fn);
-    if (n == 0) return ok();
-    LS_TRY(check_ptr(param, "param", true));
-    LS_TRY(check_ptr(grad, "grad", true));
-    LS_TRY(check_ptr(exp_avg, "exp_avg", true));
-    LS_TRY(check_ptr(exp_avg_sq, "exp_avg_sq", true));
-    LS_TRY(check_ptr4(factor, "factor", true));
-    const size_t b = static_cast<size_t>(n) * elem_size(dtype), f = static_cast<size_t>(n) * 4;
-    const Span outs[] = {{"param", param, b}, {"exp_avg", exp_avg, f}, {"exp_avg_sq", exp_avg_sq, f}};
-    const Span ins[] = {{"grad", grad, b}, {"factor", factor, 4}};
-    LS_TRY(check_disjoint(outs, 3, ins, 2));
-    const ls::AdamScaled h{lr, beta1, beta2, eps, weight_decay, step, factor};
-    return from_cuda(ls::launch_adam_scaled(dtype, param, grad, exp_avg, exp_avg_sq, n, h, as_stream(stream)),
-                     fn);
+    return run_adam("ls_adam_update_scaled", dtype, param, grad, exp_avg, exp_avg_sq, n,
+                    {lr, beta1, beta2, eps, weight_decay, step, factor, nullptr}, stream);
+}
+
+ls_status ls_adam_update_clipped(ls_dtype dtype, void* param, const void* grad, float* exp_avg,
+                                 float* exp_avg_sq, int64_t n, float lr, float beta1, float beta2,
+                                 float eps, float weight_decay, int64_t step, const float* norm,
+                                 const float* factor, void* stream) {
+    LS_TRY(check_ptr4(norm, "norm", n > 0));
+    return run_adam("ls_adam_update_clipped", dtype, param, grad, exp_avg, exp_avg_sq, n,
+                    {lr, beta1, beta2, eps, weight_decay, step, factor, norm}, stream);
 }
 
 }  // extern "C"

@@ -43,6 +43,7 @@ struct AdamScaled {
     float lr, beta1, beta2, eps, weight_decay;
     int64_t step;
     const float* factor;
+    const float* norm;  // nullable
 };
 cudaError_t launch_adam_scaled(ls_dtype dt, void* param, const void* grad, float* m, float* v,
                                int64_t n, const AdamScaled& h, cudaStream_t s);

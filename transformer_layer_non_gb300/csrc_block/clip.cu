@@ -247,6 +247,7 @@ struct AdamArgs {
     float b1, b2, omb1, omb2;
     float step_size, inv_sqrt_bc2, eps, decay;
     const float* factor;
+    const float* norm;  // nullable: where it is not finite, nothing is written
 };
 __device__ __forceinline__ void adam1(float& p, float g, float& m, float& v, const AdamArgs& a) {
     m = a.b1 * m + a.omb1 * g;
@@ -260,6 +261,7 @@ adam_scaled_kernel(T* __restrict__ param, const T* __restrict__ grad, float* __r
                    const __grid_constant__ AdamArgs a) {
     pdl_enter();
     const float factor = *a.factor;
+    if (a.norm && !(fabsf(*a.norm) < INFINITY)) return;
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * kThreads;
     for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x; i < a.nv; i += step) {
         const uint64_t e = i * kVec;
@@ -391,6 +393,7 @@ cudaError_t launch_adam_scaled(ls_dtype dt, void* param, const void* grad, float
     a.eps = h.eps;
     a.decay = static_cast<float>(1.0 - static_cast<double>(h.lr) * h.weight_decay);
     a.factor = h.factor;
+    a.norm = h.norm;
     if (dt == LS_F16) return adam<__half>(param, grad, m, v, a, s);
     if (dt == LS_BF16) return adam<bf16>(param, grad, m, v, a, s);
     return adam<float>(param, grad, m, v, a, s);

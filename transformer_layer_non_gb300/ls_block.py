@@ -34,6 +34,7 @@ EXPORTS = (
     "ls_qk_norm_rotary_fwd", "ls_qk_norm_rotary_bwd", "ls_qk_norm_rotary_workspace_bytes",
     "ls_gated_linear_fwd", "ls_gated_linear_bwd", "ls_gated_linear_workspace_bytes",
     "ls_grad_norm", "ls_grad_norm_workspace_bytes", "ls_scale_gradients", "ls_adam_update_scaled",
+    "ls_adam_update_clipped",
 )
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -69,6 +70,8 @@ _SIGNATURES = {
     "ls_scale_gradients": (_INT, [_S, _S, _I64, _P, _P]),
     "ls_adam_update_scaled": (_INT, [_INT, _P, _P, _P, _P, _I64, _F32, _F32, _F32, _F32, _F32, _I64,
                                      _P, _P]),
+    "ls_adam_update_clipped": (_INT, [_INT, _P, _P, _P, _P, _I64, _F32, _F32, _F32, _F32, _F32, _I64,
+                                      _P, _P, _P]),
 }
 
 
@@ -478,10 +481,31 @@ def ls_adam_update_scaled(param, grad, exp_avg, exp_avg_sq, factor, lr: float, b
     if status >= 0:
         return _made(status)
     dev = _v._device()
-    pp, (n,) = _v._shaped("param", param, 1, None, dev)
-    pg = _v._tensor("grad", grad, (n,), param.dtype, dev)
-    pm = _v._tensor("exp_avg", exp_avg, (n,), _v._float32, dev)
-    pv = _v._tensor("exp_avg_sq", exp_avg_sq, (n,), _v._float32, dev)
+    code, p, n = _update_tensors(param, grad, exp_avg, exp_avg_sq, dev)
     pf = _v._tensor("factor", factor, (1,), _v._float32, dev)
-    _check(load().ls_adam_update_scaled(_v._storage_code(param), pp, pg, pm, pv, n, lr, beta1, beta2, eps,
-                                        weight_decay, step, pf, _v._stream_of(stream, dev)))
+    _check(load().ls_adam_update_scaled(code, *p, n, lr, beta1, beta2, eps, weight_decay, step, pf,
+                                        _v._stream_of(stream, dev)))
+
+
+def _update_tensors(param, grad, exp_avg, exp_avg_sq, dev):
+    pp, (n,) = _v._shaped("param", param, 1, None, dev)
+    return _v._storage_code(param), (pp, _v._tensor("grad", grad, (n,), param.dtype, dev),
+                                     _v._tensor("exp_avg", exp_avg, (n,), _v._float32, dev),
+                                     _v._tensor("exp_avg_sq", exp_avg_sq, (n,), _v._float32, dev)), n
+
+
+def ls_adam_update_clipped(param, grad, exp_avg, exp_avg_sq, norm, factor, lr: float, beta1: float = 0.9,
+                           beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, step: int = 1,
+                           stream=None):
+    """ls_adam_update_scaled, but for a norm (FP32 of one element on the device)
+    that is infinite or a NaN: then nothing is written."""
+    status = (_call or _Closer()).adam_clipped(param, grad, exp_avg, exp_avg_sq, norm, factor, lr, beta1,
+        beta2, eps, weight_decay, step, stream)
+    if status >= 0:
+        return _made(status)
+    dev = _v._device()
+    code, p, n = _update_tensors(param, grad, exp_avg, exp_avg_sq, dev)
+    pn = _v._tensor("norm", norm, (1,), _v._float32, dev)
+    pf = _v._tensor("factor", factor, (1,), _v._float32, dev)
+    _check(load().ls_adam_update_clipped(code, *p, n, lr, beta1, beta2, eps, weight_decay, step, pn, pf,
+                                         _v._stream_of(stream, dev)))

@@ -74,7 +74,10 @@ class LinkedParameters:
         """One fused Adam update of every linked parameter (one launch).  With
         max_norm the gradients are clipped to that global norm first, which
         ``grad_norm`` then holds: two more launches, no copy of the gradients
-        and no synchronisation."""
+        and no synchronisation.  A step whose norm is infinite or a NaN (a
+        scaled loss that overflowed) changes neither parameters nor moments;
+        the host does not see that, so a program that reads such a norm takes
+        one off ``step``, and off the loss scale what it likes."""
         self.step += 1
         if max_norm is None:
             ls_ops.ls_adam_update(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq, lr,
@@ -86,6 +89,6 @@ class LinkedParameters:
         ls_block.ls_grad_norm(self._norm, self._factor, self._grad_list, max_norm, grad_scale,
                               workspace=self._norm_ws, stream=stream)
         self.grad_norm = self._norm
-        ls_block.ls_adam_update_scaled(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq,
-                                       self._factor, lr, beta1, beta2, eps, weight_decay, self.step,
-                                       stream=stream)
+        ls_block.ls_adam_update_clipped(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq,
+                                        self._norm, self._factor, lr, beta1, beta2, eps, weight_decay,
+                                        self.step, stream=stream)
