@@ -78,11 +78,11 @@ class LinkedParameters:
         scaled loss that overflowed) changes neither parameters nor moments;
         the host does not see that, so a program that reads such a norm takes
         one off ``step``, and off the loss scale what it likes."""
-        self.step += 1
+        step = self.step + 1  # counted once the update has been enqueued
         if max_norm is None:
             ls_ops.ls_adam_update(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq, lr,
-                                  beta1, beta2, eps, weight_decay, self.step, grad_scale,
-                                  stream=stream)
+                                  beta1, beta2, eps, weight_decay, step, grad_scale, stream=stream)
+            self.step = step
             return
         if self._grad_list is None or self._grad_list.tensors[0] is not self.grad_ws:
             self._grad_list = ls_block.TensorList([self.grad_ws])
@@ -91,4 +91,5 @@ class LinkedParameters:
         self.grad_norm = self._norm
         ls_block.ls_adam_update_clipped(self.param_ws, self.grad_ws, self.exp_avg, self.exp_avg_sq,
                                         self._norm, self._factor, lr, beta1, beta2, eps, weight_decay,
-                                        self.step, stream=stream)
+                                        step, stream=stream)
+        self.step = step
