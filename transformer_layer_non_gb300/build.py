@@ -31,9 +31,9 @@ VOCAB_CSRC = os.path.join(PKG, "csrc_vocab")
 VOCAB_LIB = os.path.join(BUILD, "libls_vocab.so")
 BLOCK_CSRC = os.path.join(PKG, "csrc_block")
 BLOCK_LIB = os.path.join(BUILD, "libls_block.so")
-# The compiled half of ls_block.py, a Python extension module.
+# The compiled half of ls_block.py, an extension module of the Python that its file names.
 BINDING_SRC = os.path.join(BLOCK_CSRC, "binding.cpp")
-BINDING_LIB = os.path.join(BUILD, "_ls_block_call.so")
+BINDING_LIB = os.path.join(BUILD, "_ls_block_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 # The benchmark's reference streaming kernel (not part of the operator library).
 FLOOR_SRC = os.path.join(PKG, "floor", "stream_floor.cu")
 FLOOR_LIB = os.path.join(BUILD, "libls_floor.so")
