@@ -9,7 +9,7 @@
 // kernel's arguments (no copy, and a graph captures it by value), 48,
 // 320 or 1024 tensors of it.  Tensors are cut into chunks of 32768 elements (of small models
 // fewer, down to 8192), dealt to a fixed number of CTAs in turn, so that what a CTA adds depends on the sizes alone, and
-// that the CTAs read neighbouring memory at about the same time (1.0 G BF16
+// that CTAs that run at the same time read neighbouring memory (1.0 G BF16
 // gradients, norm and scaling: 897 us, 6.7 TB/s; an equal run of chunks for each
 // CTA 914, chunks of 8192 1035).  Scaling goes through them backwards: what the
 // norm read last is still in L2.
@@ -29,7 +29,11 @@ namespace ls {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kNormCtas = 912;      // six on each of 152 SMs
+// CTAs of the norm and of scaling, each of which takes its chunks in turn.  An SM holds three of scaling (72 registers a
+// thread), so these are two even rounds, and four of the norm (55), so there they are one and a half.  With the 608 that
+// run at once the norm alone is faster (1008 M BF16: 291 us for 300, 137 M FP16 44.5 for 46.5) and scaling slower (norm
+// and scaling 1003 for 904, 146 for 136); below 20 M elements nothing changes.
+constexpr int kNormCtas = 912;
 constexpr int kMostChunk = 15, kLeastChunk = 13;  // log2 of a chunk's elements
 constexpr int kSlots = 8;           // vectors in flight for each thread, of the norm
 constexpr int kScaleSlots = 4;      // and of scaling (8 of them spill)
