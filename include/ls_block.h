@@ -191,7 +191,12 @@ ls_status ls_gated_linear_fwd(ls_dtype dtype, void* h, const void* x, const void
  *   dg = dh u act'(g),  du = dh act(g)                    (rounded once to the storage dtype; of up
  *                                to 32 rows and 16384 elements to two numbers of it each)
  *   dx = dg gate_weight + du up_weight,  dgate_weight = dg^T x,  dup_weight = du^T x
- * dx: [rows, hidden] in the storage dtype, written, or NULL.  dgate_weight and
+ * That rounding adds as much error as the gradients' own: sqrt(2) of a rounding
+ * as a whole.  In LS_F16 it also has the type's range: a dg or du beyond 65504
+ * is infinite, and the gradients that it is part of are infinite or NaNs, and
+ * one below 2^-25 is zero, even where the gradients themselves are in range.  A
+ * loss scale has to keep dg and du in range as it has to keep the gradients;
+ * LS_BF16 has FP32's range.  dx: [rows, hidden] in the storage dtype, written, or NULL.  dgate_weight and
  * dup_weight: [ffn, hidden], both or neither NULL; with dweight_dtype == dtype
  * they are written; with dweight_dtype == LS_F32 the gradients are ADDED to
  * them.  rows == 0 writes zeros to weight gradients in the storage dtype.  The

@@ -56,10 +56,11 @@ constexpr uint32_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * 
 constexpr int kGroupM = 16;   // row tiles that share a sweep over the columns
 constexpr int kPairs = 76;    // pairs of SMs; a constant, so that plans depend on the shapes alone
 constexpr int kMostHalf = 128;
-// dg and du are rounded to 16 bits before they are summed up to gradients.  Of many elements that adds as much again
-// to the gradients' own rounding, as a whole (1.4 times the error); of few, single ones show (3 x 376 x 240: 1.5
-// times), so these are kept as two 16-bit numbers each.  Up to kPairRows rows, whose K block of dW has room for the
-// second ones; dx takes twice the K blocks (1 x 344 x 480, step: 10.1 -> 10.7 us).
+// dg and du are rounded to 16 bits before they are summed up to gradients, which adds as much error again as the
+// gradients' own rounding: sqrt(2) times that as a whole, at any size (4096 x 1280 x 5120 BF16: 0.00235 and 0.00166).  How
+// far single tensors are from that depends on how many roundings there are, rows x ffn of each: of few of them some are
+// well above it (3 x 376 x 240: 1.52 times), so these are kept as two 16-bit numbers each.  Up to kPairRows rows, whose
+// K block of dW has room for the second ones; dx takes twice the K blocks (1 x 344 x 480, step: 10.1 -> 10.7 us).
 constexpr int kPairRows = 32;
 constexpr int64_t kPairElements = 16384;
 
